@@ -21,12 +21,14 @@ DEVICE_ERRORS = {0: "ok", 1: "MOE_DEV_BAD_BLOCK", 2: "MOE_DEV_BAD_INDEX", 3: "MO
 
 GATE_UP, DOWN = 0, 1
 IMPL_AUTO, IMPL_TC, IMPL_GEMV, IMPL_TC2, IMPL_TC_BF16 = 0, 2, 3, 4, 5
+KV_BF16, KV_E4M3 = 0, 1
 IMPLS = {"auto": IMPL_AUTO, "tc": IMPL_TC, "gemv": IMPL_GEMV, "tc2": IMPL_TC2, "tc_bf16": IMPL_TC_BF16}
 
 # Exported symbols of include/moe_w4.h (checked by the CPU tests).
 SYMBOLS = ["moe_version", "moe_launch_count", "moe_route_noalloc", "moe_route_x", "moe_router", "moe_rms_norm", "moe_norm_router",
            "moe_down_combine", "moe_down_combine_workspace_size", "moe_expert_ffn_w4", "moe_block_map_capacity", "moe_route_workspace_size", "moe_route",
            "moe_repacked_bytes", "moe_repack_w4", "moe_expanded_bytes", "moe_expand_w4", "moe_expert_gemm_w4", "moe_combine", "moe_decode_workspace_size",
+           "moe_kv_append", "moe_kv_read", "moe_kv_attention", "moe_kv_attention_workspace_size",
            "moe_layer_forward", "moe_layer_forward_host", "moe_get_device_error", "moe_set_wait_limit_ns",
            "moe_trace_words", "moe_trace_reset", "moe_trace_read"]
 
@@ -51,6 +53,20 @@ class Buffers(ctypes.Structure):
                 ("combine_ws", _vp), ("combine_ws_bytes", _sz)]
 
 
+class KVCache(ctypes.Structure):
+    _fields_ = [("k", _vp), ("v", _vp), ("k_scale", _vp), ("v_scale", _vp), ("num_pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("heads", ctypes.c_int32), ("d", ctypes.c_int32),
+                ("format", ctypes.c_int32)]
+
+
+class KVBatch(ctypes.Structure):
+    _fields_ = [("page_table", _vp), ("cu_q", _vp), ("kv_len", _vp), ("B", ctypes.c_int32),
+                ("table_width", ctypes.c_int32), ("T", ctypes.c_int32)]
+
+
+_i64 = ctypes.c_int64
+_kv = [ctypes.POINTER(KVCache), ctypes.POINTER(KVBatch)]
+
 _SIGS = {
     "moe_version": ([], _i),
     "moe_launch_count": ([], ctypes.c_uint64),
@@ -74,6 +90,10 @@ _SIGS = {
     "moe_decode_workspace_size": ([_i, _i], _sz),
     "moe_layer_forward": ([_vp, _vp, _vp] + [_i] * 7 + [ctypes.POINTER(Weights), ctypes.POINTER(Buffers), _vp], _i),
     "moe_layer_forward_host": ([_vp] * 6 + [_i] * 7 + [ctypes.POINTER(Weights), ctypes.POINTER(Buffers), _vp], _i),
+    "moe_kv_append": ([_vp, _i64, _i64, _vp, _i64, _i64] + _kv + [_vp], _i),
+    "moe_kv_read": ([_vp, _vp] + _kv + [_vp], _i),
+    "moe_kv_attention": ([_vp, _i64, _i64, _i, ctypes.c_float] + _kv + [_vp, _vp, _vp, _sz, _vp], _i),
+    "moe_kv_attention_workspace_size": ([_i], _sz),
     "moe_get_device_error": ([ctypes.POINTER(ctypes.c_int32)], _i),
     "moe_set_wait_limit_ns": ([ctypes.c_uint64], None),
     "moe_trace_words": ([], ctypes.c_size_t),
@@ -254,6 +274,28 @@ def moe_layer_forward_host(x_host, logits_host, out_host, x_dev, logits_dev, out
     _call("moe_layer_forward_host", _ptr(x_host), _ptr(logits_host), _ptr(out_host), _ptr(x_dev), _ptr(logits_dev),
           _ptr(out_dev), T, H, F, E, k, block_n, impl, ctypes.byref(weights), ctypes.byref(buffers),
           _stream(stream))
+
+
+def moe_kv_append(k, v, cache: KVCache, batch: KVBatch, stream=None):
+    """Write new tokens' k, v (bf16 [T, heads, d], any token and head strides) into their pages."""
+    ks, vs = k.stride(), v.stride()
+    _call("moe_kv_append", k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], cache, batch, _stream(stream))
+
+
+def moe_kv_read(k, v, cache: KVCache, batch: KVBatch, stream=None):
+    """Read the new tokens' positions back into dense bf16 k, v [T, heads, d]."""
+    _call("moe_kv_read", k.data_ptr(), v.data_ptr(), cache, batch, _stream(stream))
+
+
+def moe_kv_attention_workspace_size(d) -> int:
+    return int(load().moe_kv_attention_workspace_size(d))
+
+
+def moe_kv_attention(q, scale, cache: KVCache, batch: KVBatch, out, lse, workspace, stream=None):
+    """Causal attention of q (bf16 [T, q_heads, d], any token and head strides) over the cache."""
+    qs = q.stride()
+    _call("moe_kv_attention", q.data_ptr(), qs[0], qs[1], q.shape[1], scale, cache, batch, out.data_ptr(), _ptr(lse),
+          _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream))
 
 
 def moe_set_wait_limit_ns(ns: int) -> None:

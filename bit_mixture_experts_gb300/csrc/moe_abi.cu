@@ -6,6 +6,7 @@
 #include <mutex>
 
 #include "moe_common.cuh"
+#include "moe_kv_dev.cuh"
 #ifdef MOE_TRACE
 #include "moe_tc_dev.cuh"  // the trace words' layout (TRACE_ERR_INTS, TRACE_CTAS, trace_wait)
 #endif
@@ -101,8 +102,60 @@ cudaError_t launch_gemm_pair(int mode, const uint16_t* act, int T, int H, int F,
                              const int32_t* perm, const int32_t* block_map, const int32_t* num_blocks, int bn, int cap,
                              void* out, cudaStream_t s);
 void set_wait_limit_ns(unsigned long long ns);
+cudaError_t launch_kv_append(const kv::Args& a, bool q8, const uint16_t* k, long long k_token, long long k_head,
+                             const uint16_t* v, long long v_token, long long v_head, cudaStream_t s);
+cudaError_t launch_kv_read(const kv::Args& a, bool q8, uint16_t* k, uint16_t* v, cudaStream_t s);
+cudaError_t launch_kv_attention(const kv::Args& a, bool q8, const uint16_t* q, long long q_token, long long q_head,
+                                int q_heads, float scale, uint16_t* out, float* lse, void* ws, cudaStream_t s);
+size_t kv_attention_workspace_bytes(int d);
 
 namespace {
+
+// Checks a cache and a batch and fills the kernels' description of them.  Sizes before pointers, as
+// elsewhere.  T = 0 passes (the entry points then return before they look at the dense tensors).
+int kv_args(const moe_kv_cache_t* c, const moe_kv_batch_t* b, kv::Args* a) {
+  if (!c || !b) return MOE_ERR_NULL;
+  if (c->format != MOE_KV_BF16 && c->format != MOE_KV_E4M3) return MOE_ERR_MODE;
+  if (c->d != 64 && c->d != 128) return MOE_ERR_SHAPE;
+  if (c->page_size < 16 || c->page_size > 1024 || c->page_size % 16 != 0) return MOE_ERR_SHAPE;
+  if (c->heads < 1 || c->heads > 1024 || c->num_pages < 1) return MOE_ERR_SHAPE;
+  if (static_cast<long long>(c->num_pages) * c->heads * c->page_size >= (1ll << 31)) return MOE_ERR_SHAPE;
+  if (b->T < 0 || b->T > (1 << 20) || b->B < 1 || b->B > 65536 || b->table_width < 1) return MOE_ERR_SHAPE;
+  if (static_cast<long long>(b->table_width) * c->page_size > (1ll << 30)) return MOE_ERR_SHAPE;
+  const bool q8 = c->format == MOE_KV_E4M3;
+  int rc = check_ptrs(c->k, c->v);
+  if (!rc && q8) rc = check_ptrs(c->k_scale, c->v_scale);
+  if (rc) return rc;
+  const void* idx[3] = {b->page_table, b->cu_q, b->kv_len};
+  for (const void* p : idx)
+    if (!p) return MOE_ERR_NULL;
+  for (const void* p : idx)
+    if (reinterpret_cast<uintptr_t>(p) & 3u) return MOE_ERR_ALIGN;
+  a->k = c->k;
+  a->v = c->v;
+  a->k_scale = q8 ? c->k_scale : nullptr;
+  a->v_scale = q8 ? c->v_scale : nullptr;
+  a->page_table = b->page_table;
+  a->cu_q = b->cu_q;
+  a->kv_len = b->kv_len;
+  a->num_pages = c->num_pages;
+  a->page_size = c->page_size;
+  a->heads = c->heads;
+  a->d = c->d;
+  a->B = b->B;
+  a->table_width = b->table_width;
+  a->T = b->T;
+  return MOE_OK;
+}
+
+// Strides of a [T, heads, d] tensor whose rows of d are contiguous: rows must start on 16 bytes.  The
+// stride of a dimension of one element says nothing and is not looked at.
+bool kv_strides_ok(long long token, long long head, int T, int heads) {
+  const long long most = 1ll << 40;
+  if (T <= 1) token = 0;
+  if (heads <= 1) head = 0;
+  return token % 8 == 0 && head % 8 == 0 && token >= 0 && head >= 0 && token < most && head < most;
+}
 
 int cuda_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
 
@@ -335,6 +388,62 @@ int moe_layer_forward(const uint16_t* x, const float* logits, uint16_t* out, int
                           b->num_blocks, block_n, b->y, stream);
   if (rc) return rc;
   return moe_combine(b->y, b->inv_perm, b->topk_w, out, T, H, k, stream);
+}
+
+int moe_kv_append(const uint16_t* k, int64_t k_token_stride, int64_t k_head_stride, const uint16_t* v,
+                  int64_t v_token_stride, int64_t v_head_stride, const moe_kv_cache_t* cache,
+                  const moe_kv_batch_t* batch, moe_stream_t stream) {
+  kv::Args a;
+  int rc = kv_args(cache, batch, &a);
+  if (rc) return rc;
+  if (!kv_strides_ok(k_token_stride, k_head_stride, a.T, a.heads) ||
+      !kv_strides_ok(v_token_stride, v_head_stride, a.T, a.heads))
+    return MOE_ERR_SHAPE;
+  if (a.T == 0) return MOE_OK;
+  rc = check_ptrs(k, v);
+  if (rc) return rc;
+  if (!(a.err = device_error_ptr())) return MOE_ERR_CUDA;
+  return cuda_status(launch_kv_append(a, cache->format == MOE_KV_E4M3, k, k_token_stride, k_head_stride, v,
+                                      v_token_stride, v_head_stride, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int moe_kv_read(uint16_t* k, uint16_t* v, const moe_kv_cache_t* cache, const moe_kv_batch_t* batch,
+                moe_stream_t stream) {
+  kv::Args a;
+  int rc = kv_args(cache, batch, &a);
+  if (rc) return rc;
+  if (a.T == 0) return MOE_OK;
+  rc = check_ptrs(k, v);
+  if (rc) return rc;
+  if (!(a.err = device_error_ptr())) return MOE_ERR_CUDA;
+  return cuda_status(
+      launch_kv_read(a, cache->format == MOE_KV_E4M3, k, v, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t moe_kv_attention_workspace_size(int d) { return d == 64 || d == 128 ? kv_attention_workspace_bytes(d) : 0; }
+
+int moe_kv_attention(const uint16_t* q, int64_t q_token_stride, int64_t q_head_stride, int q_heads, float scale,
+                     const moe_kv_cache_t* cache, const moe_kv_batch_t* batch, uint16_t* out, float* lse,
+                     void* workspace, size_t workspace_bytes, moe_stream_t stream) {
+  kv::Args a;
+  int rc = kv_args(cache, batch, &a);
+  if (rc) return rc;
+  if (q_heads < 1 || q_heads % a.heads != 0 || q_heads / a.heads > 128) return MOE_ERR_SHAPE;
+  if (!kv_strides_ok(q_token_stride, q_head_stride, a.T, q_heads)) return MOE_ERR_SHAPE;
+  if (!(scale > 0.0f) || scale > 3.0e38f) return MOE_ERR_SHAPE;
+  if (a.T == 0) return MOE_OK;
+  rc = check_ptrs(q, out);
+  if (rc) return rc;
+  if (reinterpret_cast<uintptr_t>(lse) & 3u) return MOE_ERR_ALIGN;
+  const size_t need = kv_attention_workspace_bytes(a.d);
+  if (need > 0) {
+    if (workspace_bytes < need) return MOE_ERR_WORKSPACE;
+    rc = check_ptrs(workspace);
+    if (rc) return rc;
+  }
+  if (!(a.err = device_error_ptr())) return MOE_ERR_CUDA;
+  return cuda_status(launch_kv_attention(a, cache->format == MOE_KV_E4M3, q, q_token_stride, q_head_stride, q_heads,
+                                         scale, out, lse, workspace, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 // The device's address of host memory it can read and write directly (pinned or registered, and

@@ -441,6 +441,101 @@ int moe_layer_forward_host(const uint16_t* x_host, const float* logits_host, uin
                            moe_stream_t stream);
 
 /* ------------------------------------------------------------------------ */
+/* Paged key/value cache and the attention that reads it                    */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * The other half of a decoder block around the MoE layer: grouped-query
+ * attention ("Perplexity Open Sources Lily", Technical Details, Model bullet:
+ * attention layers of 16 query heads over 2 KV heads).  The keys and values of
+ * all tokens seen so far live in pages of one pool; three calls share one
+ * description of a step's batch:
+ *
+ *   sequence b's new tokens are rows cu_q[b] .. cu_q[b+1]-1 of the call's
+ *   dense tensors (n_b of them, n_b >= 0); kv_len[b] counts the sequence's
+ *   tokens with the new ones, so new token i sits at position
+ *   p = kv_len[b] - n_b + i, which is row p % page_size of page
+ *   page_table[b][p / page_size].
+ *
+ * Tokens at a negative position (n_b > kv_len[b]) exist in no page: append
+ * skips them, read gives zeros, attention sees no key for them.  Rows of T that
+ * no sequence covers are left alone.
+ *
+ * Limits: d 64 or 128; page_size a multiple of 16, at most 1024;
+ * num_pages * heads * page_size < 2^31; 0 <= T <= 2^20 (T = 0 does nothing);
+ * 1 <= B <= 65536; table_width * page_size <= 2^30; heads <= 1024.  Device
+ * pointers as elsewhere 16-byte aligned, but page_table, cu_q and kv_len only
+ * 4-byte aligned.  Faults in device data never lead to an access outside the
+ * caches: a kv_len outside [0, table_width * page_size] is clamped, a page id
+ * outside [0, num_pages) is not followed; both set MOE_DEV_BAD_INDEX, as does
+ * a cu_q outside [0, T] or decreasing.
+ */
+enum {
+  MOE_KV_BF16 = 0, /* k, v bf16 */
+  MOE_KV_E4M3 = 1  /* k, v 8-bit floats (1-4-3, bias 7, no infinity) times a float32 scale, a power
+                      of two, per token and head */
+};
+
+typedef struct {
+  void* k;        /* [num_pages, heads, page_size, d] */
+  void* v;        /* same shape */
+  float* k_scale; /* MOE_KV_E4M3: [num_pages, heads, page_size]; MOE_KV_BF16: not read */
+  float* v_scale;
+  int32_t num_pages, page_size, heads, d, format;
+} moe_kv_cache_t;
+
+typedef struct {
+  const int32_t* page_table; /* [B, table_width] */
+  const int32_t* cu_q;       /* [B + 1] */
+  const int32_t* kv_len;     /* [B] */
+  int32_t B, table_width, T;
+} moe_kv_batch_t;
+
+/*
+ * moe_kv_append -- write the new tokens' keys and values into their pages.
+ * k, v bf16 [T, heads, d], element (t, h, c) at t * token_stride + h *
+ * head_stride + c (strides in elements, multiples of 8, so slices of a fused
+ * projection's output need no copy).  MOE_KV_E4M3 quantises each row of d:
+ * scale 2^e, e the least integer >= -126 with max|x| <= 448 * 2^e (e = 0 for a
+ * row of zeros), each value rounded to the nearest e4m3, ties to even; a row
+ * with an infinity or NaN is stored as NaN.  Two new tokens must not share a
+ * slot.  One launch.
+ */
+int moe_kv_append(const uint16_t* k, int64_t k_token_stride, int64_t k_head_stride, const uint16_t* v,
+                  int64_t v_token_stride, int64_t v_head_stride, const moe_kv_cache_t* cache,
+                  const moe_kv_batch_t* batch, moe_stream_t stream);
+
+/*
+ * moe_kv_read -- the values the cache stands for at the new tokens' positions:
+ * k, v bf16 [T, heads, d], dense.  With kv_len[b] new tokens a sequence is read
+ * whole.  MOE_KV_E4M3 values times their scale are exact in bf16 short of its
+ * overflow and underflow.  One launch.
+ */
+int moe_kv_read(uint16_t* k, uint16_t* v, const moe_kv_cache_t* cache, const moe_kv_batch_t* batch,
+                moe_stream_t stream);
+
+/*
+ * moe_kv_attention -- causal attention of the new tokens over their sequence's
+ * cached tokens (which must include them: append first).  q bf16 [T, q_heads,
+ * d] with strides as for moe_kv_append; q_heads a multiple of heads, at most
+ * 128 per KV head; query head h reads KV head h / (q_heads / heads).  For the
+ * token at position p:
+ *   out[t, h] = bf16(sum_j w_j v_j / sum_j w_j),  w_j = exp(scale q.k_j - m),
+ *   lse[t, h] = m + ln sum_j w_j,   j = 0 .. p,   m = max_j scale q.k_j
+ * out bf16 [T, q_heads, d], lse float32 [T, q_heads] or NULL, both dense.  A
+ * token that sees no key gets out = 0 and lse = -infinity.  Positions after a
+ * token's own, and rows of its pages past kv_len, do not enter its result
+ * whatever they hold.  Scores, sums and the output are accumulated in FP32.
+ * scale is finite and > 0.
+ * workspace: moe_kv_attention_workspace_size(d) bytes of scratch that no other
+ * call uses at the same time; its contents need no preparation.
+ */
+size_t moe_kv_attention_workspace_size(int d);
+int moe_kv_attention(const uint16_t* q, int64_t q_token_stride, int64_t q_head_stride, int q_heads, float scale,
+                     const moe_kv_cache_t* cache, const moe_kv_batch_t* batch, uint16_t* out, float* lse,
+                     void* workspace, size_t workspace_bytes, moe_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
 /* Diagnostics                                                              */
 /* ------------------------------------------------------------------------ */
 
