@@ -1,0 +1,204 @@
+// Shared by the two forms of the attention over the paged cache: the tile form
+// (moe_kv_attn.cu) and the thin one (moe_kv_thin.cuh), which run in one kernel.
+#pragma once
+#include "moe_kv_plan.cuh"
+#include "moe_ptx.cuh"
+#include "moe_tc_dev.cuh"
+
+namespace moe {
+namespace kv {
+
+struct AttnArgs {
+  const uint16_t* q;
+  long long q_token, q_head;
+  uint16_t* out;
+  float* lse;
+  float* part;  // workspace: two slots per CTA
+  float scale_log2;
+  int q_heads, group, tpt, chunk;  // chunk: rows of one copy, divides page_size and TILE
+  int least;                       // units of a CTA's share at least
+  unsigned long long wait_cycles;
+  uint32_t sleep_ns;
+};
+
+// A partial result: raw output [256][D], then its rows' maximum (times scale_log2) and sum.
+template <int D>
+__host__ __device__ constexpr int slot_floats() {
+  return 2 * TILE * (D + 2);
+}
+
+constexpr int SEGS = 4;  // work segments published ahead
+
+template <int D, bool Q8>
+struct Layout {
+  static constexpr int NH = D / 64;                // 64-wide swizzled panels of a row
+  static constexpr int PANEL = TILE * 128;         // bytes of one panel of a tile
+  static constexpr int TB = NH * PANEL;            // one bf16 tile of 128 rows
+  static constexpr int NS = Q8 ? 3 : (D == 128 ? 5 : 10);  // bf16 key/value tiles in the ring
+  static constexpr int NR = Q8 ? (D == 128 ? 3 : 12) : 0;  // e4m3 tiles in the ring
+  static constexpr int NL = Q8 ? NR : NS;          // the ring that copies land in
+  static constexpr int LAND = Q8 ? TILE * D : TB;  // bytes of one of its tiles
+  static constexpr int Q_OFF = 0;
+  static constexpr int KV_OFF = 2 * TB;
+  static constexpr int RAW_OFF = KV_OFF + NS * TB;
+  static constexpr int LAND_OFF = Q8 ? RAW_OFF : KV_OFF;
+  static constexpr int SCALE_OFF = RAW_OFF + NR * TILE * D;  // TILE scales per e4m3 tile
+  static constexpr int BAR_OFF = SCALE_OFF + NR * TILE * 4;
+  // barriers; LFULL / LEMPTY: the ring that copies land in; FULL / EMPTY: the bf16 ring, when another
+  static constexpr int LFULL = 0, LEMPTY = LFULL + NL, FULL = Q8 ? LEMPTY + NL : LFULL,
+                       EMPTY = Q8 ? FULL + NS : LEMPTY, SFULL = EMPTY + NS, PREADY = SFULL + 2, QFULL = PREADY + 2,
+                       QEMPTY = QFULL + 2, OFULL = QEMPTY + 2, FIX = OFULL + 2, ML = FIX + 2, OBFREE = ML + 1,
+                       TEAM = OBFREE + 1, SEGF = TEAM + 1, SEGE = SEGF + SEGS, DRAIN = SEGE + SEGS, NBAR = DRAIN + 1;
+  static constexpr int MISC_OFF = BAR_OFF + 8 * NBAR;       // TMEM address, abort flag, bad-row masks
+  static constexpr int SEG_OFF = (MISC_OFF + 48 + 15) / 16 * 16;  // SEGS segments of 48 bytes
+  static constexpr int ML_OFF = SEG_OFF + 48 * SEGS;        // row maxima, sums and flags: 3 x 128
+  static constexpr int BYTES = ML_OFF + 3 * TILE * 4 + 1024;  // + alignment
+  static constexpr int THREADS = Q8 ? 512 : 384;
+  // registers per thread: 128 (Q8) or 168 at launch, moved to the two softmax warpgroups
+  static constexpr int REGS_SOFTMAX = Q8 ? 176 : 208, REGS_OTHER = Q8 ? 80 : 88;
+  static_assert(256 * REGS_SOFTMAX + (THREADS - 256) * REGS_OTHER <= THREADS * (Q8 ? 128 : 168), "register split");
+  static_assert(BYTES <= 232448, "shared memory of one CTA");
+};
+
+constexpr int TM_S = 0, TM_O = 256;  // TMEM columns: S a, S b (128 each), O a, O b (D each)
+
+// Instruction descriptor of P V: D fp32, A and B bf16, A (P) K-major, B (V, rows of d per key) MN-major.
+__device__ __forceinline__ uint32_t idesc_pv(int N) { return ptx::idesc_bf16_f32(TILE, N) | (1u << 16); }
+
+// Descriptor of an MN-major operand in 128-byte swizzled atoms of 8 keys x 64 columns: the next 8 keys
+// 1024 bytes on, the next 64 columns one panel on.
+__device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t saddr, uint32_t panel) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
+  d |= static_cast<uint64_t>(panel >> 4) << 16;
+  d |= static_cast<uint64_t>(1024 >> 4) << 32;
+  d |= static_cast<uint64_t>(1) << 46;
+  d |= static_cast<uint64_t>(2) << 61;
+  return d;
+}
+
+// Two K16 steps of O += P V: P columns a, a + 8; V keys 16 further (2048 bytes) per step.
+__device__ __forceinline__ void mma_pv2_elect(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q, e;\n\t.reg .b32 x;\n\t.reg .b64 c;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %3, 0;\n\t"
+      "add.u32 x, %1, 8;\n\t"
+      "add.s64 c, %2, 128;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], c, %3, q;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+
+__device__ __forceinline__ float2 unpack2(uint64_t x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+  return r;
+}
+
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+__device__ __forceinline__ uint32_t bf16x2_mul(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a)
+               : "memory");
+  return v;
+}
+
+__device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void reg_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void reg_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// Four e4m3 codes -> four bf16 values times s (a bf16 pair).  The code's bits s eeee mmm become
+// s 0000eeee mmm0000, a bf16 that is 2^-120 of the code's value (its subnormals are bf16 subnormals);
+// s holds 2^120 times the scale as far as bf16 goes.  The product is exact short of bf16's own
+// underflow.
+__device__ __forceinline__ uint2 expand4(uint32_t x, uint32_t s) {
+  // bytes sign-extended to 16 bits (prmt's sign mode), then moved up by 4: the sign's copies that land
+  // on the exponent's upper bits are masked away
+  uint32_t a, b;
+  asm("prmt.b32 %0, %1, 0, 0x9180;" : "=r"(a) : "r"(x));
+  asm("prmt.b32 %0, %1, 0, 0xB3A2;" : "=r"(b) : "r"(x));
+  return make_uint2(bf16x2_mul((a << 4) & 0x87f087f0u, s), bf16x2_mul((b << 4) & 0x87f087f0u, s));
+}
+
+// 16 consecutive 32-bit columns of this thread's lane.
+__device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+      "[%16];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+      : "r"(taddr)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+
+constexpr int AHEAD = 3;  // key tiles by which an e4m3 cache is asked for ahead of the copies
+
+__device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
+
+// Arrive n times.
+__device__ __forceinline__ void mbar_arrive_n(uint32_t bar, uint32_t n) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(n) : "memory");
+}
+
+}  // namespace kv
+}  // namespace moe

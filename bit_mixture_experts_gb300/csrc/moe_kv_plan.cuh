@@ -9,7 +9,9 @@
 // pair, key tile are one line, of which CTA c of n takes [W c / n, W (c+1) / n):
 // even shares whatever the lengths, an item being cut where a share ends
 // (its parts are merged afterwards).  A pair that sees no key counts one unit,
-// which writes its zeros.
+// which writes its zeros.  Where a pair has rows in its first tile alone (the
+// last of a sequence, and every decode step), the second tile's half of the CTA
+// takes every other key tile instead.
 #pragma once
 #include "moe_kv_dev.cuh"
 
@@ -18,23 +20,26 @@ namespace kv {
 
 constexpr int TILE = 128;  // query rows of a tile, keys of a tile
 
-// Sum of floor((a i + b) / m) for i = 0 .. n-1 (the Euclid-like recursion on the slope a / m).
-__device__ __forceinline__ long long floor_sum(unsigned long long n, unsigned m, unsigned a, unsigned long long b) {
-  unsigned long long ans = 0;
-  while (n > 0) {
-    ans += n * (n - 1) / 2 * (a / m);
-    a %= m;
-    ans += n * (b / m);
-    b %= m;
-    const unsigned long long y = a * n + b;
-    if (y < m) break;
+// Sum of floor((a i + b) / TILE) for i = 0 .. n-1, n <= 2^20, a <= 2 TILE (the Euclid-like recursion
+// on the slope).  After the first step every term but the sum itself fits 32 bits.
+__device__ __forceinline__ long long floor_sum(int n_, int a_, long long b_) {
+  static_assert(TILE == 128, "shift");
+  unsigned long long n = static_cast<unsigned>(n_);
+  long long ans = static_cast<long long>(n * (n - 1) / 2) * (a_ >> 7) + static_cast<long long>(n) * (b_ >> 7);
+  if (n_ == 0) return 0;
+  uint32_t m = TILE, a = a_ & (TILE - 1), b = static_cast<uint32_t>(b_) & (TILE - 1);
+  for (;;) {
+    const uint32_t y = a * static_cast<uint32_t>(n) + b;
+    if (y < m) return ans;
     n = y / m;
     b = y % m;
-    const unsigned t = m;
+    const uint32_t t = m;
     m = a;
     a = t;
+    ans += static_cast<long long>(n * (n - 1) / 2) * (a / m) + static_cast<long long>(n) * (b / m);
+    a %= m;
+    b %= m;
   }
-  return static_cast<long long>(ans);
 }
 
 // A sequence's pairs: M of them of tp tokens (the last may have fewer).
@@ -55,7 +60,7 @@ struct Pairs {
     int z = 0;  // pairs that see nothing
     if (base < 0) z = min(mp, -base / tp);
     const long long first = base + (z + 1ll) * tp + TILE - 1;
-    return z + floor_sum(mp - z, TILE, tp, first);
+    return z + floor_sum(mp - z, tp, first);
   }
 
   __device__ __forceinline__ long long units() const { return M == 0 ? 0 : before(M - 1) + tiles(M - 1); }
@@ -74,12 +79,17 @@ struct Pairs {
   }
 };
 
-// A run of key tiles [t0, t1) of one item.
+// A run of key tiles [t0, t1) of one item: sequence b (first row row0, len tokens), KV head h, tokens
+// i0 .. i0 + ntok - 1 of its new ones, the first of which sits at position base; nt: the item's tiles.
 struct Seg {
-  Seq s;
-  int b, h, i0, ntok;  // sequence, KV head, first token of the pair, tokens in it
-  int t0, t1, nt;      // nt: the item's tiles
+  int row0, len, b, h, i0, ntok, base, t0, t1, nt;
 };
+
+// Quotient of two counts that nearly always fit 32 bits (a 64-bit division costs several times as much).
+__device__ __forceinline__ long long divide(long long x, long long y) {
+  if (((x | y) >> 32) == 0) return static_cast<uint32_t>(x) / static_cast<uint32_t>(y);
+  return x / y;
+}
 
 // Walks the segments of units [u, end), starting in sequence b whose first unit is b_lo.
 struct Walk {
@@ -100,13 +110,15 @@ struct Walk {
       b_hi += per_head * a.heads;
     }
     const Pairs p(s, tp);
-    const long long v = u - b_lo, r = v % per_head;
+    const long long v = u - b_lo, h = divide(v, per_head), r = v - h * per_head;
     const int mp = p.find(r);
-    g.s = s;
+    g.row0 = s.row0;
+    g.len = s.len;
     g.b = b;
-    g.h = static_cast<int>(v / per_head);
+    g.h = static_cast<int>(h);
     g.i0 = mp * tp;
     g.ntok = min(tp, s.n - g.i0);
+    g.base = s.len - s.n + g.i0;
     g.nt = p.tiles(mp);
     g.t0 = static_cast<int>(r - p.before(mp));
     g.t1 = static_cast<int>(min(static_cast<long long>(g.nt), g.t0 + (end - u)));
@@ -115,26 +127,38 @@ struct Walk {
   }
 };
 
-// Where a call's line of units is cut.
+// How a call's line of units is cut: `ctas` shares of at least `least` units (but for a line shorter
+// than that), as even as can be.
 struct Share {
-  long long total;  // W
-  int ctas;         // n: CTAs with work
-  __device__ __forceinline__ long long lo(int c) const { return total * c / ctas; }
+  long long total, each;
+  int ctas, more;  // CTAs with work; how many of them take one unit more than `each`
+
+  __device__ __forceinline__ void set(long long units, int grid, int least) {
+    total = units;
+    ctas = static_cast<int>(min(static_cast<long long>(grid), max(1ll, divide(units, least))));
+    if (units == 0) ctas = 0;
+    each = ctas ? divide(units, ctas) : 0;
+    more = static_cast<int>(units - each * ctas);
+  }
+  __device__ __forceinline__ long long lo(int c) const { return each * c + min(c, more); }
 };
 
+// A unit's sequence and that sequence's first unit.
 struct Start {
   long long b_lo;
   int b;
 };
 
-// Block-wide: the total of all sequences' units, then (for the unit that `pick` returns for that
-// total; negative: none) the sequence that holds it.  `scratch`: 33 long longs and a Start in shared
-// memory, free again on return.  NT threads.
-template <int NT, typename Pick>
-__device__ __forceinline__ long long locate(const Args& a, int tp, long long* scratch, Start* found, Pick pick) {
+// Sets `share` and finds the sequence that holds unit share.lo(cut), if there is such a share.  All
+// threads of the block; `scratch`: 34 long longs of shared memory, free again on return.  Up to 32
+// sequences every warp works it out for itself, a sequence per lane; more are dealt to the block's threads.
+template <int NT>
+__device__ __forceinline__ Start locate(const Args& a, int tp, int grid, int least, int cut, long long* scratch,
+                                        Share& share) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int per = ceil_div(a.B, NT);
-  const int b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
+  const bool small = a.B <= 32;
+  const int per = small ? 1 : ceil_div(a.B, NT);
+  const int b0 = min((small ? lane : tid) * per, a.B), b1 = min(b0 + per, a.B);
   long long mine = 0;
   for (int b = b0; b < b1; ++b) mine += Pairs(load_seq(a, b), tp).units() * a.heads;
   long long incl = mine;
@@ -142,6 +166,17 @@ __device__ __forceinline__ long long locate(const Args& a, int tp, long long* sc
   for (int d = 1; d < 32; d <<= 1) {
     const long long o = __shfl_up_sync(0xffffffffu, incl, d);
     if (lane >= d) incl += o;
+  }
+  Start found = {0, 0};
+  if (small) {
+    share.set(__shfl_sync(0xffffffffu, incl, 31), grid, least);
+    const long long want = share.lo(cut);
+    const uint32_t past = __ballot_sync(0xffffffffu, incl > want);  // sequences that end after it
+    if (cut < share.ctas) {
+      found.b = __ffs(past) - 1;
+      found.b_lo = __shfl_sync(0xffffffffu, incl - mine, found.b);
+    }
+    return found;
   }
   if (lane == 31) scratch[warp] = incl;
   __syncthreads();
@@ -152,20 +187,23 @@ __device__ __forceinline__ long long locate(const Args& a, int tp, long long* sc
     if (w < warp) off += x;
     total += x;
   }
-  const long long want = pick(total);
+  share.set(total, grid, least);
+  const long long want = share.lo(cut);
   long long lo = off + incl - mine;
-  if (want >= lo && want < lo + mine) {
+  Start* shared = reinterpret_cast<Start*>(scratch + 32);
+  if (cut < share.ctas && want >= lo && want < lo + mine) {
     int b = b0;
     for (;; ++b) {
       const long long n = Pairs(load_seq(a, b), tp).units() * a.heads;
       if (want < lo + n) break;
       lo += n;
     }
-    found->b = b;
-    found->b_lo = lo;
+    shared->b = b;
+    shared->b_lo = lo;
   }
   __syncthreads();
-  return total;
+  if (cut < share.ctas) found = *shared;
+  return found;
 }
 
 }  // namespace kv
