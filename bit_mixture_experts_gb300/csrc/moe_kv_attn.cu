@@ -57,10 +57,8 @@ __global__ void __launch_bounds__(Layout<D, Q8>::THREADS, 1)
   const int cta = static_cast<int>(blockIdx.x);
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < L::NL; ++i) {
-      ptx::mbar_init(bar(L::LFULL + i), 1);
-      ptx::mbar_init(bar(L::LEMPTY + i), 8);
-    }
+    for (int i = 0; i < 2 * L::NL; ++i) ptx::mbar_init(bar(L::LFULL + i), 1);
+    for (int i = 0; i < L::NL; ++i) ptx::mbar_init(bar(L::LEMPTY + i), L::LEMPTY_COUNT);
     if (Q8)
       for (int i = 0; i < NS; ++i) {
         ptx::mbar_init(bar(L::FULL + i), 4);
@@ -70,7 +68,7 @@ __global__ void __launch_bounds__(Layout<D, Q8>::THREADS, 1)
       ptx::mbar_init(bar(L::SFULL + t), 1);
       ptx::mbar_init(bar(L::PREADY + t), 4);
       ptx::mbar_init(bar(L::QFULL + t), 1);
-      ptx::mbar_init(bar(L::QEMPTY + t), 8);
+      ptx::mbar_init(bar(L::QEMPTY + t), t == 0 ? 9 : 8);
       ptx::mbar_init(bar(L::OFULL + t), 1);
       ptx::mbar_init(bar(L::FIX + t), 4);
     }
@@ -93,8 +91,15 @@ __global__ void __launch_bounds__(Layout<D, Q8>::THREADS, 1)
   kv::Share share;
   kv::Start from;
   if (a.B > 32 || warp == 3)
-    from = kv::locate<L::THREADS>(a, 2 * g.tpt, static_cast<int>(gridDim.x), g.least, cta,
+    from = kv::locate<L::THREADS>(a, 2 * g.tpt, static_cast<int>(gridDim.x), cta,
                                   reinterpret_cast<long long*>(smem + L::KV_OFF), share);
+  Seg sg;
+  kv::Walk walk(a, 2 * g.tpt, 0, 0, 0, 0, false);
+  if (warp == 3) {  // publishes the segments; the first is worked out while the CTA starts up
+    if (cta < share.ctas)
+      walk = kv::Walk(a, 2 * g.tpt, share.lo(cta), share.lo(cta + 1), from.b, from.b_lo, share.whole);
+    if (!walk.next(sg)) sg.ntok = 0;  // the end
+  }
   ptx::fence_proxy_async_smem();  // the scratch is overwritten by copies
   ptx::tc_fence_before();
   __syncthreads();
@@ -119,7 +124,6 @@ __global__ void __launch_bounds__(Layout<D, Q8>::THREADS, 1)
     return sg.ntok > 0;
   };
   auto thin = [&](const Seg& sg) -> bool { return sg.ntok * g.group <= THIN_ROWS; };
-  Seg sg;
 
   if (warp < 4) {
     reg_dec<L::REGS_OTHER>();
@@ -165,7 +169,7 @@ __global__ void __launch_bounds__(Layout<D, Q8>::THREADS, 1)
               ok = false;
               break;
             }
-            const uint32_t f = bar(L::LFULL + st), dst = sbase + L::LAND_OFF + st * L::LAND;
+            const uint32_t f = bar(L::LFULL + n % (2 * L::NL)), dst = sbase + L::LAND_OFF + st * L::LAND;
             const CUtensorMap* map = kind ? &tmap_v : &tmap_k;
             const float* scale = kind ? a.v_scale : a.k_scale;
             ptx::mbar_arrive_expect_tx_elect(f, static_cast<uint32_t>(have * g.chunk * (Q8 ? D + 4 : 2 * D)));
@@ -192,74 +196,62 @@ __global__ void __launch_bounds__(Layout<D, Q8>::THREADS, 1)
       }
       // every copy issued has landed before the CTA ends (at once unless a wait gave up)
       for (int i = n > L::NL ? n - L::NL : 0; i < n; ++i)
-        tc_dev::wait_drain(bar(L::LFULL + i % L::NL), (i / L::NL) & 1, 0);
+        tc_dev::wait_drain(bar(L::LFULL + i % (2 * L::NL)), (i / (2 * L::NL)) & 1, 0);
     } else if (warp == 1) {
       // ---------------------------------------------- MMA issue, one unit behind for P V
       // A unit's tiles: a and b (a pair), or one of them (t alternates along the keys).
       const uint32_t id_s = ptx::idesc_bf16_f32(TILE, TILE), id_o = idesc_pv(D);
-      uint32_t p_ph[2] = {0, 0}, q_ph[2] = {0, 0};
-      int kst = 0, kph = 0;  // ring slot of the current unit's K
+      uint32_t p_ph[2] = {0, 0}, qb_ph = 0;
+      int ki = 0;  // the current unit's K in the bf16 ring, V next to it
       struct {
-        int tiles, st, ph;  // bit mask of tiles whose P V is still to do; ring slot of V
-        bool first, last;   // of the item's run for its tiles
-      } prev = {0, 0, 0, false, false};
-      auto advance = [&](int by) {
-        kst += by;
-        if (kst >= NS) {
-          kst -= NS;
-          kph ^= 1;
-        }
+        int tiles, vi;     // bit mask of tiles whose P V is still to do; V in the ring
+        bool first, last;  // of the item's run for its tiles
+      } prev = {0, 0, false, false};
+      auto full = [&](int i) -> bool {
+        return Q8 ? wait(L::FULL + i % NS, (i / NS) & 1) : wait(L::LFULL + i % (2 * NS), (i / (2 * NS)) & 1);
       };
       // releases a ring tile once the MMAs issued so far are done with it
-      auto release = [&](int st) {
-        if (!Q8 && lane == 0) mbar_arrive_n(bar(L::EMPTY + st), 7);
-        ptx::mma_commit_elect(bar(L::EMPTY + st));
+      auto release = [&](int i) {
+        const uint32_t b = bar((Q8 ? L::EMPTY : L::LEMPTY) + i % NS);
+        if (!Q8 && lane == 0) mbar_arrive_n(b, L::LEMPTY_COUNT - 1);
+        ptx::mma_commit_elect(b);
       };
       // O += P V of the previous unit for tile t
       auto finish = [&](int t) -> bool {
         if (!(prev.tiles >> t & 1)) return true;
-        if (!wait(L::FULL + prev.st, prev.ph) || !wait(L::PREADY + t, p_ph[t])) return false;
+        if (!full(prev.vi) || !wait(L::PREADY + t, p_ph[t])) return false;
         p_ph[t] ^= 1;
         ptx::tc_fence_after();
         const uint32_t o = tmem + TM_O + t * D, p = tmem + TM_S + t * TILE;
-        const uint64_t d = desc_mn_sw128(sbase + L::KV_OFF + prev.st * TB, PANEL);
+        const uint64_t d = desc_mn_sw128(sbase + L::KV_OFF + prev.vi % NS * TB, PANEL);
 #pragma unroll
         for (int j = 0; j < 4; ++j) mma_pv2_elect(o, p + 16 * j, d + 256 * j, id_o, (j > 0 || !prev.first) ? 1u : 0u);
         if (prev.last) ptx::mma_commit_elect(bar(L::OFULL + t));
         prev.tiles &= ~(1 << t);
-        if (prev.tiles == 0) release(prev.st);
+        if (prev.tiles == 0) release(prev.vi);
         return true;
       };
       // S = Q K^T of the current unit into tile t's scores, from query tile q
       auto scores = [&](int t, int q, bool last) {
         const uint64_t dq = ptx::smem_desc_sw128(sbase + L::Q_OFF + q * TB);
-        const uint64_t dk = ptx::smem_desc_sw128(sbase + L::KV_OFF + kst * TB);
+        const uint64_t dk = ptx::smem_desc_sw128(sbase + L::KV_OFF + ki % NS * TB);
 #pragma unroll
         for (int hf = 0; hf < NH; ++hf)
           ptx::mma_group_ss_elect(tmem + TM_S + t * TILE, dq + hf * (PANEL >> 4), dk + hf * (PANEL >> 4), id_s,
                                   hf ? 1u : 0u);
         ptx::mma_commit_elect(bar(L::SFULL + t));
         if (last) {
-          if (lane == 0) mbar_arrive_n(bar(L::QEMPTY + q), 7);
+          if (q == 1 && lane == 0) mbar_arrive_n(bar(L::QEMPTY + 1), 7);
           ptx::mma_commit_elect(bar(L::QEMPTY + q));
         }
-      };
-      auto query = [&](int q) -> bool {
-        const uint32_t ph = q_ph[q];
-        q_ph[q] ^= 1;
-        return wait(L::QFULL + q, ph);
       };
       bool ok = true;
       while (ok && next(sg)) {
         if (thin(sg)) {
           // the softmax warps' own; its tiles pass by, and what is pending must not wait for it
-          ok = finish(0) && finish(1);
-          q_ph[0] ^= 1;
-          if (!Q8) {
-            const int by = 2 * (sg.t1 - sg.t0), to = kst + by;
-            kph ^= to / NS & 1;
-            kst = to % NS;
-          }
+          ok = finish(0) && finish(1) && wait(L::QFULL, (segs - 1) & 1);
+          if (ok && lane == 0) ptx::mbar_arrive(bar(L::QEMPTY));
+          if (!Q8) ki += 2 * (sg.t1 - sg.t0);
           continue;
         }
         const bool pair = sg.ntok > g.tpt;
@@ -268,25 +260,24 @@ __global__ void __launch_bounds__(Layout<D, Q8>::THREADS, 1)
           const bool last = kt + 1 == sg.t1;
           const int t = pair ? 0 : j & 1;
           // the scores of the next unit come before the previous unit's P V, unless they share a buffer
-          ok = finish(t) && (j > 0 || query(0)) && wait(L::FULL + kst, kph);
+          ok = finish(t) && (j > 0 || wait(L::QFULL, (segs - 1) & 1)) && full(ki);
           if (!ok) break;
           ptx::tc_fence_after();
           scores(t, 0, last);
           if (pair) {
-            ok = finish(1) && (j > 0 || query(1));
+            ok = finish(1) && (j > 0 || wait(L::QFULL + 1, qb_ph));
             if (!ok) break;
+            if (j == 0) qb_ph ^= 1;
             ptx::tc_fence_after();
             scores(1, 1, last);
           }
-          release(kst);
+          release(ki);
           if (!pair && !(ok = finish(t ^ 1))) break;
-          advance(1);
           prev.tiles = pair ? 3 : 1 << t;
-          prev.st = kst;
-          prev.ph = kph;
+          prev.vi = ki + 1;
           prev.first = j < (pair ? 1 : 2);
           prev.last = kt + (pair ? 1 : 2) >= sg.t1;
-          advance(1);
+          ki += 2;
         }
       }
       if (ok) ok = finish(0) && finish(1);
@@ -299,24 +290,29 @@ __global__ void __launch_bounds__(Layout<D, Q8>::THREADS, 1)
       uint32_t ph[2] = {1, 1};  // of QEMPTY: the first use waits for nothing
       bool ok = true;
       while (ok && next(sg)) {
-        int t = 0;
-        for (; t < 2; ++t) {
-          const int tok0 = t * g.tpt, ntok = min(g.tpt, sg.ntok - tok0);
-          if (ntok <= 0) break;
+        const bool two = sg.ntok > g.tpt;
+        for (int t = 0; t < 2; ++t) {
+          const int tok0 = t * g.tpt, rows = min(g.tpt, sg.ntok - tok0) * g.group;
+          if (t == 1 && !two && !thin(sg)) break;
           ok = wait(L::QEMPTY + t, ph[t]);
           if (!ok) break;
           ph[t] ^= 1;
+          if (t == 1 && !two) break;  // the thin form uses both tiles' memory
+          // a lane's column of 8 values, 32 / C rows at a time, in the order token, head
+          const long long by_token = g.q_token - g.group * g.q_head;
+          int hd = lane / C;
           const uint16_t* src = g.q + static_cast<long long>(sg.row0 + sg.i0 + tok0) * g.q_token +
-                                static_cast<long long>(sg.h) * g.group * g.q_head + lane % C * 8;
+                                (static_cast<long long>(sg.h) * g.group + hd) * g.q_head + lane % C * 8;
           const uint32_t col = sbase + L::Q_OFF + t * TB + (lane % C >> 3) * PANEL;
-          int tok = 0, hd = lane / C;  // 32 / C rows at a time
-          for (int r = lane / C; r < ntok * g.group; r += 32 / C) {
+#pragma unroll 4
+          for (int r = lane / C; r < rows; r += 32 / C) {
             while (hd >= g.group) {
               hd -= g.group;
-              ++tok;
+              src += by_token;
             }
-            ptx::cp_async_16(col + r * 128 + (((lane & 7) ^ (r & 7)) << 4), src + tok * g.q_token + hd * g.q_head);
+            ptx::cp_async_16(col + r * 128 + (((lane & 7) ^ (r & 7)) << 4), src);
             hd += 32 / C;
+            src += 32 / C * g.q_head;
           }
           ptx::cp_async_commit();
           if (t == 1) {
@@ -331,15 +327,13 @@ __global__ void __launch_bounds__(Layout<D, Q8>::THREADS, 1)
         if (!ok) break;
         ptx::fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(bar(L::QFULL + t - 1));
+        if (lane == 0) ptx::mbar_arrive(bar(L::QFULL + (two ? 1 : 0)));
       }
     } else {
       // ---------------------------------------------- the CTA's segments
-      const bool work = cta < share.ctas;
-      kv::Walk walk(a, 2 * g.tpt, work ? share.lo(cta) : 0, work ? share.lo(cta + 1) : 0, from.b, from.b_lo);
       for (int n = 0;; ++n) {
         const int slot = n % SEGS;
-        if (!walk.next(sg)) sg.ntok = 0;  // the end
+        if (n > 0 && !walk.next(sg)) sg.ntok = 0;
         if (n >= SEGS && !wait(L::SEGE + slot, (n / SEGS - 1) & 1)) break;
         if (lane == 0) {
           int4* p = reinterpret_cast<int4*>(smem + L::SEG_OFF + slot * 48);
@@ -367,6 +361,8 @@ __global__ void __launch_bounds__(Layout<D, Q8>::THREADS, 1)
     bool ok = true, lent = false;  // lent: O b (and its rows' sums) are being read by tile a's threads
     while (ok && next(sg)) {
       const int run = sg.t1 - sg.t0;
+      ok = wait(L::QFULL, (segs - 1) & 1);
+      if (!ok) break;
       if (thin(sg)) {
         if (lent) {
           ok = wait(L::OBFREE, t == 1 ? x_ph : x_ph ^ 1);
@@ -375,11 +371,12 @@ __global__ void __launch_bounds__(Layout<D, Q8>::THREADS, 1)
           lent = false;
         }
         const ThinCtx ctx = {sbase, smem, s_abort, warp - 4, lane};
-        ok = thin_segment<D, Q8>(a, g, sg, ctx, cta, all, segs - 1, team_ph);
+        ok = thin_segment<D, Q8>(a, g, sg, ctx, cta, all, team_ph);
         all += run;
         continue;
       }
-      const int ring0 = Q8 ? 2 * n : 2 * all;  // ring tiles before the segment
+      if (lane == 0) ptx::mbar_arrive(bar(L::QEMPTY));  // the queries are the MMA warp's
+      const int ring0 = Q8 ? 2 * n : 2 * all;           // bf16 tiles before the segment
       const int n0 = n;
       all += run;
       n += run;
@@ -413,7 +410,7 @@ __global__ void __launch_bounds__(Layout<D, Q8>::THREADS, 1)
         if (t == 0 || !pair) {
           if (fix) {
             const int v = ring0 + 2 * (kt - sg.t0) + 1, st = v % NS;
-            ok = wait(L::FULL + st, (v / NS) & 1);
+            ok = Q8 ? wait(L::FULL + st, (v / NS) & 1) : wait(L::LFULL + v % (2 * NS), (v / (2 * NS)) & 1);
             if (!ok) break;
             const uint32_t row = sbase + L::KV_OFF + st * TB + r * 128;
             const int p = k0 + r;
@@ -477,7 +474,8 @@ __global__ void __launch_bounds__(Layout<D, Q8>::THREADS, 1)
           const float top = fmaxf(m, max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]));
           if (kt == first) {
             m = top;
-          } else if (__any_sync(0xffffffffu, (top - m) * g.scale_log2 > 8.f)) {
+          } else if (__any_sync(0xffffffffu, valid && (top - m) * g.scale_log2 > 8.f)) {
+            // (rows of no query hold leftovers and have no say)
             // this tile's scores are complete, so the P V that was issued before them is too
             const float f = top == m ? 1.f : ex2((m - top) * g.scale_log2);
 #pragma unroll 1
@@ -524,7 +522,7 @@ __global__ void __launch_bounds__(Layout<D, Q8>::THREADS, 1)
         // tile a's threads join both halves of the keys
         s_ml[r] = ml;
         s_ml[TILE + r] = l;
-        s_ml[2 * TILE + r] = bad ? 1.f : 0.f;
+        smem[L::ML_OFF + 8 * TILE + r] = bad;
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(bar(L::ML));
         o_ph[1] ^= 1;
@@ -546,7 +544,7 @@ __global__ void __launch_bounds__(Layout<D, Q8>::THREADS, 1)
           fb = ex2(mb - top0);
           l = l * fa + s_ml[TILE + r] * fb;
           ml = top;
-          bad |= s_ml[2 * TILE + r] != 0.f;
+          bad |= smem[L::ML_OFF + 8 * TILE + r] != 0;
         }
         o_ph[1] ^= 1;
       }
@@ -629,14 +627,15 @@ __global__ void __launch_bounds__(Layout<D, Q8>::THREADS, 1)
     int n = 0, m = 0;          // tiles landed, tiles expanded
     bool ok = true;
     while (ok && next(sg)) {
-      if (thin(sg)) {
-        n += 2 * (sg.t1 - sg.t0);
-        continue;
-      }
-      for (int x = 0; ok && x < 2 * (sg.t1 - sg.t0); ++x, ++n, ++m) {
+      const bool pass = thin(sg);
+      for (int x = 0; ok && x < 2 * (sg.t1 - sg.t0); ++x, ++n) {
         const int rs = n % L::NL, ts = m % NS;
-        ok = wait(L::LFULL + rs, (n / L::NL) & 1);
+        ok = wait(L::LFULL + n % (2 * L::NL), (n / (2 * L::NL)) & 1);
         if (!ok) break;
+        if (pass) {
+          if (lane == 0) ptx::mbar_arrive(bar(L::LEMPTY + rs));
+          continue;
+        }
         // one row per thread; the swizzles keep eight neighbouring threads' loads and stores in
         // different banks
         const uint32_t src = sbase + L::LAND_OFF + rs * L::LAND + tid * D, dst = sbase + L::KV_OFF + ts * TB + tid * 128;
@@ -670,9 +669,10 @@ __global__ void __launch_bounds__(Layout<D, Q8>::THREADS, 1)
         ptx::fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive_n(bar(L::LEMPTY + rs), 2);
+          mbar_arrive_n(bar(L::LEMPTY + rs), 3);
           ptx::mbar_arrive(bar(L::FULL + ts));
         }
+        ++m;
       }
     }
   }
@@ -693,17 +693,17 @@ constexpr int MERGE_WARPS = 8, MERGE_Y = 8;
 template <int D>
 __global__ void __launch_bounds__(32 * MERGE_WARPS) kv_merge_kernel(const kv::Args a, const AttnArgs g, int ctas) {
   constexpr int V = D / 32;
-  __shared__ long long scratch[40];
+  __shared__ long long scratch[50];
   __shared__ float s_m[MERGE_WARPS], s_l[MERGE_WARPS], s_acc[MERGE_WARPS][D];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int cut = static_cast<int>(blockIdx.x) + 1;
   kv::Share share;
-  const kv::Start from = kv::locate<32 * MERGE_WARPS>(a, 2 * g.tpt, ctas, g.least, cut, scratch, share);
+  const kv::Start from = kv::locate<32 * MERGE_WARPS>(a, 2 * g.tpt, ctas, cut, scratch, share);
   Seg sg;
   int np = 0;  // parts: slot 1 of CTA cut - 1, slot 0 of the CTAs after it
-  if (cut < share.ctas) {
+  if (cut < share.ctas && !share.whole) {
     const long long u = share.lo(cut);
-    kv::Walk walk(a, 2 * g.tpt, u, share.total, from.b, from.b_lo);
+    kv::Walk walk(a, 2 * g.tpt, u, share.total, from.b, from.b_lo, false);
     walk.next(sg);
     const long long first = u - sg.t0, end = first + sg.nt;  // the item's units
     if (sg.t0 > 0 && share.lo(cut - 1) <= first) {           // a cut, and the first of its item
@@ -817,8 +817,8 @@ cudaError_t launch(const kv::Args& a, const AttnArgs& g, const CUtensorMap& tk, 
   kv_attention_kernel<D, Q8><<<ctas, L::THREADS, L::BYTES, s>>>(a, g, tk, tv);
   note_launches(1);
   e = cudaGetLastError();
-  // items of one key tile are never cut
-  if (e != cudaSuccess || ctas < 2 || static_cast<long long>(a.table_width) * a.page_size <= TILE) return e;
+  // items of up to WHOLE key tiles are never cut
+  if (e != cudaSuccess || static_cast<long long>(a.table_width) * a.page_size <= WHOLE * TILE) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas - 1, min(static_cast<long long>(a.T) * g.group, static_cast<long long>(MERGE_Y)));
   cfg.blockDim = dim3(32 * MERGE_WARPS);
@@ -866,7 +866,6 @@ cudaError_t launch_kv_attention(const kv::Args& a, bool q8, const uint16_t* q, l
   const long long rows = static_cast<long long>(a.num_pages) * a.heads * a.page_size;
   if (!encode_pool(&tk, a.k, rows, a.d, g.chunk, q8) || !encode_pool(&tv, a.v, rows, a.d, g.chunk, q8))
     return cudaErrorInvalidValue;
-  g.least = 1;
   const int ctas = num_sms();
   if (a.d == 64) return q8 ? launch<64, true>(a, g, tk, tv, ctas, s) : launch<64, false>(a, g, tk, tv, ctas, s);
   return q8 ? launch<128, true>(a, g, tk, tv, ctas, s) : launch<128, false>(a, g, tk, tv, ctas, s);

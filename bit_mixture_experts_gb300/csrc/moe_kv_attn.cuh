@@ -16,7 +16,6 @@ struct AttnArgs {
   float* part;  // workspace: two slots per CTA
   float scale_log2;
   int q_heads, group, tpt, chunk;  // chunk: rows of one copy, divides page_size and TILE
-  int least;                       // units of a CTA's share at least
   unsigned long long wait_cycles;
   uint32_t sleep_ns;
 };
@@ -44,15 +43,24 @@ struct Layout {
   static constexpr int LAND_OFF = Q8 ? RAW_OFF : KV_OFF;
   static constexpr int SCALE_OFF = RAW_OFF + NR * TILE * D;  // TILE scales per e4m3 tile
   static constexpr int BAR_OFF = SCALE_OFF + NR * TILE * 4;
-  // barriers; LFULL / LEMPTY: the ring that copies land in; FULL / EMPTY: the bf16 ring, when another
-  static constexpr int LFULL = 0, LEMPTY = LFULL + NL, FULL = Q8 ? LEMPTY + NL : LFULL,
-                       EMPTY = Q8 ? FULL + NS : LEMPTY, SFULL = EMPTY + NS, PREADY = SFULL + 2, QFULL = PREADY + 2,
-                       QEMPTY = QFULL + 2, OFULL = QEMPTY + 2, FIX = OFULL + 2, ML = FIX + 2, OBFREE = ML + 1,
-                       TEAM = OBFREE + 1, SEGF = TEAM + 1, SEGE = SEGF + SEGS, DRAIN = SEGE + SEGS, NBAR = DRAIN + 1;
+  // Barriers.  LFULL / LEMPTY: the ring that copies land in; FULL / EMPTY: the e4m3 form's bf16 ring.  A
+  // wait by parity is only right if its thread cannot fall two phases behind or get ahead of the phase
+  // before it, so
+  //  - tile i of the landing ring completes LFULL[i % (2 NL)], twice as many barriers as slots: a team of
+  //    the thin form that waits for tile i skipped the tiles of the other team, but released tile i - 3 or
+  //    a later one of its own, whose slot was filled after tile i - 2 NL had landed (NL >= 3);
+  //  - whoever waits for QFULL[0] (the MMA warp and the softmax warps) does so for every segment, and
+  //    QEMPTY[0] needs all of them;
+  //  - the expanding warps take note of every landed tile, the thin form's too, and LEMPTY needs them.
+  static constexpr int LFULL = 0, LEMPTY = LFULL + 2 * NL, FULL = LEMPTY + NL, EMPTY = FULL + (Q8 ? NS : 0),
+                       SFULL = EMPTY + (Q8 ? NS : 0), PREADY = SFULL + 2, QFULL = PREADY + 2, QEMPTY = QFULL + 2,
+                       OFULL = QEMPTY + 2, FIX = OFULL + 2, ML = FIX + 2, OBFREE = ML + 1, TEAM = OBFREE + 1,
+                       SEGF = TEAM + 1, SEGE = SEGF + SEGS, DRAIN = SEGE + SEGS, NBAR = DRAIN + 1;
+  static constexpr int LEMPTY_COUNT = Q8 ? 12 : 8;          // arrivals that release a slot
   static constexpr int MISC_OFF = BAR_OFF + 8 * NBAR;       // TMEM address, abort flag, bad-row masks
   static constexpr int SEG_OFF = (MISC_OFF + 48 + 15) / 16 * 16;  // SEGS segments of 48 bytes
-  static constexpr int ML_OFF = SEG_OFF + 48 * SEGS;        // row maxima, sums and flags: 3 x 128
-  static constexpr int BYTES = ML_OFF + 3 * TILE * 4 + 1024;  // + alignment
+  static constexpr int ML_OFF = SEG_OFF + 48 * SEGS;        // row maxima and sums (2 x 128 floats), flags (128 bytes)
+  static constexpr int BYTES = ML_OFF + 9 * TILE + 1024;    // + alignment
   static constexpr int THREADS = Q8 ? 512 : 384;
   // registers per thread: 128 (Q8) or 168 at launch, moved to the two softmax warpgroups
   static constexpr int REGS_SOFTMAX = Q8 ? 176 : 208, REGS_OTHER = Q8 ? 80 : 88;

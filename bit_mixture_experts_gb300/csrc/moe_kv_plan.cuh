@@ -8,7 +8,8 @@
 // pair's last token sees.  All units of a call in the order sequence, head,
 // pair, key tile are one line, of which CTA c of n takes [W c / n, W (c+1) / n):
 // even shares whatever the lengths, an item being cut where a share ends
-// (its parts are merged afterwards).  A pair that sees no key counts one unit,
+// (its parts are merged afterwards).  Where all items are short it goes whole to
+// the CTA whose share it starts in: nothing to merge.  A pair that sees no key counts one unit,
 // which writes its zeros.  Where a pair has rows in its first tile alone (the
 // last of a sequence, and every decode step), the second tile's half of the CTA
 // takes every other key tile instead.
@@ -93,21 +94,31 @@ __device__ __forceinline__ long long divide(long long x, long long y) {
 
 // Walks the segments of units [u, end), starting in sequence b whose first unit is b_lo.
 struct Walk {
-  const Args& a;
+  const Args* ap;
   int tp, b;
   long long u, end, b_lo, b_hi, per_head;
   Seq s;
+  bool whole;
 
-  __device__ __forceinline__ Walk(const Args& a_, int tp_, long long u_, long long end_, int b_, long long b_lo_)
-      : a(a_), tp(tp_), b(b_ - 1), u(u_), end(end_), b_lo(0), b_hi(b_lo_), per_head(0) {}
+  __device__ __forceinline__ Walk(const Args& a_, int tp_, long long u_, long long end_, int b_, long long b_lo_,
+                                  bool whole_)
+      : ap(&a_), tp(tp_), b(b_ - 1), u(u_), end(end_), b_lo(0), b_hi(b_lo_), per_head(0), whole(whole_) {}
 
+  // `whole`: items that start in [u, end), each in full; otherwise units [u, end).
   __device__ __forceinline__ bool next(Seg& g) {
-    if (u >= end) return false;
+    for (;;) {
+      if (u >= end) return false;
+      step(g);
+      if (!whole || g.t0 == 0) return true;
+    }
+  }
+
+  __device__ __forceinline__ void step(Seg& g) {
     while (u >= b_hi) {
-      s = load_seq(a, ++b);
+      s = load_seq(*ap, ++b);
       per_head = Pairs(s, tp).units();
       b_lo = b_hi;
-      b_hi += per_head * a.heads;
+      b_hi += per_head * ap->heads;
     }
     const Pairs p(s, tp);
     const long long v = u - b_lo, h = divide(v, per_head), r = v - h * per_head;
@@ -121,24 +132,27 @@ struct Walk {
     g.base = s.len - s.n + g.i0;
     g.nt = p.tiles(mp);
     g.t0 = static_cast<int>(r - p.before(mp));
-    g.t1 = static_cast<int>(min(static_cast<long long>(g.nt), g.t0 + (end - u)));
+    g.t1 = whole ? g.nt : static_cast<int>(min(static_cast<long long>(g.nt), g.t0 + (end - u)));
     u += g.t1 - g.t0;
-    return true;
   }
 };
 
-// How a call's line of units is cut: `ctas` shares of at least `least` units (but for a line shorter
-// than that), as even as can be.
+// Items of up to WHOLE units are not cut (merging their parts costs more than they do), nor items that are
+// small beside a share.
+constexpr int WHOLE = 5;
+
+// How a call's line of units is dealt out: as evenly as can be.
 struct Share {
   long long total, each;
   int ctas, more;  // CTAs with work; how many of them take one unit more than `each`
+  bool whole;
 
-  __device__ __forceinline__ void set(long long units, int grid, int least) {
+  __device__ __forceinline__ void set(long long units, int longest, int grid) {
     total = units;
-    ctas = static_cast<int>(min(static_cast<long long>(grid), max(1ll, divide(units, least))));
-    if (units == 0) ctas = 0;
+    ctas = static_cast<int>(min(static_cast<long long>(grid), units));
     each = ctas ? divide(units, ctas) : 0;
     more = static_cast<int>(units - each * ctas);
+    whole = longest <= WHOLE + each / 16;
   }
   __device__ __forceinline__ long long lo(int c) const { return each * c + min(c, more); }
 };
@@ -150,17 +164,22 @@ struct Start {
 };
 
 // Sets `share` and finds the sequence that holds unit share.lo(cut), if there is such a share.  All
-// threads of the block; `scratch`: 34 long longs of shared memory, free again on return.  Up to 32
+// threads of the block; `scratch`: 50 long longs of shared memory, free again on return.  Up to 32
 // sequences every warp works it out for itself, a sequence per lane; more are dealt to the block's threads.
 template <int NT>
-__device__ __forceinline__ Start locate(const Args& a, int tp, int grid, int least, int cut, long long* scratch,
-                                        Share& share) {
+__device__ __forceinline__ Start locate(const Args& a, int tp, int grid, int cut, long long* scratch, Share& share) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const bool small = a.B <= 32;
   const int per = small ? 1 : ceil_div(a.B, NT);
   const int b0 = min((small ? lane : tid) * per, a.B), b1 = min(b0 + per, a.B);
   long long mine = 0;
-  for (int b = b0; b < b1; ++b) mine += Pairs(load_seq(a, b), tp).units() * a.heads;
+  int longest = 0;
+  for (int b = b0; b < b1; ++b) {
+    const Pairs p(load_seq(a, b), tp);
+    mine += p.units() * a.heads;
+    if (p.M > 0) longest = max(longest, p.tiles(p.M - 1));
+  }
+  longest = __reduce_max_sync(0xffffffffu, longest);
   long long incl = mine;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
@@ -169,7 +188,7 @@ __device__ __forceinline__ Start locate(const Args& a, int tp, int grid, int lea
   }
   Start found = {0, 0};
   if (small) {
-    share.set(__shfl_sync(0xffffffffu, incl, 31), grid, least);
+    share.set(__shfl_sync(0xffffffffu, incl, 31), longest, grid);
     const long long want = share.lo(cut);
     const uint32_t past = __ballot_sync(0xffffffffu, incl > want);  // sequences that end after it
     if (cut < share.ctas) {
@@ -178,7 +197,11 @@ __device__ __forceinline__ Start locate(const Args& a, int tp, int grid, int lea
     }
     return found;
   }
-  if (lane == 31) scratch[warp] = incl;
+  int* longests = reinterpret_cast<int*>(scratch + 32);
+  if (lane == 31) {
+    scratch[warp] = incl;
+    longests[warp] = longest;
+  }
   __syncthreads();
   long long off = 0, total = 0;
 #pragma unroll
@@ -186,11 +209,12 @@ __device__ __forceinline__ Start locate(const Args& a, int tp, int grid, int lea
     const long long x = scratch[w];
     if (w < warp) off += x;
     total += x;
+    longest = max(longest, longests[w]);
   }
-  share.set(total, grid, least);
+  share.set(total, longest, grid);
   const long long want = share.lo(cut);
   long long lo = off + incl - mine;
-  Start* shared = reinterpret_cast<Start*>(scratch + 32);
+  Start* shared = reinterpret_cast<Start*>(scratch + 48);
   if (cut < share.ctas && want >= lo && want < lo + mine) {
     int b = b0;
     for (;; ++b) {

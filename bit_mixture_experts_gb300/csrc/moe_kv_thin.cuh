@@ -3,8 +3,9 @@
 //
 // Such an item is bound by reading its keys and values, and a 128-row tile
 // would spend its one-thread-per-row softmax on a handful of rows.  Instead the
-// eight softmax warps share out the key tile: 16 query rows and 16 keys per
-// warp and step (32 keys with two groups of 16 rows), the scores of a row
+// eight softmax warps share out the keys: 16 query rows and 32 keys per warp
+// and tile, four warps to a key tile (with up to 16 rows the other four take
+// the next tile, with more they take the other 16 rows), the scores of a row
 // spread over the four lanes of a quad, each warp with its own running maximum,
 // sum and output, joined once at the end of the item's run.  Keys and values
 // come straight from where the copies land: e4m3 codes are expanded in
@@ -28,8 +29,7 @@ constexpr int THIN_ROWS = 32;
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
       "{%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -63,23 +63,6 @@ __device__ __forceinline__ uint32_t expand_pair(uint32_t x, uint32_t y) {
   return bf16x2_mul((a << 4) & 0x87f087f0u, 0x7b807b80u);  // times 2^120
 }
 
-// A pair of V's values with what must not meet a zero weight taken out: keep 0 the value as it is, 1 zero
-// unless finite (reported in *bad), 2 zero.
-__device__ __forceinline__ uint32_t clean(uint32_t x, int keep_lo, int keep_hi, uint32_t bit_lo, uint32_t bit_hi,
-                                          uint32_t* bad) {
-  if (keep_lo == 2) x &= 0xffff0000u;
-  if (keep_lo == 1 && (x & 0x7f80u) == 0x7f80u) {
-    x &= 0xffff0000u;
-    *bad |= bit_lo;
-  }
-  if (keep_hi == 2) x &= 0xffffu;
-  if (keep_hi == 1 && (x & 0x7f800000u) == 0x7f800000u) {
-    x &= 0xffffu;
-    *bad |= bit_hi;
-  }
-  return x;
-}
-
 // What the roles of the kernel share with the thin form.
 struct ThinCtx {
   uint32_t sbase;
@@ -88,11 +71,11 @@ struct ThinCtx {
   int warp, lane;  // warp: 0..7 of the team
 };
 
-// One segment by the team's eight warps.  units: ring units before it; ordinal: segments before it;
+// One segment by the team's eight warps, whose query rows have landed.  units: ring units before it;
 // team_ph: phases of the TEAM barrier so far.  False when a wait gave up.
 template <int D, bool Q8>
 __device__ __forceinline__ bool thin_segment(const Args& a, const AttnArgs& g, const Seg& sg, const ThinCtx& x, int cta,
-                                             int units, int ordinal, uint32_t& team_ph) {
+                                             int units, uint32_t& team_ph) {
   using L = Layout<D, Q8>;
   constexpr int STEPS = D / 16, DQ = D / 4, QC = DQ / 8, NT = D / 8;
   const int lane = x.lane, gr = lane >> 2, q = lane & 3;
@@ -109,15 +92,23 @@ __device__ __forceinline__ bool thin_segment(const Args& a, const AttnArgs& g, c
     return ok;
   };
   const int rows = sg.ntok * g.group;
-  const int groups = rows <= 16 ? 1 : 2;  // of 16 rows
-  const int mg = x.warp & (groups - 1), slice = groups == 1 ? x.warp : x.warp >> 1;
+  // up to 16 rows: warps 0-3 and 4-7 take alternate tiles; more: all tiles, rows 0-15 and 16-31
+  const int groups = rows <= 16 ? 1 : 2;
+  const int mg = groups == 1 ? 0 : x.warp >> 2, first_tile = groups == 1 ? x.warp >> 2 : 0, step = 3 - groups;
+  const int first_key = (x.warp & 3) * 32;
   const int r0 = mg * 16 + gr, r1 = r0 + 8;
   const bool ok0 = r0 < rows, ok1 = r1 < rows;
   const int vis0 = sg.base + 1;  // keys that all rows see; row r sees those before vis0 + its token
   const int see0 = ok0 ? vis0 + r0 / g.group : 0, see1 = ok1 ? vis0 + r1 / g.group : 0;
 
+  auto landed = [&](int i) -> bool { return wait(L::LFULL + i % (2 * L::NL), (i / (2 * L::NL)) & 1); };
+  // a tile is released by the four warps that read it, or all eight
+  auto release = [&](int st) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive_n(bar(L::LEMPTY + st), step);
+  };
+
   // Q's fragments
-  if (!wait(L::QFULL, ordinal & 1)) return false;
   uint32_t qa[STEPS][4];
 #pragma unroll
   for (int c = 0; c < QC; ++c) {
@@ -135,64 +126,58 @@ __device__ __forceinline__ bool thin_segment(const Args& a, const AttnArgs& g, c
   float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
   bool bad0 = false, bad1 = false;
 
-  for (int kt = sg.t0; kt < sg.t1; ++kt) {
+  for (int kt = sg.t0 + first_tile; kt < sg.t1; kt += step) {
     const int k0 = kt * TILE, ki = 2 * (units + kt - sg.t0);
     const int ks = ki % L::NL, vs = (ki + 1) % L::NL;
     const uint32_t kbase = sbase + L::LAND_OFF + ks * L::LAND, vbase = sbase + L::LAND_OFF + vs * L::LAND;
-    const int first_key = slice * 16 * groups;
     const bool fix = k0 + TILE > min(vis0, sg.len);
-    if (!wait(L::LFULL + ks, (ki / L::NL) & 1)) return false;
-    // ---- scores of 16 keys per group of rows: two fragments of 8 keys each
+    if (!landed(ki)) return false;
+    // ---- scores of 32 keys: four fragments of 8
     float s[4][4];
 #pragma unroll
     for (int n = 0; n < 4; ++n) {
       s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
-      if (n < 2 * groups) {
-        const int kr = first_key + 8 * n + gr;
-        if (!Q8) {
+      const int kr = first_key + 8 * n + gr;
+      if (!Q8) {
 #pragma unroll
-          for (int c = 0; c < QC; ++c) {
-            const int d = DQ * q + 8 * c;
-            const uint4 v = lds128(kbase + (d >> 6) * L::PANEL + kr * 128 + ((((d & 63) >> 3) ^ (kr & 7)) << 4));
-            mma16816(s[n], qa[2 * c][0], qa[2 * c][1], qa[2 * c][2], qa[2 * c][3], v.x, v.y);
-            mma16816(s[n], qa[2 * c + 1][0], qa[2 * c + 1][1], qa[2 * c + 1][2], qa[2 * c + 1][3], v.z, v.w);
-          }
-        } else {
-#pragma unroll
-          for (int c = 0; c < D / 64; ++c) {
-            const uint32_t at = D == 128 ? kr * 128 + (((2 * q + c) ^ (kr & 7)) << 4)
-                                         : kr * 64 + ((q ^ ((kr >> 1) & 3)) << 4);
-            const uint4 v = lds128(kbase + at);
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const uint2 b = expand4(w[e], 0x7b807b80u);
-              const int st = 4 * c + e;
-              mma16816(s[n], qa[st][0], qa[st][1], qa[st][2], qa[st][3], b.x, b.y);
-            }
-          }
-          const float2 sc = lds_float2(sbase + L::SCALE_OFF + (ks * TILE + first_key + 8 * n + 2 * q) * 4);
-          s[n][0] *= sc.x, s[n][1] *= sc.y, s[n][2] *= sc.x, s[n][3] *= sc.y;
+        for (int c = 0; c < QC; ++c) {
+          const int d = DQ * q + 8 * c;
+          const uint4 v = lds128(kbase + (d >> 6) * L::PANEL + kr * 128 + ((((d & 63) >> 3) ^ (kr & 7)) << 4));
+          mma16816(s[n], qa[2 * c][0], qa[2 * c][1], qa[2 * c][2], qa[2 * c][3], v.x, v.y);
+          mma16816(s[n], qa[2 * c + 1][0], qa[2 * c + 1][1], qa[2 * c + 1][2], qa[2 * c + 1][3], v.z, v.w);
         }
+      } else {
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) {
+          const uint32_t at = D == 128 ? kr * 128 + (((2 * q + c) ^ (kr & 7)) << 4)
+                                       : kr * 64 + ((q ^ ((kr >> 1) & 3)) << 4);
+          const uint4 v = lds128(kbase + at);
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint2 b = expand4(w[e], 0x7b807b80u);
+            const int st = 4 * c + e;
+            mma16816(s[n], qa[st][0], qa[st][1], qa[st][2], qa[st][3], b.x, b.y);
+          }
+        }
+        const float2 sc = lds_float2(sbase + L::SCALE_OFF + (ks * TILE + first_key + 8 * n + 2 * q) * 4);
+        s[n][0] *= sc.x, s[n][1] *= sc.y, s[n][2] *= sc.x, s[n][3] *= sc.y;
       }
     }
-    __syncwarp();
-    if (lane == 0) ptx::mbar_arrive(bar(L::LEMPTY + ks));
+    release(ks);
     // ---- weights
-    float x0 = -INFINITY, x1 = -INFINITY;
+    if (fix) {
 #pragma unroll
-    for (int n = 0; n < 4; ++n)
-      if (n < 2 * groups) {
-        if (fix) {
-          const int p = k0 + first_key + 8 * n + 2 * q;
-          if (p >= see0) s[n][0] = -INFINITY;
-          if (p + 1 >= see0) s[n][1] = -INFINITY;
-          if (p >= see1) s[n][2] = -INFINITY;
-          if (p + 1 >= see1) s[n][3] = -INFINITY;
-        }
-        x0 = max3(x0, s[n][0], s[n][1]);
-        x1 = max3(x1, s[n][2], s[n][3]);
+      for (int n = 0; n < 4; ++n) {
+        const int p = k0 + first_key + 8 * n + 2 * q;
+        if (p >= see0) s[n][0] = -INFINITY;
+        if (p + 1 >= see0) s[n][1] = -INFINITY;
+        if (p >= see1) s[n][2] = -INFINITY;
+        if (p + 1 >= see1) s[n][3] = -INFINITY;
       }
+    }
+    float x0 = max3(max3(s[0][0], s[0][1], s[1][0]), max3(s[1][1], s[2][0], s[2][1]), fmaxf(s[3][0], s[3][1]));
+    float x1 = max3(max3(s[0][2], s[0][3], s[1][2]), max3(s[1][3], s[2][2], s[2][3]), fmaxf(s[3][2], s[3][3]));
 #pragma unroll
     for (int w = 1; w <= 2; w <<= 1) {
       x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, w));
@@ -200,7 +185,7 @@ __device__ __forceinline__ bool thin_segment(const Args& a, const AttnArgs& g, c
     }
     x0 = fmaxf(m0, x0);
     x1 = fmaxf(m1, x1);
-    if (kt == sg.t0) {
+    if (kt == sg.t0 + first_tile) {
       m0 = x0;
       m1 = x1;
     } else if (__any_sync(0xffffffffu, fmaxf(x0 - m0, x1 - m1) * g.scale_log2 > 8.f)) {
@@ -214,124 +199,108 @@ __device__ __forceinline__ bool thin_segment(const Args& a, const AttnArgs& g, c
       m1 = x1;
     }
     const float n0 = m0 == -INFINITY ? 0.f : -m0 * g.scale_log2, n1 = m1 == -INFINITY ? 0.f : -m1 * g.scale_log2;
-    if (!wait(L::LFULL + vs, ((ki + 1) / L::NL) & 1)) return false;
+    if (!landed(ki + 1)) return false;
     uint32_t p[4][2];  // weights as bf16 pairs: fragment n, row r0 / r1
 #pragma unroll
-    for (int n = 0; n < 4; ++n)
-      if (n < 2 * groups) {
-        float e0 = ex2(fmaf(s[n][0], g.scale_log2, n0)), e1 = ex2(fmaf(s[n][1], g.scale_log2, n0));
-        float e2 = ex2(fmaf(s[n][2], g.scale_log2, n1)), e3 = ex2(fmaf(s[n][3], g.scale_log2, n1));
-        l0 += e0 + e1;
-        l1 += e2 + e3;
-        if (Q8) {
-          float2 sc = lds_float2(sbase + L::SCALE_OFF + (vs * TILE + first_key + 8 * n + 2 * q) * 4);
-          e0 = e0 == 0.f ? 0.f : e0 * sc.x;  // a hidden key's scale may be anything
-          e1 = e1 == 0.f ? 0.f : e1 * sc.y;
-          e2 = e2 == 0.f ? 0.f : e2 * sc.x;
-          e3 = e3 == 0.f ? 0.f : e3 * sc.y;
-        }
-        p[n][0] = pack_bf16x2(e0, e1);
-        p[n][1] = pack_bf16x2(e2, e3);
+    for (int n = 0; n < 4; ++n) {
+      float e0 = ex2(fmaf(s[n][0], g.scale_log2, n0)), e1 = ex2(fmaf(s[n][1], g.scale_log2, n0));
+      float e2 = ex2(fmaf(s[n][2], g.scale_log2, n1)), e3 = ex2(fmaf(s[n][3], g.scale_log2, n1));
+      l0 += e0 + e1;
+      l1 += e2 + e3;
+      if (Q8) {
+        const float2 sc = lds_float2(sbase + L::SCALE_OFF + (vs * TILE + first_key + 8 * n + 2 * q) * 4);
+        e0 = e0 == 0.f ? 0.f : e0 * sc.x;  // a hidden key's scale may be anything
+        e1 = e1 == 0.f ? 0.f : e1 * sc.y;
+        e2 = e2 == 0.f ? 0.f : e2 * sc.x;
+        e3 = e3 == 0.f ? 0.f : e3 * sc.y;
       }
+      p[n][0] = pack_bf16x2(e0, e1);
+      p[n][1] = pack_bf16x2(e2, e3);
+    }
+    if (!Q8 && fix) {
+      // Values that must not reach a row through its zero weights (0 x NaN) are replaced by zeros in
+      // this warp's 32 rows: those past the sequence's end, and those that some row does not see yet
+      // and that are not finite (rows that do see one take note).  An e4m3 code is always finite.
+      constexpr int LANES = D / 8, RPI = 32 / LANES;  // 16-byte pieces of a row, rows at a time
+      const int piece = lane % LANES;
+#pragma unroll 1
+      for (int rb = max(0, min(vis0, sg.len) - k0 - first_key) / RPI * RPI; rb < 32; rb += RPI) {
+        const int rr = rb + lane / LANES, key = k0 + first_key + rr;
+        const uint32_t at = vbase + (piece >> 3) * L::PANEL + (first_key + rr) * 128 + (((piece & 7) ^ (rr & 7)) << 4);
+        bool wipe = key >= sg.len;
+        if (!wipe && key >= vis0) {
+          const uint4 v = lds128(at);
+          uint32_t acc = ptx::bf16x2_fma(v.x, 0u, 0u);
+          acc = ptx::bf16x2_fma(v.y, 0u, acc);
+          acc = ptx::bf16x2_fma(v.z, 0u, acc);
+          acc = ptx::bf16x2_fma(v.w, 0u, acc);
+          wipe = (acc & 0x7fff7fffu) != 0;  // 0 x Inf, 0 x NaN: NaN
+        }
+        const uint32_t hit = __ballot_sync(0xffffffffu, wipe);
+        if (hit >> (lane / LANES * LANES) & ((1u << LANES) - 1u)) sts128(at, make_uint4(0, 0, 0, 0));
+#pragma unroll
+        for (int h = 0; h < RPI; ++h) {
+          const int other = k0 + first_key + rb + h;
+          if (other < sg.len && (hit >> (h * LANES) & ((1u << LANES) - 1u))) {
+            bad0 |= other < see0;
+            bad1 |= other < see1;
+          }
+        }
+      }
+      ptx::fence_proxy_async_smem();  // the copies overwrite what was written here
+      __syncwarp();
+    }
     // ---- O += P V
 #pragma unroll
-    for (int n = 0; n < 4; n += 2)
-      if (n < 2 * groups) {
-        const int kb = first_key + 8 * n;
-        if (!Q8) {
-          uint32_t badkeys = 0;
-          const int kp = k0 + kb + 2 * q;  // this lane's keys of a fragment: kp, kp + 1, kp + 8, kp + 9
-          int keep[4];
+    for (int n = 0; n < 4; n += 2) {
+      const int kb = first_key + 8 * n;
+      if (!Q8) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int key = kp + (i & 1) + (i >> 1) * 8;
-            keep[i] = key >= sg.len ? 2 : key >= vis0 ? 1 : 0;
-          }
+        for (int j = 0; j < D / 16; ++j) {
+          const int row = kb + ((lane >> 3) & 1) * 8 + (lane & 7), ch = 2 * j + (lane >> 4);
+          uint32_t v[4];
+          ldmatrix_x4_trans(vbase + (ch >> 3) * L::PANEL + row * 128 + (((ch & 7) ^ (row & 7)) << 4), v);
+          mma16816(o[2 * j], p[n][0], p[n][1], p[n + 1][0], p[n + 1][1], v[0], v[1]);
+          mma16816(o[2 * j + 1], p[n][0], p[n][1], p[n + 1][0], p[n + 1][1], v[2], v[3]);
+        }
+      } else {
+        uint32_t v[4][D / 32];
 #pragma unroll
-          for (int j = 0; j < D / 16; ++j) {
-            const int row = kb + ((lane >> 3) & 1) * 8 + (lane & 7), ch = 2 * j + (lane >> 4);
-            uint32_t v[4];
-            ldmatrix_x4_trans(vbase + (ch >> 3) * L::PANEL + row * 128 + (((ch & 7) ^ (row & 7)) << 4), v);
-            if (fix) {
-              v[0] = clean(v[0], keep[0], keep[1], 1u << (2 * q), 2u << (2 * q), &badkeys);
-              v[1] = clean(v[1], keep[2], keep[3], 256u << (2 * q), 512u << (2 * q), &badkeys);
-              v[2] = clean(v[2], keep[0], keep[1], 1u << (2 * q), 2u << (2 * q), &badkeys);
-              v[3] = clean(v[3], keep[2], keep[3], 256u << (2 * q), 512u << (2 * q), &badkeys);
-            }
-            mma16816(o[2 * j], p[n][0], p[n][1], p[n + 1][0], p[n + 1][1], v[0], v[1]);
-            mma16816(o[2 * j + 1], p[n][0], p[n][1], p[n + 1][0], p[n + 1][1], v[2], v[3]);
-          }
-          if (fix) {
-            badkeys = __reduce_or_sync(0xffffffffu, badkeys);
-            const int c0 = see0 - (k0 + kb), c1 = see1 - (k0 + kb);  // the row sees keys before this
-            bad0 |= (badkeys & (c0 >= 16 ? 0xffffu : c0 <= 0 ? 0u : (1u << c0) - 1u)) != 0;
-            bad1 |= (badkeys & (c1 >= 16 ? 0xffffu : c1 <= 0 ? 0u : (1u << c1) - 1u)) != 0;
-          }
-        } else {
-          uint32_t v[4][D / 32];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int row = kb + 2 * q + (i & 1) + (i >> 1) * 8;
-            if (D == 128) {
-              const uint4 w = lds128(vbase + row * 128 + ((gr ^ (row & 7)) << 4));
-              v[i][0] = w.x, v[i][1] = w.y, v[i][D / 32 - 2] = w.z, v[i][D / 32 - 1] = w.w;
-            } else {
-              const uint2 w = lds64(vbase + row * 64 + (((gr >> 1) ^ ((row >> 1) & 3)) << 4) + (gr & 1) * 8);
-              v[i][0] = w.x, v[i][1] = w.y;
-            }
-          }
-#pragma unroll
-          for (int w = 0; w < D / 32; ++w) {
-            mma16816(o[4 * w], p[n][0], p[n][1], p[n + 1][0], p[n + 1][1], expand_pair<0>(v[0][w], v[1][w]),
-                     expand_pair<0>(v[2][w], v[3][w]));
-            mma16816(o[4 * w + 1], p[n][0], p[n][1], p[n + 1][0], p[n + 1][1], expand_pair<1>(v[0][w], v[1][w]),
-                     expand_pair<1>(v[2][w], v[3][w]));
-            mma16816(o[4 * w + 2], p[n][0], p[n][1], p[n + 1][0], p[n + 1][1], expand_pair<2>(v[0][w], v[1][w]),
-                     expand_pair<2>(v[2][w], v[3][w]));
-            mma16816(o[4 * w + 3], p[n][0], p[n][1], p[n + 1][0], p[n + 1][1], expand_pair<3>(v[0][w], v[1][w]),
-                     expand_pair<3>(v[2][w], v[3][w]));
+        for (int i = 0; i < 4; ++i) {
+          const int row = kb + 2 * q + (i & 1) + (i >> 1) * 8;
+          if (D == 128) {
+            const uint4 w = lds128(vbase + row * 128 + ((gr ^ (row & 7)) << 4));
+            v[i][0] = w.x, v[i][1] = w.y, v[i][D / 32 - 2] = w.z, v[i][D / 32 - 1] = w.w;
+          } else {
+            const uint2 w = lds64(vbase + row * 64 + (((gr >> 1) ^ ((row >> 1) & 3)) << 4) + (gr & 1) * 8);
+            v[i][0] = w.x, v[i][1] = w.y;
           }
         }
+#pragma unroll
+        for (int w = 0; w < D / 32; ++w) {
+          mma16816(o[4 * w], p[n][0], p[n][1], p[n + 1][0], p[n + 1][1], expand_pair<0>(v[0][w], v[1][w]),
+                   expand_pair<0>(v[2][w], v[3][w]));
+          mma16816(o[4 * w + 1], p[n][0], p[n][1], p[n + 1][0], p[n + 1][1], expand_pair<1>(v[0][w], v[1][w]),
+                   expand_pair<1>(v[2][w], v[3][w]));
+          mma16816(o[4 * w + 2], p[n][0], p[n][1], p[n + 1][0], p[n + 1][1], expand_pair<2>(v[0][w], v[1][w]),
+                   expand_pair<2>(v[2][w], v[3][w]));
+          mma16816(o[4 * w + 3], p[n][0], p[n][1], p[n + 1][0], p[n + 1][1], expand_pair<3>(v[0][w], v[1][w]),
+                   expand_pair<3>(v[2][w], v[3][w]));
+        }
       }
-    __syncwarp();
-    if (lane == 0) ptx::mbar_arrive(bar(L::LEMPTY + vs));
+    }
+    release(vs);
   }
 #pragma unroll
   for (int w = 1; w <= 2; w <<= 1) {
     l0 += __shfl_xor_sync(0xffffffffu, l0, w);
     l1 += __shfl_xor_sync(0xffffffffu, l1, w);
   }
-  // ---- the warps' results joined: maxima and sums first, then the outputs, brought to the common maximum,
-  // by way of the query tile's memory (four regions of 16 rows: warps 4-7 write, 0-3 add their own)
+  // ---- the warps' results joined by way of the query tiles' memory, a region of 16 rows per warp
   float* s_m = reinterpret_cast<float*>(x.smem + L::ML_OFF);
   float* s_l = s_m + 128;
-  float* s_b = s_m + 256;
+  uint8_t* s_b = x.smem + L::ML_OFF + 8 * TILE;
   float* region = reinterpret_cast<float*>(x.smem + L::Q_OFF);
-  if (q == 0) {
-    s_m[x.warp * 16 + gr] = m0 == -INFINITY ? m0 : m0 * g.scale_log2;
-    s_m[x.warp * 16 + gr + 8] = m1 == -INFINITY ? m1 : m1 * g.scale_log2;
-    s_l[x.warp * 16 + gr] = l0;
-    s_l[x.warp * 16 + gr + 8] = l1;
-    s_b[x.warp * 16 + gr] = bad0 ? 1.f : 0.f;
-    s_b[x.warp * 16 + gr + 8] = bad1 ? 1.f : 0.f;
-  }
-  if (!team()) return false;
-  float top0 = -INFINITY, top1 = -INFINITY, sum0 = 0.f, sum1 = 0.f, flag0 = 0.f, flag1 = 0.f;
-  for (int w = mg; w < 8; w += groups) {
-    top0 = fmaxf(top0, s_m[w * 16 + gr]);
-    top1 = fmaxf(top1, s_m[w * 16 + gr + 8]);
-  }
-  const float t0 = top0 == -INFINITY ? 0.f : top0, t1 = top1 == -INFINITY ? 0.f : top1;
-  for (int w = mg; w < 8; w += groups) {
-    sum0 = fmaf(s_l[w * 16 + gr], ex2(s_m[w * 16 + gr] - t0), sum0);
-    sum1 = fmaf(s_l[w * 16 + gr + 8], ex2(s_m[w * 16 + gr + 8] - t1), sum1);
-    flag0 = fmaxf(flag0, s_b[w * 16 + gr]);
-    flag1 = fmaxf(flag1, s_b[w * 16 + gr + 8]);
-  }
-  const float f0 = ex2(s_m[x.warp * 16 + gr] - t0), f1 = ex2(s_m[x.warp * 16 + gr + 8] - t1);
-#pragma unroll
-  for (int j = 0; j < NT; ++j) o[j][0] *= f0, o[j][1] *= f0, o[j][2] *= f1, o[j][3] *= f1;
-  float* mine = region + (x.warp & 3) * 16 * D;
   // column of o[j][0]: bf16 fragments are natural, e4m3's column 2q of step j is d = j + (D/8) 2q; its
   // place in the region is swizzled so that a warp's 32 stores go to 32 banks
   auto place = [](int row, int col) {
@@ -340,41 +309,55 @@ __device__ __forceinline__ bool thin_segment(const Args& a, const AttnArgs& g, c
   auto at = [&](int j, int e) {
     return place(gr + (e >> 1) * 8, Q8 ? j + NT * (2 * q + (e & 1)) : 8 * j + 2 * q + (e & 1));
   };
-  if (x.warp >= 4) {
-#pragma unroll
-    for (int j = 0; j < NT; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) mine[at(j, e)] = o[j][e];
-  }
+  // every warp has read its query rows (the first barrier), then their memory is written (the second)
   if (!team()) return false;
-  if (x.warp < 4) {
+  float* mine = region + x.warp * 16 * D;
 #pragma unroll
-    for (int j = 0; j < NT; ++j)
+  for (int j = 0; j < NT; ++j) {
+    mine[at(j, 0)] = o[j][0];
+    mine[at(j, 1)] = o[j][1];
+  }
+  if (rows > 8) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) mine[at(j, e)] += o[j][e];
-    if (x.warp < groups && q == 0) {
-      s_m[mg * 16 + gr] = top0, s_m[mg * 16 + gr + 8] = top1;
-      s_l[mg * 16 + gr] = sum0, s_l[mg * 16 + gr + 8] = sum1;
-      s_b[mg * 16 + gr] = flag0, s_b[mg * 16 + gr + 8] = flag1;
+    for (int j = 0; j < NT; ++j) {
+      mine[at(j, 2)] = o[j][2];
+      mine[at(j, 3)] = o[j][3];
     }
+  }
+  if (q == 0) {
+    s_m[x.warp * 16 + gr] = m0 == -INFINITY ? m0 : m0 * g.scale_log2;
+    s_m[x.warp * 16 + gr + 8] = m1 == -INFINITY ? m1 : m1 * g.scale_log2;
+    s_l[x.warp * 16 + gr] = l0;
+    s_l[x.warp * 16 + gr + 8] = l1;
+    s_b[x.warp * 16 + gr] = bad0;
+    s_b[x.warp * 16 + gr + 8] = bad1;
   }
   if (!team()) return false;
   const bool whole = sg.t0 == 0 && sg.t1 == sg.nt;
   float* slot = g.part + (2ll * cta + (sg.t0 == 0 ? 1 : 0)) * slot_floats<D>();
   // lanes: columns 2 lane, 2 lane + 1 and (D = 128) those 64 further
   for (int r = x.warp; r < rows; r += 8) {
+    const int w0 = r >> 4 << 2, n = groups == 1 ? 8 : 4;  // the warps that have this row
+    float ml = -INFINITY, l = 0.f;
+    bool bad = false;
+    for (int w = w0; w < w0 + n; ++w) ml = fmaxf(ml, s_m[w * 16 + (r & 15)]);
+    const float top = ml == -INFINITY ? 0.f : ml;
     float2 y[NT / 8];
 #pragma unroll
     for (int j = 0; j < NT / 8; ++j) y[j] = make_float2(0.f, 0.f);
-    for (int w = r >> 4; w < 4; w += groups)
+#pragma unroll 4
+    for (int w = w0; w < w0 + n; ++w) {
+      const float f = ex2(s_m[w * 16 + (r & 15)] - top);
+      l = fmaf(s_l[w * 16 + (r & 15)], f, l);
+      bad |= s_b[w * 16 + (r & 15)] != 0;
 #pragma unroll
       for (int j = 0; j < NT / 8; ++j) {
-        y[j].x += region[w * 16 * D + place(r & 15, 64 * j + 2 * lane)];
-        y[j].y += region[w * 16 * D + place(r & 15, 64 * j + 2 * lane + 1)];
+        y[j].x = fmaf(region[w * 16 * D + place(r & 15, 64 * j + 2 * lane)], f, y[j].x);
+        y[j].y = fmaf(region[w * 16 * D + place(r & 15, 64 * j + 2 * lane + 1)], f, y[j].y);
       }
-    const float ml = s_m[r], l = s_l[r];
+    }
     const int tok = r / g.group;
-    if (!Q8 && s_b[r] != 0.f) {
+    if (!Q8 && bad) {
       // values that are not finite and that this row sees enter the sums as they are
       for (int p = max(vis0, sg.t0 * TILE); p < min(vis0 + tok, sg.t1 * TILE); ++p) {
         const int page = find_page(a, sg.b, p);
@@ -406,7 +389,10 @@ __device__ __forceinline__ bool thin_segment(const Args& a, const AttnArgs& g, c
     }
   }
   __syncwarp();
-  if (lane == 0) ptx::mbar_arrive(bar(L::QEMPTY));
+  if (lane == 0) {
+    ptx::mbar_arrive(bar(L::QEMPTY));
+    ptx::mbar_arrive(bar(L::QEMPTY + 1));
+  }
   return true;
 }
 

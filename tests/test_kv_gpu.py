@@ -142,6 +142,31 @@ def test_attention(q_lens, kv_lens, heads, g, d, page, fmt):
 
 
 @pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("d,page", [(128, 32), (64, 16)])
+@pytest.mark.parametrize("kind", ["decode", "decode short", "mixed"])
+def test_attention_many_sequences(kind, d, page, fmt):
+    """More sequences than a warp has lanes and many items per CTA, of one token or of all sizes in turn: what
+    one item leaves behind in the CTA must not reach the next.  Several runs, since it would be a matter of time."""
+    import torch
+    r = np.random.default_rng(d + len(kind))
+    if kind == "decode":
+        q, kv, heads, g = [1] * 40, r.integers(1, 3000, 40).tolist(), 4, 2
+    elif kind == "decode short":
+        q, kv, heads, g = [1] * 150, r.integers(1, 300, 150).tolist(), 8, 1
+    else:
+        q = r.choice([0, 1, 1, 2, 5, 8, 9, 17, 40, 130], 60).tolist()
+        kv, heads, g = [int(n + r.integers(0, 400)) for n in q], 4, 4
+    s = K.Setup(q, kv, heads=heads, g=g, d=d, page=page, fmt=fmt, seed=31)
+    out, lse = s.cache.attention(s.q, s.batch, return_lse=True)
+    _ok()
+    K.check(s, out, lse, what=kind)
+    for _ in range(10):
+        again = s.cache.attention(s.q, s.batch, return_lse=True)
+    _ok()
+    assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
 @pytest.mark.parametrize("scale,sigma", [(1.0, 1.0), (0.02, 4.0), (3.0, 2.0)])
 def test_attention_scales(scale, sigma, fmt):
     """Flat and nearly one-hot softmax: the running maximum moves a lot or not at all."""
