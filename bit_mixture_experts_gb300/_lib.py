@@ -135,9 +135,12 @@ def _ptr(t):
 
 
 def _stream(stream=None):
-    import torch
-    s = torch.cuda.current_stream() if stream is None else stream
-    return s.cuda_stream
+    """The raw handle of a torch stream, of the current one for None; a raw handle as it is."""
+    if stream is None:
+        import torch
+        # torch.cuda.current_stream().cuda_stream without the Stream object (3 us of host time a call)
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 # --------------------------------------------------------------------------- #
@@ -292,10 +295,12 @@ def moe_kv_attention_workspace_size(d) -> int:
 
 
 def moe_kv_attention(q, scale, cache: KVCache, batch: KVBatch, out, lse, workspace, stream=None):
-    """Causal attention of q (bf16 [T, q_heads, d], any token and head strides) over the cache."""
-    qs = q.stride()
-    _call("moe_kv_attention", q.data_ptr(), qs[0], qs[1], q.shape[1], scale, cache, batch, out.data_ptr(), _ptr(lse),
-          _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream))
+    """Causal attention of q (bf16 [T, q_heads, d], any token and head strides) over the cache; workspace: a
+    tensor or (pointer, bytes)."""
+    token, head, _ = q.stride()
+    ws, n = workspace if isinstance(workspace, tuple) else (workspace.data_ptr(), workspace.nbytes)
+    _call("moe_kv_attention", q.data_ptr(), token, head, q.shape[1], scale, cache, batch, out.data_ptr(), _ptr(lse), ws,
+          n, _stream(stream))
 
 
 def moe_set_wait_limit_ns(ns: int) -> None:

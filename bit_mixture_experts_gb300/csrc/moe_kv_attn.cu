@@ -56,37 +56,17 @@ __global__ void __launch_bounds__(Layout<D, Q8>::THREADS, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int cta = static_cast<int>(blockIdx.x);
 
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < 2 * L::NL; ++i) ptx::mbar_init(bar(L::LFULL + i), 1);
-    for (int i = 0; i < L::NL; ++i) ptx::mbar_init(bar(L::LEMPTY + i), L::LEMPTY_COUNT);
-    if (Q8)
-      for (int i = 0; i < NS; ++i) {
-        ptx::mbar_init(bar(L::FULL + i), 4);
-        ptx::mbar_init(bar(L::EMPTY + i), 1);
-      }
-    for (int t = 0; t < 2; ++t) {
-      ptx::mbar_init(bar(L::SFULL + t), 1);
-      ptx::mbar_init(bar(L::PREADY + t), 4);
-      ptx::mbar_init(bar(L::QFULL + t), 1);
-      ptx::mbar_init(bar(L::QEMPTY + t), t == 0 ? 9 : 8);
-      ptx::mbar_init(bar(L::OFULL + t), 1);
-      ptx::mbar_init(bar(L::FIX + t), 4);
-    }
-    ptx::mbar_init(bar(L::ML), 4);
-    ptx::mbar_init(bar(L::OBFREE), 4);
-    ptx::mbar_init(bar(L::TEAM), 8);
-    for (int i = 0; i < SEGS; ++i) {
-      ptx::mbar_init(bar(L::SEGF + i), 1);
-      ptx::mbar_init(bar(L::SEGE + i), L::THREADS / 32 - 1);
-    }
-    ptx::mbar_init(bar(L::DRAIN), 1);
-    *s_abort = 0;
+  if (warp == 0) {
+    for (int i = lane; i < L::NBAR; i += 32) ptx::mbar_init(bar(i), L::arrivals(i));
+    if (lane == 0) *s_abort = 0;
     ptx::fence_mbar_init();
   }
   if (warp == 1) {
     ptx::tmem_alloc(ptx::smem_u32(s_tmem), 512);
     ptx::tmem_relinquish();
   }
+  // the kernel may start while the one before it in the stream ends: nothing is read before it has
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   // this CTA's share of the units (the scan's scratch lies where the key/value ring will be)
   kv::Share share;
   kv::Start from;
@@ -117,7 +97,8 @@ __global__ void __launch_bounds__(Layout<D, Q8>::THREADS, 1)
     if (!wait(L::SEGF + slot, (segs / SEGS) & 1)) return false;
     const int4* p = reinterpret_cast<const int4*>(smem + L::SEG_OFF + slot * 48);
     const int4 x = p[0], y = p[1], z = p[2];
-    sg = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w, z.x, z.y};
+    sg = {uniform(x.x), uniform(x.y), uniform(x.z), uniform(x.w), uniform(y.x),
+          uniform(y.y), uniform(y.z), uniform(y.w), uniform(z.x), uniform(z.y)};
     __syncwarp();
     if (lane == 0) ptx::mbar_arrive(bar(L::SEGE + slot));
     ++segs;
@@ -130,73 +111,90 @@ __global__ void __launch_bounds__(Layout<D, Q8>::THREADS, 1)
     if (warp == 0) {
       // ---------------------------------------------- copies: K and V of every key tile, in that order
       const int per_page = a.page_size / g.chunk, per_tile = TILE / g.chunk;
-      int n = 0, st = 0, ph = 0;  // tiles issued; ring slot and its round's parity
+      // per ring (tile form, thin form): tiles issued, next slot, its round's parity, landing barrier
+      struct Ring {
+        int n, st, ph, fl;
+      } tile_ring = {0, 0, 0, 0}, thin_ring = {0, 0, 0, 0};
       bool ok = true;
+      int form = -1;  // the last segment's
+      uint32_t tc_ph = 0;
       while (ok && next(sg)) {
+        const int now = Q8 && thin(sg) ? 1 : 0;
+        if (Q8 && form >= 0 && now != form) {
+          // the rings share memory
+          if (now == 1) {
+            ok = wait(L::TCDONE, tc_ph);
+            tc_ph ^= 1;
+          } else {
+            const int n = thin_ring.n;
+            for (int i = max(0, n - L::NH_); ok && i < n; ++i) ok = wait(L::HEMPTY + i % L::NH_, (i / L::NH_) & 1);
+          }
+          if (!ok) break;
+        }
+        form = now;
+        Ring rg = now ? thin_ring : tile_ring;
+        const int slots = now ? L::NH_ : L::NL, full0 = now ? L::HFULL : L::LFULL, empty0 = now ? L::HEMPTY : L::LEMPTY;
+        const uint32_t ring0 = sbase + (now ? L::H_OFF : L::L_OFF);
         const int32_t* table = a.page_table + static_cast<size_t>(sg.b) * a.table_width;
         const int last = ceil_div(sg.len, g.chunk);  // chunks of the sequence
         int c0 = sg.t0 * per_tile;
-        // page ids of chunks c0 .. c0 + 31 and the 32 after them, one per lane
-        int ids = c0 + lane < last ? __ldg(table + (c0 + lane) / per_page) : 0;
-        int ids2 = c0 + 32 + lane < last ? __ldg(table + (c0 + 32 + lane) / per_page) : 0;
+        // the pool's rows where chunks c0 .. c0 + 31 start, and the 32 after them, one per lane
+        auto rows_of = [&](int c) -> int {
+          if (c >= last) return 0;
+          const int e = c / per_page;
+          int page = __ldg(table + e);
+          if (page < 0 || page >= a.num_pages) {
+            set_device_error(a.err, MOE_DEV_BAD_INDEX);
+            page = 0;
+          }
+          return (page * a.heads + sg.h) * a.page_size + (c - e * per_page) * g.chunk;
+        };
+        int rows = rows_of(c0 + lane), rows2 = rows_of(c0 + 32 + lane);
         for (int kt = sg.t0; ok && kt < sg.t1; ++kt) {
           const int c = kt * per_tile;
           if (c - c0 >= 32) {
             c0 += 32;
-            ids = ids2;
-            ids2 = c0 + 32 + lane < last ? __ldg(table + (c0 + 32 + lane) / per_page) : 0;
+            rows = rows2;
+            rows2 = rows_of(c0 + 32 + lane);
           }
           const int have = max(0, min(per_tile, last - c));
-          if (Q8) {
-            // the ring holds less than what is on its way from memory at full speed: ask for the tiles
-            // after it, so that it fills from the L2 cache
-            const int cp = c + AHEAD * per_tile + (lane >> 1) - c0;
-            const int near = __shfl_sync(0xffffffffu, ids, cp & 31), next32 = __shfl_sync(0xffffffffu, ids2, cp & 31);
-            const int far = cp < 32 ? near : next32;
-            if ((lane >> 1) < per_tile && kt + AHEAD < sg.t1 && c0 + cp < last && far >= 0 && far < a.num_pages) {
-              const size_t row = (static_cast<size_t>(far) * a.heads + sg.h) * a.page_size + (c0 + cp) % per_page * g.chunk;
-              prefetch_l2(static_cast<const uint8_t*>(lane & 1 ? a.v : a.k) + row * D, g.chunk * D);
-            }
-          }
-          int page = ids;
-          if (page < 0 || page >= a.num_pages) {
-            if (c0 + lane < last) set_device_error(a.err, MOE_DEV_BAD_INDEX);
-            page = 0;
-          }
 #pragma unroll 1
           for (int kind = 0; kind < 2; ++kind) {
-            if (n >= L::NL && !wait(L::LEMPTY + st, ph ^ 1)) {
+            if (rg.n >= slots && !wait(empty0 + rg.st, rg.ph ^ 1)) {
               ok = false;
               break;
             }
-            const uint32_t f = bar(L::LFULL + n % (2 * L::NL)), dst = sbase + L::LAND_OFF + st * L::LAND;
+            const uint32_t f = bar(full0 + rg.fl), dst = ring0 + rg.st * L::LAND;
             const CUtensorMap* map = kind ? &tmap_v : &tmap_k;
             const float* scale = kind ? a.v_scale : a.k_scale;
             ptx::mbar_arrive_expect_tx_elect(f, static_cast<uint32_t>(have * g.chunk * (Q8 ? D + 4 : 2 * D)));
 #pragma unroll 1
             for (int j = 0; j < have; ++j) {
-              const int pg = __shfl_sync(0xffffffffu, page, c - c0 + j);
-              const int row = (pg * a.heads + sg.h) * a.page_size + (c + j) % per_page * g.chunk;
+              const int row = uniform(lane == c - c0 + j ? rows : 0);
               if (!Q8) {
 #pragma unroll
                 for (int hf = 0; hf < NH; ++hf)
                   ptx::tma_load_2d_elect(dst + hf * PANEL + j * g.chunk * 128, map, hf * 64, row, f);
               } else {
                 ptx::tma_load_2d_elect(dst + j * g.chunk * D, map, 0, row, f);
-                ptx::bulk_g2s_elect(sbase + L::SCALE_OFF + (st * TILE + j * g.chunk) * 4, scale + row, g.chunk * 4, f);
+                ptx::bulk_g2s_elect(sbase + L::SCALE_OFF + (rg.st * TILE + j * g.chunk) * 4, scale + row, g.chunk * 4, f);
               }
             }
-            ++n;
-            if (++st == L::NL) {
-              st = 0;
-              ph ^= 1;
+            ++rg.n;
+            if (++rg.fl == 2 * slots) rg.fl = 0;
+            if (++rg.st == slots) {
+              rg.st = 0;
+              rg.ph ^= 1;
             }
           }
         }
+        (now ? thin_ring : tile_ring) = rg;
       }
       // every copy issued has landed before the CTA ends (at once unless a wait gave up)
-      for (int i = n > L::NL ? n - L::NL : 0; i < n; ++i)
+      for (int i = max(0, tile_ring.n - L::NL); i < tile_ring.n; ++i)
         tc_dev::wait_drain(bar(L::LFULL + i % (2 * L::NL)), (i / (2 * L::NL)) & 1, 0);
+      for (int i = max(0, thin_ring.n - L::NH_); i < thin_ring.n; ++i)
+        tc_dev::wait_drain(bar(L::HFULL + i % (2 * L::NH_)), (i / (2 * L::NH_)) & 1, 0);
     } else if (warp == 1) {
       // ---------------------------------------------- MMA issue, one unit behind for P V
       // A unit's tiles: a and b (a pair), or one of them (t alternates along the keys).
@@ -213,7 +211,7 @@ __global__ void __launch_bounds__(Layout<D, Q8>::THREADS, 1)
       // releases a ring tile once the MMAs issued so far are done with it
       auto release = [&](int i) {
         const uint32_t b = bar((Q8 ? L::EMPTY : L::LEMPTY) + i % NS);
-        if (!Q8 && lane == 0) mbar_arrive_n(b, L::LEMPTY_COUNT - 1);
+        if (!Q8 && lane == 0) mbar_arrive_n(b, 7);
         ptx::mma_commit_elect(b);
       };
       // O += P V of the previous unit for tile t
@@ -245,15 +243,18 @@ __global__ void __launch_bounds__(Layout<D, Q8>::THREADS, 1)
           ptx::mma_commit_elect(bar(L::QEMPTY + q));
         }
       };
-      bool ok = true;
+      bool ok = true, tiles_before = false;  // tiles_before: the last segment was of the tile form
       while (ok && next(sg)) {
         if (thin(sg)) {
           // the softmax warps' own; its tiles pass by, and what is pending must not wait for it
           ok = finish(0) && finish(1) && wait(L::QFULL, (segs - 1) & 1);
           if (ok && lane == 0) ptx::mbar_arrive(bar(L::QEMPTY));
+          if (Q8 && tiles_before) ptx::mma_commit_elect(bar(L::TCDONE));
+          tiles_before = false;
           if (!Q8) ki += 2 * (sg.t1 - sg.t0);
           continue;
         }
+        tiles_before = true;
         const bool pair = sg.ntok > g.tpt;
         for (int kt = sg.t0; kt < sg.t1; ++kt) {
           const int j = kt - sg.t0;
@@ -356,7 +357,7 @@ __global__ void __launch_bounds__(Layout<D, Q8>::THREADS, 1)
     const uint32_t ts = tmem + lanes + TM_S + t * TILE, to = tmem + lanes + TM_O + t * D;
     float* s_ml = reinterpret_cast<float*>(smem + L::ML_OFF);
     uint32_t s_ph = 0, o_ph[2] = {0, 0}, x_ph = 0;
-    int all = 0, n = 0;  // units before the current segment: in all, and of tiles
+    int all = 0, n = 0;  // units before the current segment: in all, and of the tile form
     uint32_t team_ph = 0;
     bool ok = true, lent = false;  // lent: O b (and its rows' sums) are being read by tile a's threads
     while (ok && next(sg)) {
@@ -371,7 +372,7 @@ __global__ void __launch_bounds__(Layout<D, Q8>::THREADS, 1)
           lent = false;
         }
         const ThinCtx ctx = {sbase, smem, s_abort, warp - 4, lane};
-        ok = thin_segment<D, Q8>(a, g, sg, ctx, cta, all, team_ph);
+        ok = thin_segment<D, Q8>(a, g, sg, ctx, cta, Q8 ? all - n : all, team_ph);
         all += run;
         continue;
       }
@@ -624,33 +625,27 @@ __global__ void __launch_bounds__(Layout<D, Q8>::THREADS, 1)
     reg_dec<L::REGS_OTHER>();
     const int tid = threadIdx.x - 384;
     constexpr int C = D / 16;  // 16-byte chunks of a row of codes
-    int n = 0, m = 0;          // tiles landed, tiles expanded
+    int n = 0;                 // tiles so far
     bool ok = true;
     while (ok && next(sg)) {
-      const bool pass = thin(sg);
+      if (thin(sg)) continue;
       for (int x = 0; ok && x < 2 * (sg.t1 - sg.t0); ++x, ++n) {
-        const int rs = n % L::NL, ts = m % NS;
+        const int rs = n % L::NL, ts = n % NS;
         ok = wait(L::LFULL + n % (2 * L::NL), (n / (2 * L::NL)) & 1);
         if (!ok) break;
-        if (pass) {
-          if (lane == 0) ptx::mbar_arrive(bar(L::LEMPTY + rs));
-          continue;
-        }
         // one row per thread; the swizzles keep eight neighbouring threads' loads and stores in
         // different banks
-        const uint32_t src = sbase + L::LAND_OFF + rs * L::LAND + tid * D, dst = sbase + L::KV_OFF + ts * TB + tid * 128;
+        const uint32_t src = sbase + L::L_OFF + rs * L::LAND + tid * D, dst = sbase + L::KV_OFF + ts * TB + tid * 128;
         uint4 codes[C];
 #pragma unroll
         for (int c = 0; c < C; ++c) codes[c] = lds128(src + ((c ^ (D == 128 ? tid & 7 : (tid >> 1) & 3)) << 4));
-        uint32_t sc;
-        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(sc) : "r"(sbase + L::SCALE_OFF + (rs * TILE + tid) * 4) : "memory");
-        // 2^120 times the scale as two bf16 powers of two (scale: exponent 1..247, or NaN)
-        const int e = static_cast<int>(sc >> 23) + 120;
-        const uint32_t lo = min(e, 254), hi = e - lo + 127;
-        const uint32_t s1 = (sc > 0x7f800000u ? 0x7fffu : lo << 7) * 0x10001u, s2 = (hi << 7) * 0x10001u;
-        const bool twice = __any_sync(0xffffffffu, hi != 127);  // scales of 2^8 and more
-        if (m >= NS) {
-          ok = wait(L::EMPTY + ts, (m / NS - 1) & 1);
+        float sc;
+        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(sc) : "r"(sbase + L::SCALE_OFF + (rs * TILE + tid) * 4) : "memory");
+        uint32_t s1, s2;
+        scale_pairs(sc, &s1, &s2);
+        const bool twice = __any_sync(0xffffffffu, s2 != 0x3f803f80u);
+        if (n >= NS) {
+          ok = wait(L::EMPTY + ts, (n / NS - 1) & 1);
           if (!ok) break;
         }
 #pragma unroll
@@ -669,10 +664,9 @@ __global__ void __launch_bounds__(Layout<D, Q8>::THREADS, 1)
         ptx::fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive_n(bar(L::LEMPTY + rs), 3);
+          ptx::mbar_arrive(bar(L::LEMPTY + rs));
           ptx::mbar_arrive(bar(L::FULL + ts));
         }
-        ++m;
       }
     }
   }
@@ -814,20 +808,24 @@ cudaError_t launch(const kv::Args& a, const AttnArgs& g, const CUtensorMap& tk, 
   using L = Layout<D, Q8>;
   cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void*>(kv_attention_kernel<D, Q8>), L::BYTES);
   if (e != cudaSuccess) return e;
-  kv_attention_kernel<D, Q8><<<ctas, L::THREADS, L::BYTES, s>>>(a, g, tk, tv);
-  note_launches(1);
-  e = cudaGetLastError();
-  // items of up to WHOLE key tiles are never cut
-  if (e != cudaSuccess || static_cast<long long>(a.table_width) * a.page_size <= WHOLE * TILE) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas - 1, min(static_cast<long long>(a.T) * g.group, static_cast<long long>(MERGE_Y)));
-  cfg.blockDim = dim3(32 * MERGE_WARPS);
-  cfg.stream = s;
+  // each kernel may start while the one before it in the stream ends, and waits for its results itself
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(L::THREADS);
+  cfg.dynamicSmemBytes = L::BYTES;
+  cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, kv_attention_kernel<D, Q8>, a, g, tk, tv);
+  note_launches(1);
+  // items of up to WHOLE key tiles are never cut
+  if (e != cudaSuccess || static_cast<long long>(a.table_width) * a.page_size <= WHOLE * TILE) return e;
+  cfg.gridDim = dim3(ctas - 1, min(static_cast<long long>(a.T) * g.group, static_cast<long long>(MERGE_Y)));
+  cfg.blockDim = dim3(32 * MERGE_WARPS);
+  cfg.dynamicSmemBytes = 0;
   e = cudaLaunchKernelEx(&cfg, kv_merge_kernel<D>, a, g, ctas);
   note_launches(1);
   return e;

@@ -30,38 +30,57 @@ constexpr int SEGS = 4;  // work segments published ahead
 
 template <int D, bool Q8>
 struct Layout {
+  static constexpr int THREADS = Q8 ? 512 : 384;
   static constexpr int NH = D / 64;                // 64-wide swizzled panels of a row
   static constexpr int PANEL = TILE * 128;         // bytes of one panel of a tile
   static constexpr int TB = NH * PANEL;            // one bf16 tile of 128 rows
   static constexpr int NS = Q8 ? 3 : (D == 128 ? 5 : 10);  // bf16 key/value tiles in the ring
-  static constexpr int NR = Q8 ? (D == 128 ? 3 : 12) : 0;  // e4m3 tiles in the ring
-  static constexpr int NL = Q8 ? NR : NS;          // the ring that copies land in
-  static constexpr int LAND = Q8 ? TILE * D : TB;  // bytes of one of its tiles
+  static constexpr int NR = Q8 ? (D == 128 ? 3 : 8) : 0;  // e4m3 tiles in front of it
+  static constexpr int LAND = Q8 ? TILE * D : TB;  // bytes of a tile as copied
+  // The rings that copies land in.  bf16: one.  e4m3: the tile form's (L) in front of its bf16 ring, and the
+  // thin form's (H), which takes the memory of both: a segment of the other form starts when the last one's
+  // tiles are done with.
+  static constexpr int NL = Q8 ? NR : NS;
+  static constexpr int NH_ = Q8 ? NS * TB / LAND + NR : NS;
   static constexpr int Q_OFF = 0;
   static constexpr int KV_OFF = 2 * TB;
   static constexpr int RAW_OFF = KV_OFF + NS * TB;
-  static constexpr int LAND_OFF = Q8 ? RAW_OFF : KV_OFF;
-  static constexpr int SCALE_OFF = RAW_OFF + NR * TILE * D;  // TILE scales per e4m3 tile
-  static constexpr int BAR_OFF = SCALE_OFF + NR * TILE * 4;
-  // Barriers.  LFULL / LEMPTY: the ring that copies land in; FULL / EMPTY: the e4m3 form's bf16 ring.  A
-  // wait by parity is only right if its thread cannot fall two phases behind or get ahead of the phase
-  // before it, so
-  //  - tile i of the landing ring completes LFULL[i % (2 NL)], twice as many barriers as slots: a team of
-  //    the thin form that waits for tile i skipped the tiles of the other team, but released tile i - 3 or
-  //    a later one of its own, whose slot was filled after tile i - 2 NL had landed (NL >= 3);
+  static constexpr int L_OFF = Q8 ? RAW_OFF : KV_OFF;
+  static constexpr int H_OFF = KV_OFF;
+  static constexpr int SCALE_OFF = RAW_OFF + NR * LAND;  // TILE scales per landed e4m3 tile
+  static constexpr int BAR_OFF = SCALE_OFF + (Q8 ? NH_ * TILE * 4 : 0);
+  // Barriers.  LFULL / LEMPTY, HFULL / HEMPTY: the rings that copies land in (the same when there is one);
+  // FULL / EMPTY: the e4m3 form's bf16 ring.  A wait by parity is only right if its thread cannot fall two
+  // phases behind or get ahead of the phase before it, so
+  //  - tile i of a landing ring completes FULL[i % (2 N)], twice as many barriers as slots: a team of the
+  //    thin form that waits for tile i skipped the tiles of the other team, but released tile i - 3 or a
+  //    later one of its own, whose slot was filled after tile i - 2 N had landed (N >= 3);
   //  - whoever waits for QFULL[0] (the MMA warp and the softmax warps) does so for every segment, and
-  //    QEMPTY[0] needs all of them;
-  //  - the expanding warps take note of every landed tile, the thin form's too, and LEMPTY needs them.
-  static constexpr int LFULL = 0, LEMPTY = LFULL + 2 * NL, FULL = LEMPTY + NL, EMPTY = FULL + (Q8 ? NS : 0),
+  //    QEMPTY[0] needs all of them.
+  static constexpr int LFULL = 0, LEMPTY = LFULL + 2 * NL, HFULL = Q8 ? LEMPTY + NL : LFULL,
+                       HEMPTY = Q8 ? HFULL + 2 * NH_ : LEMPTY, FULL = HEMPTY + NH_, EMPTY = FULL + (Q8 ? NS : 0),
                        SFULL = EMPTY + (Q8 ? NS : 0), PREADY = SFULL + 2, QFULL = PREADY + 2, QEMPTY = QFULL + 2,
                        OFULL = QEMPTY + 2, FIX = OFULL + 2, ML = FIX + 2, OBFREE = ML + 1, TEAM = OBFREE + 1,
-                       SEGF = TEAM + 1, SEGE = SEGF + SEGS, DRAIN = SEGE + SEGS, NBAR = DRAIN + 1;
-  static constexpr int LEMPTY_COUNT = Q8 ? 12 : 8;          // arrivals that release a slot
+                       TCDONE = TEAM + 1, SEGF = TCDONE + 1, SEGE = SEGF + SEGS, DRAIN = SEGE + SEGS, NBAR = DRAIN + 1;
+  // arrivals that complete a phase of barrier i
+  static __device__ __forceinline__ int arrivals(int i) {
+    if (i < LEMPTY) return 1;
+    if (i < LEMPTY + NL) return Q8 ? 4 : 8;
+    if (Q8 && i < HEMPTY) return 1;
+    if (i < FULL) return 8;
+    if (i < EMPTY) return 4;
+    if (i < SFULL) return 1;
+    if (i >= PREADY && i < QFULL) return 4;
+    if (i >= QEMPTY && i < OFULL) return i == QEMPTY ? 9 : 8;
+    if (i >= FIX && i < TEAM) return 4;
+    if (i == TEAM) return 8;
+    if (i >= SEGE && i < DRAIN) return THREADS / 32 - 1;
+    return 1;
+  }
   static constexpr int MISC_OFF = BAR_OFF + 8 * NBAR;       // TMEM address, abort flag, bad-row masks
   static constexpr int SEG_OFF = (MISC_OFF + 48 + 15) / 16 * 16;  // SEGS segments of 48 bytes
   static constexpr int ML_OFF = SEG_OFF + 48 * SEGS;        // row maxima and sums (2 x 128 floats), flags (128 bytes)
   static constexpr int BYTES = ML_OFF + 9 * TILE + 1024;    // + alignment
-  static constexpr int THREADS = Q8 ? 512 : 384;
   // registers per thread: 128 (Q8) or 168 at launch, moved to the two softmax warpgroups
   static constexpr int REGS_SOFTMAX = Q8 ? 176 : 208, REGS_OTHER = Q8 ? 80 : 88;
   static_assert(256 * REGS_SOFTMAX + (THREADS - 256) * REGS_OTHER <= THREADS * (Q8 ? 128 : 168), "register split");
@@ -136,12 +155,6 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return d;
 }
 
-__device__ __forceinline__ uint32_t bf16x2_mul(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
-
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
   uint4 v;
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
@@ -164,19 +177,6 @@ __device__ __forceinline__ void reg_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-// Four e4m3 codes -> four bf16 values times s (a bf16 pair).  The code's bits s eeee mmm become
-// s 0000eeee mmm0000, a bf16 that is 2^-120 of the code's value (its subnormals are bf16 subnormals);
-// s holds 2^120 times the scale as far as bf16 goes.  The product is exact short of bf16's own
-// underflow.
-__device__ __forceinline__ uint2 expand4(uint32_t x, uint32_t s) {
-  // bytes sign-extended to 16 bits (prmt's sign mode), then moved up by 4: the sign's copies that land
-  // on the exponent's upper bits are masked away
-  uint32_t a, b;
-  asm("prmt.b32 %0, %1, 0, 0x9180;" : "=r"(a) : "r"(x));
-  asm("prmt.b32 %0, %1, 0, 0xB3A2;" : "=r"(b) : "r"(x));
-  return make_uint2(bf16x2_mul((a << 4) & 0x87f087f0u, s), bf16x2_mul((b << 4) & 0x87f087f0u, s));
-}
-
 // 16 consecutive 32-bit columns of this thread's lane.
 __device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t (&v)[16]) {
   asm volatile(
@@ -197,10 +197,10 @@ __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&v)[
       : "memory");
 }
 
-constexpr int AHEAD = 3;  // key tiles by which an e4m3 cache is asked for ahead of the copies
-
-__device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
-  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+// A value that all lanes hold, or one lane (the others 0), as a warp-uniform one: what the copy and MMA
+// instructions take without going lane by lane.
+__device__ __forceinline__ int uniform(int x) {
+  return static_cast<int>(__reduce_or_sync(0xffffffffu, static_cast<uint32_t>(x)));
 }
 
 // Arrive n times.

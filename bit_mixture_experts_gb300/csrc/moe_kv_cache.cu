@@ -10,8 +10,13 @@
 // reading back rounds nothing and an attention over the cache sees the same
 // bits as one over the bf16 values it stands for.
 //
-// Both kernels move every byte once and compute next to nothing: a thread per
-// eight values (one 16-byte load or store of bf16), d/8 threads per row.
+// Both kernels move every byte once and compute next to nothing.  A warp takes
+// 1, 4 or 16 consecutive tokens: its lanes look up one token's sequence, page
+// and row each, then move the tokens' rows (keys then values, by head), a row
+// per d/8 lanes (d/16 where a row is read from e4m3: 16 codes a lane).  The
+// lookups cost as much as moving several rows, so they are not done per row:
+// with one thread per eight values looking up its own token the kernels ran at
+// the instruction rate, not the memory's.
 #include "moe_kv_dev.cuh"
 
 namespace moe {
@@ -43,103 +48,129 @@ __device__ __forceinline__ uint32_t row_scale_bits(uint32_t amax, uint32_t* inv)
   return static_cast<uint32_t>(127 + e) << 23;
 }
 
-// One thread: eight values of one row.  Item i: chunk i % (D/8) of row i / (D/8); rows in the order
-// token, key before value, head.
+// A token's place: the pool's row of its head 0 (head h: h * page_size further), or -1 where it has none
+// (rows of no sequence: -2).
+__device__ __forceinline__ int find_place(const kv::Args& a, int t) {
+  if (t >= a.T) return -2;
+  const int b = kv::find_seq(a, t);
+  if (b < 0) return -2;
+  const kv::Seq s = kv::load_seq(a, b);
+  const int p = s.len - s.n + t - s.row0;
+  if (p < 0 || p >= s.len) return -1;
+  const int e = p / a.page_size, page = kv::find_page(a, b, p);
+  return page < 0 ? -1 : page * a.heads * a.page_size + p - e * a.page_size;
+}
+
 template <int D, bool Q8>
-__global__ void __launch_bounds__(KV_THREADS) kv_append_kernel(const kv::Args a, const NewRows in) {
-  constexpr int C = D / 8;
-  const long long items = static_cast<long long>(a.T) * 2 * a.heads * C;
-  const long long i = static_cast<long long>(blockIdx.x) * KV_THREADS + threadIdx.x;
-  const bool live = i < items;
-  const long long row = live ? i / C : 0;
-  const int c = static_cast<int>(i % C);
-  const int t = static_cast<int>(row / (2 * a.heads)), r = static_cast<int>(row % (2 * a.heads));
-  const bool is_v = r >= a.heads;
-  const int h = is_v ? r - a.heads : r;
-  uint4 x = make_uint4(0, 0, 0, 0);
-  size_t at = 0;  // row of the pool
-  bool write = false;
-  if (live) {
-    const uint16_t* src = is_v ? in.v + t * in.v_token + h * in.v_head : in.k + t * in.k_token + h * in.k_head;
-    x = __ldg(reinterpret_cast<const uint4*>(src) + c);
-    const int b = kv::find_seq(a, t);
-    if (b >= 0) {
-      const kv::Seq s = kv::load_seq(a, b);
-      const int p = s.len - s.n + t - s.row0;
-      const int page = p >= 0 && p < s.len ? kv::find_page(a, b, p) : -1;
-      write = page >= 0;
-      at = (static_cast<size_t>(max(page, 0)) * a.heads + h) * a.page_size + max(p, 0) % a.page_size;
+__global__ void __launch_bounds__(KV_THREADS) kv_append_kernel(const kv::Args a, const NewRows in, int tokens) {
+  constexpr int C = D / 8, RPW = 32 / C;  // lanes of a row, rows at a time
+  const int warp = (blockIdx.x * KV_THREADS + threadIdx.x) >> 5, lane = threadIdx.x & 31;
+  const int t0 = warp * tokens, c = lane % C;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (t0 >= a.T) return;
+  const int mine = lane < tokens ? find_place(a, t0 + lane) : -2;
+  for (int i = 0; i < tokens; ++i) {
+    const int place = __shfl_sync(0xffffffffu, mine, i), t = t0 + i;
+    if (place < 0) continue;
+#pragma unroll 4
+    for (int r0 = 0; r0 < 2 * a.heads; r0 += RPW) {
+      const int r = r0 + lane / C;
+      const bool live = r < 2 * a.heads, is_v = r >= a.heads;
+      const int h = is_v ? r - a.heads : r;
+      const uint16_t* src = is_v ? in.v + t * in.v_token + h * in.v_head : in.k + t * in.k_token + h * in.k_head;
+      const uint4 x = live ? __ldg(reinterpret_cast<const uint4*>(src) + c) : make_uint4(0, 0, 0, 0);
+      const size_t at = static_cast<size_t>(place) + h * a.page_size;
+      if (!Q8) {
+        if (live) reinterpret_cast<uint4*>(is_v ? a.v : a.k)[at * C + c] = x;
+        continue;
+      }
+      const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+      uint32_t amax = 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) amax = max(amax, max(u[j] & 0x7fffu, (u[j] >> 16) & 0x7fffu));
+#pragma unroll
+      for (int m = C / 2; m >= 1; m >>= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, m));
+      uint32_t inv_bits;
+      const uint32_t scale = row_scale_bits(amax, &inv_bits);
+      const float inv = __uint_as_float(inv_bits);
+      uint32_t o[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        uint16_t lo, hi;
+        const uint32_t p = u[2 * j], q = u[2 * j + 1];
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;"
+            : "=h"(lo)
+            : "f"(__uint_as_float(p & 0xffff0000u) * inv), "f"(__uint_as_float(p << 16) * inv));
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;"
+            : "=h"(hi)
+            : "f"(__uint_as_float(q & 0xffff0000u) * inv), "f"(__uint_as_float(q << 16) * inv));
+        o[j] = static_cast<uint32_t>(lo) | static_cast<uint32_t>(hi) << 16;
+      }
+      if (live) {
+        reinterpret_cast<uint2*>(is_v ? a.v : a.k)[at * C + c] = make_uint2(o[0], o[1]);
+        if (c == 0) (is_v ? a.v_scale : a.k_scale)[at] = __uint_as_float(scale);
+      }
     }
-  }
-  if (!Q8) {
-    if (write) reinterpret_cast<uint4*>(is_v ? a.v : a.k)[at * C + c] = x;
-    return;
-  }
-  const uint32_t u[4] = {x.x, x.y, x.z, x.w};
-  uint32_t amax = 0;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) amax = max(amax, max(u[j] & 0x7fffu, (u[j] >> 16) & 0x7fffu));
-#pragma unroll
-  for (int m = C / 2; m >= 1; m >>= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, m));
-  uint32_t inv_bits;
-  const uint32_t scale = row_scale_bits(amax, &inv_bits);
-  const float inv = __uint_as_float(inv_bits);
-  uint32_t o[2];
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    uint16_t lo, hi;
-    const uint32_t p = u[2 * j], q = u[2 * j + 1];
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;"
-        : "=h"(lo)
-        : "f"(__uint_as_float(p & 0xffff0000u) * inv), "f"(__uint_as_float(p << 16) * inv));
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;"
-        : "=h"(hi)
-        : "f"(__uint_as_float(q & 0xffff0000u) * inv), "f"(__uint_as_float(q << 16) * inv));
-    o[j] = static_cast<uint32_t>(lo) | static_cast<uint32_t>(hi) << 16;
-  }
-  if (write) {
-    reinterpret_cast<uint2*>(is_v ? a.v : a.k)[at * C + c] = make_uint2(o[0], o[1]);
-    if (c == 0) (is_v ? a.v_scale : a.k_scale)[at] = __uint_as_float(scale);
   }
 }
 
 template <int D, bool Q8>
 __global__ void __launch_bounds__(KV_THREADS) kv_read_kernel(const kv::Args a, uint16_t* __restrict__ k_out,
-                                                             uint16_t* __restrict__ v_out) {
-  constexpr int C = D / 8;
-  const long long items = static_cast<long long>(a.T) * 2 * a.heads * C;
-  const long long i = static_cast<long long>(blockIdx.x) * KV_THREADS + threadIdx.x;
-  if (i >= items) return;
-  const long long row = i / C;
-  const int c = static_cast<int>(i % C);
-  const int t = static_cast<int>(row / (2 * a.heads)), r = static_cast<int>(row % (2 * a.heads));
-  const bool is_v = r >= a.heads;
-  const int h = is_v ? r - a.heads : r;
-  const int b = kv::find_seq(a, t);
-  if (b < 0) return;
-  const kv::Seq s = kv::load_seq(a, b);
-  const int p = s.len - s.n + t - s.row0;
-  const int page = p >= 0 && p < s.len ? kv::find_page(a, b, p) : -1;
-  uint4 o = make_uint4(0, 0, 0, 0);
-  if (page >= 0) {
-    const size_t at = (static_cast<size_t>(page) * a.heads + h) * a.page_size + p % a.page_size;
-    if (!Q8) {
-      o = reinterpret_cast<const uint4*>(is_v ? a.v : a.k)[at * C + c];
-    } else {
-      const uint2 x = reinterpret_cast<const uint2*>(is_v ? a.v : a.k)[at * C + c];
-      const float sc = (is_v ? a.v_scale : a.k_scale)[at];
-      const float2 f0 = kv::e4m3x2_to_float2(x.x & 0xffffu), f1 = kv::e4m3x2_to_float2(x.x >> 16);
-      const float2 f2 = kv::e4m3x2_to_float2(x.y & 0xffffu), f3 = kv::e4m3x2_to_float2(x.y >> 16);
-      o = make_uint4(pack_bf16x2(f0.x * sc, f0.y * sc), pack_bf16x2(f1.x * sc, f1.y * sc),
-                     pack_bf16x2(f2.x * sc, f2.y * sc), pack_bf16x2(f3.x * sc, f3.y * sc));
+                                                             uint16_t* __restrict__ v_out, int tokens) {
+  constexpr int C = Q8 ? D / 16 : D / 8, RPW = 32 / C;  // 16-byte pieces of a stored row
+  const int warp = (blockIdx.x * KV_THREADS + threadIdx.x) >> 5, lane = threadIdx.x & 31;
+  const int t0 = warp * tokens, c = lane % C;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (t0 >= a.T) return;
+  const int mine = lane < tokens ? find_place(a, t0 + lane) : -2;
+  for (int i = 0; i < tokens; ++i) {
+    const int place = __shfl_sync(0xffffffffu, mine, i), t = t0 + i;
+    if (place == -2) continue;
+#pragma unroll 4
+    for (int r = lane / C; r < 2 * a.heads; r += RPW) {
+      const bool is_v = r >= a.heads;
+      const int h = is_v ? r - a.heads : r;
+      const size_t at = static_cast<size_t>(max(place, 0)) + h * a.page_size;
+      uint4* dst = reinterpret_cast<uint4*>(is_v ? v_out : k_out) +
+                   (static_cast<size_t>(t) * a.heads + h) * (D / 8) + (Q8 ? 2 * c : c);
+      uint4 x = make_uint4(0, 0, 0, 0);
+      if (place >= 0) x = reinterpret_cast<const uint4*>(is_v ? a.v : a.k)[at * C + c];
+      if (!Q8) {
+        *dst = x;
+        continue;
+      }
+      uint32_t s1 = 0, s2 = 0;
+      if (place >= 0) kv::scale_pairs((is_v ? a.v_scale : a.k_scale)[at], &s1, &s2);
+      const uint2 v0 = kv::expand4(x.x, s1), v1 = kv::expand4(x.y, s1);
+      const uint2 v2 = kv::expand4(x.z, s1), v3 = kv::expand4(x.w, s1);
+      dst[0] = make_uint4(kv::bf16x2_mul(v0.x, s2), kv::bf16x2_mul(v0.y, s2), kv::bf16x2_mul(v1.x, s2),
+                          kv::bf16x2_mul(v1.y, s2));
+      dst[1] = make_uint4(kv::bf16x2_mul(v2.x, s2), kv::bf16x2_mul(v2.y, s2), kv::bf16x2_mul(v3.x, s2),
+                          kv::bf16x2_mul(v3.y, s2));
     }
   }
-  reinterpret_cast<uint4*>(is_v ? v_out : k_out)[(static_cast<size_t>(t) * a.heads + h) * C + c] = o;
 }
 
-unsigned blocks_for(const kv::Args& a) {
-  const long long items = static_cast<long long>(a.T) * 2 * a.heads * (a.d / 8);
-  return static_cast<unsigned>((items + KV_THREADS - 1) / KV_THREADS);
+// Tokens per warp: as many as leave every SM a few dozen warps.
+int tokens_per_warp(int T) { return T >= 16 * 4096 ? 16 : T >= 4 * 2048 ? 4 : 1; }
+
+// A grid of one warp per `tokens` tokens, started while the kernel before it in the stream ends (the
+// kernels wait for its results themselves).
+template <typename... P, typename... Q>
+cudaError_t launch_warps(void (*kernel)(P...), int T, int tokens, cudaStream_t s, Q... args) {
+  const int warps = ceil_div(T, tokens);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ceil_div(warps, KV_THREADS / 32));
+  cfg.blockDim = dim3(KV_THREADS);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+  note_launches(1);
+  return e;
 }
 
 }  // namespace
@@ -147,27 +178,21 @@ unsigned blocks_for(const kv::Args& a) {
 cudaError_t launch_kv_append(const kv::Args& a, bool q8, const uint16_t* k, long long k_token, long long k_head,
                              const uint16_t* v, long long v_token, long long v_head, cudaStream_t s) {
   const NewRows in = {k, v, k_token, k_head, v_token, v_head};
-  const unsigned grid = blocks_for(a);
+  const int n = tokens_per_warp(a.T);
   if (a.d == 64)
-    q8 ? kv_append_kernel<64, true><<<grid, KV_THREADS, 0, s>>>(a, in)
-       : kv_append_kernel<64, false><<<grid, KV_THREADS, 0, s>>>(a, in);
-  else
-    q8 ? kv_append_kernel<128, true><<<grid, KV_THREADS, 0, s>>>(a, in)
-       : kv_append_kernel<128, false><<<grid, KV_THREADS, 0, s>>>(a, in);
-  note_launches(1);
-  return cudaGetLastError();
+    return q8 ? launch_warps(kv_append_kernel<64, true>, a.T, n, s, a, in, n)
+              : launch_warps(kv_append_kernel<64, false>, a.T, n, s, a, in, n);
+  return q8 ? launch_warps(kv_append_kernel<128, true>, a.T, n, s, a, in, n)
+            : launch_warps(kv_append_kernel<128, false>, a.T, n, s, a, in, n);
 }
 
 cudaError_t launch_kv_read(const kv::Args& a, bool q8, uint16_t* k, uint16_t* v, cudaStream_t s) {
-  const unsigned grid = blocks_for(a);
+  const int n = tokens_per_warp(a.T);
   if (a.d == 64)
-    q8 ? kv_read_kernel<64, true><<<grid, KV_THREADS, 0, s>>>(a, k, v)
-       : kv_read_kernel<64, false><<<grid, KV_THREADS, 0, s>>>(a, k, v);
-  else
-    q8 ? kv_read_kernel<128, true><<<grid, KV_THREADS, 0, s>>>(a, k, v)
-       : kv_read_kernel<128, false><<<grid, KV_THREADS, 0, s>>>(a, k, v);
-  note_launches(1);
-  return cudaGetLastError();
+    return q8 ? launch_warps(kv_read_kernel<64, true>, a.T, n, s, a, k, v, n)
+              : launch_warps(kv_read_kernel<64, false>, a.T, n, s, a, k, v, n);
+  return q8 ? launch_warps(kv_read_kernel<128, true>, a.T, n, s, a, k, v, n)
+            : launch_warps(kv_read_kernel<128, false>, a.T, n, s, a, k, v, n);
 }
 
 }  // namespace moe

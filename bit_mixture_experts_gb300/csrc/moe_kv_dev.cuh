@@ -76,5 +76,34 @@ __device__ __forceinline__ float2 e4m3x2_to_float2(uint32_t x) {
   return f;
 }
 
+__device__ __forceinline__ uint32_t bf16x2_mul(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+// Four e4m3 codes -> four bf16 values times s (a bf16 pair).  The code's bits s eeee mmm become
+// s 0000eeee mmm0000, a bf16 that is 2^-120 of the code's value (its subnormals are bf16 subnormals);
+// s holds 2^120 times the scale as far as bf16 goes.  The product is exact short of bf16's own
+// underflow.
+__device__ __forceinline__ uint2 expand4(uint32_t x, uint32_t s) {
+  // bytes sign-extended to 16 bits (prmt's sign mode), then moved up by 4: the sign's copies that land
+  // on the exponent's upper bits are masked away
+  uint32_t a, b;
+  asm("prmt.b32 %0, %1, 0, 0x9180;" : "=r"(a) : "r"(x));
+  asm("prmt.b32 %0, %1, 0, 0xB3A2;" : "=r"(b) : "r"(x));
+  return make_uint2(bf16x2_mul((a << 4) & 0x87f087f0u, s), bf16x2_mul((b << 4) & 0x87f087f0u, s));
+}
+
+// 2^120 times a scale (a power of two; NaN stays NaN) as two bf16 pairs whose product it is: *s2 is 1 but
+// for scales of 2^8 and more, which 2^120 times is beyond bf16.
+__device__ __forceinline__ void scale_pairs(float scale, uint32_t* s1, uint32_t* s2) {
+  const uint32_t sc = __float_as_uint(scale);
+  const int e = static_cast<int>(sc >> 23) + 120;
+  const uint32_t lo = min(e, 254), hi = e - lo + 127;
+  *s1 = (sc > 0x7f800000u ? 0x7fffu : lo << 7) * 0x10001u;
+  *s2 = (hi << 7) * 0x10001u;
+}
+
 }  // namespace kv
 }  // namespace moe

@@ -101,11 +101,11 @@ __device__ __forceinline__ bool thin_segment(const Args& a, const AttnArgs& g, c
   const int vis0 = sg.base + 1;  // keys that all rows see; row r sees those before vis0 + its token
   const int see0 = ok0 ? vis0 + r0 / g.group : 0, see1 = ok1 ? vis0 + r1 / g.group : 0;
 
-  auto landed = [&](int i) -> bool { return wait(L::LFULL + i % (2 * L::NL), (i / (2 * L::NL)) & 1); };
+  auto landed = [&](int i) -> bool { return wait(L::HFULL + i % (2 * L::NH_), (i / (2 * L::NH_)) & 1); };
   // a tile is released by the four warps that read it, or all eight
   auto release = [&](int st) {
     __syncwarp();
-    if (lane == 0) mbar_arrive_n(bar(L::LEMPTY + st), step);
+    if (lane == 0) mbar_arrive_n(bar(L::HEMPTY + st), step);
   };
 
   // Q's fragments
@@ -128,8 +128,8 @@ __device__ __forceinline__ bool thin_segment(const Args& a, const AttnArgs& g, c
 
   for (int kt = sg.t0 + first_tile; kt < sg.t1; kt += step) {
     const int k0 = kt * TILE, ki = 2 * (units + kt - sg.t0);
-    const int ks = ki % L::NL, vs = (ki + 1) % L::NL;
-    const uint32_t kbase = sbase + L::LAND_OFF + ks * L::LAND, vbase = sbase + L::LAND_OFF + vs * L::LAND;
+    const int ks = ki % L::NH_, vs = (ki + 1) % L::NH_;
+    const uint32_t kbase = sbase + L::H_OFF + ks * L::LAND, vbase = sbase + L::H_OFF + vs * L::LAND;
     const bool fix = k0 + TILE > min(vis0, sg.len);
     if (!landed(ki)) return false;
     // ---- scores of 32 keys: four fragments of 8

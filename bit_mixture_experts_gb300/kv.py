@@ -102,18 +102,18 @@ class PagedKVCache:
     def _empty(self, shape, dtype, stream):
         """An output for a call on `stream`: allocated as memory of that stream."""
         if stream is None:
-            return torch.empty(shape, dtype=dtype, device=self.device)
+            return self.k.new_empty(shape, dtype=dtype)
         with torch.cuda.stream(stream):
-            return torch.empty(shape, dtype=dtype, device=self.device)
+            return self.k.new_empty(shape, dtype=dtype)
 
-    def workspace(self, stream=None):
-        """The attention's scratch for calls on `stream` (one per stream, so calls on two streams share none;
-        allocated at the first call there: make that one before a graph capture)."""
-        key = (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+    def _workspace(self, stream):
+        """(pointer, bytes) of the attention's scratch for calls on `stream`: one per stream, so that calls on
+        two streams share none.  Allocated at the first call there: make that one before a graph capture."""
+        key = _lib._stream(stream)
         if key not in self._workspaces:
-            n = _lib.moe_kv_attention_workspace_size(self.d)
-            self._workspaces[key] = self._empty((max(n, 16),), torch.uint8, stream)
-        return self._workspaces[key]
+            t = self._empty((max(_lib.moe_kv_attention_workspace_size(self.d), 16),), torch.uint8, stream)
+            self._workspaces[key] = (t, (t.data_ptr(), t.nbytes))
+        return self._workspaces[key][1]
 
     def append(self, k, v, batch, stream=None):
         """Write the new tokens' keys and values (bf16 [T, heads, d], strided views welcome) into the cache."""
@@ -150,5 +150,5 @@ class PagedKVCache:
                 raise ValueError("out must be contiguous")
         lse = self._empty(q.shape[:2], torch.float32, stream) if return_lse else None
         _lib.moe_kv_attention(q, self.d ** -0.5 if scale is None else scale, self.struct, batch.struct, out, lse,
-                              self.workspace(stream) if workspace is None else workspace, stream)
+                              self._workspace(stream) if workspace is None else workspace, stream)
         return (out, lse) if return_lse else out
