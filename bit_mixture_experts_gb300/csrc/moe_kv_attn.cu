@@ -70,12 +70,12 @@ __global__ void __launch_bounds__(Layout<D, Q8>::THREADS, 1)
   // this CTA's share of the units (the scan's scratch lies where the key/value ring will be)
   kv::Share share;
   kv::Start from;
-  if (a.B > 32 || warp == 3)
+  if (a.B > 32 || warp == 0)
     from = kv::locate<L::THREADS>(a, 2 * g.tpt, static_cast<int>(gridDim.x), cta,
                                   reinterpret_cast<long long*>(smem + L::KV_OFF), share);
   Seg sg;
   kv::Walk walk(a, 2 * g.tpt, 0, 0, 0, 0, false);
-  if (warp == 3) {  // publishes the segments; the first is worked out while the CTA starts up
+  if (warp == 0) {  // works the segments out; the first while the CTA starts up
     if (cta < share.ctas)
       walk = kv::Walk(a, 2 * g.tpt, share.lo(cta), share.lo(cta + 1), from.b, from.b_lo, share.whole);
     if (!walk.next(sg)) sg.ntok = 0;  // the end
@@ -90,7 +90,7 @@ __global__ void __launch_bounds__(Layout<D, Q8>::THREADS, 1)
   auto wait = [&](int i, uint32_t parity) -> bool {
     return tc_dev::wait_warp(bar(i), parity, s_abort, a.err, g.wait_cycles, g.sleep_ns);
   };
-  // the CTA's segments, in order, as warp 3 publishes them
+  // the CTA's segments, in order, as warp 0 publishes them
   int segs = 0;  // taken so far
   auto next = [&](Seg& sg) -> bool {
     const int slot = segs % SEGS;
@@ -107,9 +107,9 @@ __global__ void __launch_bounds__(Layout<D, Q8>::THREADS, 1)
   auto thin = [&](const Seg& sg) -> bool { return sg.ntok * g.group <= THIN_ROWS; };
 
   if (warp < 4) {
-    reg_dec<L::REGS_OTHER>();
+    reg_dec<L::REGS_ISSUE>();
     if (warp == 0) {
-      // ---------------------------------------------- copies: K and V of every key tile, in that order
+      // ---------------------------------------------- segments, and copies: K and V of every key tile
       const int per_page = a.page_size / g.chunk, per_tile = TILE / g.chunk;
       // per ring (tile form, thin form): tiles issued, next slot, its round's parity, landing barrier
       struct Ring {
@@ -118,7 +118,24 @@ __global__ void __launch_bounds__(Layout<D, Q8>::THREADS, 1)
       bool ok = true;
       int form = -1;  // the last segment's
       uint32_t tc_ph = 0;
-      while (ok && next(sg)) {
+      int4 join = make_int4(0, 0, 0, 0);
+      for (;; ++segs) {
+        if (segs > 0 && !walk.next(sg)) sg.ntok = 0;
+        const int slot = segs % SEGS;
+        if (segs >= SEGS && !wait(L::SEGE + slot, (segs / SEGS - 1) & 1)) break;
+        if (lane == 0) {
+          int4* p = reinterpret_cast<int4*>(smem + L::SEG_OFF + slot * 48);
+          p[0] = make_int4(sg.row0, sg.len, sg.b, sg.h);
+          p[1] = make_int4(sg.i0, sg.ntok, sg.base, sg.t0);
+          p[2] = make_int4(sg.t1, sg.nt, 0, 0);
+          ptx::mbar_arrive(bar(L::SEGF + slot));
+        }
+        __syncwarp();
+        if (sg.ntok == 0) break;
+        sg = {uniform(sg.row0), uniform(sg.len), uniform(sg.b),  uniform(sg.h),  uniform(sg.i0),
+              uniform(sg.ntok), uniform(sg.base), uniform(sg.t0), uniform(sg.t1), uniform(sg.nt)};
+        if (sg.t0 == 0 && sg.t1 < sg.nt)  // the rest of the item is other CTAs': this part will be joined with theirs
+          join = make_int4(share.of(walk.item_end - 1) - cta + 1, sg.row0 + sg.i0, sg.ntok, sg.h);
         const int now = Q8 && thin(sg) ? 1 : 0;
         if (Q8 && form >= 0 && now != form) {
           // the rings share memory
@@ -189,7 +206,9 @@ __global__ void __launch_bounds__(Layout<D, Q8>::THREADS, 1)
           }
         }
         (now ? thin_ring : tile_ring) = rg;
+        if (!ok) break;
       }
+      if (lane == 0) g.joins[cta] = join;
       // every copy issued has landed before the CTA ends (at once unless a wait gave up)
       for (int i = max(0, tile_ring.n - L::NL); i < tile_ring.n; ++i)
         tc_dev::wait_drain(bar(L::LFULL + i % (2 * L::NL)), (i / (2 * L::NL)) & 1, 0);
@@ -285,66 +304,45 @@ __global__ void __launch_bounds__(Layout<D, Q8>::THREADS, 1)
       // all MMAs are done before the tensor memory is released
       ptx::mma_commit_elect(bar(L::DRAIN));
       tc_dev::wait_drain(bar(L::DRAIN), 0, 0);
-    } else if (warp == 2) {
-      // ---------------------------------------------- query tiles a and b of every item
+    } else {
+      // ---------------------------------------------- query tile t of every item
+      const int t = warp - 2;
       constexpr int C = D / 8;
-      uint32_t ph[2] = {1, 1};  // of QEMPTY: the first use waits for nothing
-      bool ok = true;
-      while (ok && next(sg)) {
-        const bool two = sg.ntok > g.tpt;
-        for (int t = 0; t < 2; ++t) {
-          const int tok0 = t * g.tpt, rows = min(g.tpt, sg.ntok - tok0) * g.group;
-          if (t == 1 && !two && !thin(sg)) break;
-          ok = wait(L::QEMPTY + t, ph[t]);
-          if (!ok) break;
-          ph[t] ^= 1;
-          if (t == 1 && !two) break;  // the thin form uses both tiles' memory
-          // a lane's column of 8 values, 32 / C rows at a time, in the order token, head
-          const long long by_token = g.q_token - g.group * g.q_head;
-          int hd = lane / C;
-          const uint16_t* src = g.q + static_cast<long long>(sg.row0 + sg.i0 + tok0) * g.q_token +
-                                (static_cast<long long>(sg.h) * g.group + hd) * g.q_head + lane % C * 8;
-          const uint32_t col = sbase + L::Q_OFF + t * TB + (lane % C >> 3) * PANEL;
+      uint32_t ph = 1, phb = 1;  // of QEMPTY: the first use waits for nothing
+      while (next(sg)) {
+        const bool pair = sg.ntok > g.tpt;
+        if (!wait(L::QEMPTY, ph)) break;
+        ph ^= 1;
+        if (t == 1) {
+          // tile a's barrier waits for this warp too: the thin form uses both tiles' memory
+          if (pair || thin(sg)) {
+            if (!wait(L::QEMPTY + 1, phb)) break;
+            phb ^= 1;
+          }
+          if (lane == 0) ptx::mbar_arrive(bar(L::QFULL));
+          if (!pair) continue;
+        }
+        // a lane's column of 8 values, 32 / C rows at a time, in the order token, head
+        const int tok0 = t * g.tpt, rows = min(g.tpt, sg.ntok - tok0) * g.group;
+        const long long by_token = g.q_token - g.group * g.q_head;
+        int hd = lane / C;
+        const uint16_t* src = g.q + static_cast<long long>(sg.row0 + sg.i0 + tok0) * g.q_token +
+                              (static_cast<long long>(sg.h) * g.group + hd) * g.q_head + lane % C * 8;
+        const uint32_t col = sbase + L::Q_OFF + t * TB + (lane % C >> 3) * PANEL;
 #pragma unroll 4
-          for (int r = lane / C; r < rows; r += 32 / C) {
-            while (hd >= g.group) {
-              hd -= g.group;
-              src += by_token;
-            }
-            ptx::cp_async_16(col + r * 128 + (((lane & 7) ^ (r & 7)) << 4), src);
-            hd += 32 / C;
-            src += 32 / C * g.q_head;
+        for (int r = lane / C; r < rows; r += 32 / C) {
+          while (hd >= g.group) {
+            hd -= g.group;
+            src += by_token;
           }
-          ptx::cp_async_commit();
-          if (t == 1) {
-            // tile a is on its way while tile b is asked for
-            ptx::cp_async_wait<1>();
-            ptx::fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(bar(L::QFULL));
-          }
+          ptx::cp_async_16(col + r * 128 + (((lane & 7) ^ (r & 7)) << 4), src);
+          hd += 32 / C;
+          src += 32 / C * g.q_head;
         }
         ptx::cp_async_wait_all();
-        if (!ok) break;
         ptx::fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(bar(L::QFULL + (two ? 1 : 0)));
-      }
-    } else {
-      // ---------------------------------------------- the CTA's segments
-      for (int n = 0;; ++n) {
-        const int slot = n % SEGS;
-        if (n > 0 && !walk.next(sg)) sg.ntok = 0;
-        if (n >= SEGS && !wait(L::SEGE + slot, (n / SEGS - 1) & 1)) break;
-        if (lane == 0) {
-          int4* p = reinterpret_cast<int4*>(smem + L::SEG_OFF + slot * 48);
-          p[0] = make_int4(sg.row0, sg.len, sg.b, sg.h);
-          p[1] = make_int4(sg.i0, sg.ntok, sg.base, sg.t0);
-          p[2] = make_int4(sg.t1, sg.nt, 0, 0);
-          ptx::mbar_arrive(bar(L::SEGF + slot));
-        }
-        __syncwarp();
-        if (sg.ntok == 0) break;
+        if (lane == 0) ptx::mbar_arrive(bar(L::QFULL + t));
       }
     }
   } else if (warp < 12) {
@@ -622,7 +620,7 @@ __global__ void __launch_bounds__(Layout<D, Q8>::THREADS, 1)
     }
   } else if (Q8) {
     // ------------------------------------------------ e4m3 -> bf16 tiles
-    reg_dec<L::REGS_OTHER>();
+    reg_dec<L::REGS_EXPAND>();
     const int tid = threadIdx.x - 384;
     constexpr int C = D / 16;  // 16-byte chunks of a row of codes
     int n = 0;                 // tiles so far
@@ -678,41 +676,26 @@ __global__ void __launch_bounds__(Layout<D, Q8>::THREADS, 1)
   }
 }
 
-// Joins the parts of the items that were cut.  Blocks (c, y): the item that the share of CTA c + 1 starts
-// inside of, if it is the first cut of that item, and every gridDim.y-th of its rows.  A row's parts go to
-// 1, 2, 4 or 8 warps (at four parts per warp's round the loads of a round are in flight together), lanes
-// over d, each with a running maximum; the warps' sums are added in a fixed order.
+// Joins the parts of the items that were cut.  Blocks (c, y): the item whose first part is CTA c's, if
+// there is one, and every gridDim.y-th of its rows.  A row's parts go to 1, 2, 4 or 8 warps (at four parts
+// per warp's round the loads of a round are in flight together), lanes over d, each with a running
+// maximum; the warps' sums are added in a fixed order.
 constexpr int MERGE_WARPS = 8, MERGE_Y = 8;
 
 template <int D>
-__global__ void __launch_bounds__(32 * MERGE_WARPS) kv_merge_kernel(const kv::Args a, const AttnArgs g, int ctas) {
+__global__ void __launch_bounds__(32 * MERGE_WARPS) kv_merge_kernel(const AttnArgs g) {
   constexpr int V = D / 32;
-  __shared__ long long scratch[50];
   __shared__ float s_m[MERGE_WARPS], s_l[MERGE_WARPS], s_acc[MERGE_WARPS][D];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int cut = static_cast<int>(blockIdx.x) + 1;
-  kv::Share share;
-  const kv::Start from = kv::locate<32 * MERGE_WARPS>(a, 2 * g.tpt, ctas, cut, scratch, share);
-  Seg sg;
-  int np = 0;  // parts: slot 1 of CTA cut - 1, slot 0 of the CTAs after it
-  if (cut < share.ctas && !share.whole) {
-    const long long u = share.lo(cut);
-    kv::Walk walk(a, 2 * g.tpt, u, share.total, from.b, from.b_lo, false);
-    walk.next(sg);
-    const long long first = u - sg.t0, end = first + sg.nt;  // the item's units
-    if (sg.t0 > 0 && share.lo(cut - 1) <= first) {           // a cut, and the first of its item
-      np = 2;
-      while (cut + np - 1 < share.ctas && share.lo(cut + np - 1) < end) ++np;
-    }
-  }
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = static_cast<int>(blockIdx.x);
   // every block waits for the attention kernel, so that this kernel's end says that both are done
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int4 join = g.joins[cta];
+  const int np = join.x, rows = join.z * g.group;  // parts: slot 1 of this CTA, slot 0 of those after it
   if (np == 0) return;
-  const int rows = sg.ntok * g.group;  // row = token * group + head
   const int per_row = np <= 4 ? 1 : np <= 8 ? 2 : np <= 16 ? 4 : 8, per_pass = MERGE_WARPS / per_row;
   const int sub = warp % per_row;
-  const float* slot0 = g.part + (2ll * (cut - 1) + 1) * slot_floats<D>();
-  const float* slot1 = g.part + 2ll * cut * slot_floats<D>();
+  const float* slot0 = g.part + (2ll * cta + 1) * slot_floats<D>();
+  const float* slot1 = g.part + 2ll * (cta + 1) * slot_floats<D>();
   auto slot = [&](int p) { return p == 0 ? slot0 : slot1 + 2ll * (p - 1) * slot_floats<D>(); };
   for (int q0 = static_cast<int>(blockIdx.y) * per_pass; q0 < rows; q0 += per_pass * static_cast<int>(gridDim.y)) {
     const int q = min(q0 + warp / per_row, rows - 1);
@@ -778,7 +761,7 @@ __global__ void __launch_bounds__(32 * MERGE_WARPS) kv_merge_kernel(const kv::Ar
     if (sub == 0 && q0 + warp / per_row < rows) {
       const float inv = l == 0.f ? 0.f : 1.0f / l;
       const int tok = q / g.group, hd = q - tok * g.group;
-      const long long row = static_cast<long long>(sg.row0 + sg.i0 + tok) * g.q_heads + sg.h * g.group + hd;
+      const long long row = static_cast<long long>(join.y + tok) * g.q_heads + join.w * g.group + hd;
       uint32_t* dst = reinterpret_cast<uint32_t*>(g.out + row * D + lane * V);
 #pragma unroll
       for (int j = 0; j < V / 2; ++j) dst[j] = pack_bf16x2(acc[2 * j] * inv, acc[2 * j + 1] * inv);
@@ -826,7 +809,7 @@ cudaError_t launch(const kv::Args& a, const AttnArgs& g, const CUtensorMap& tk, 
   cfg.gridDim = dim3(ctas - 1, min(static_cast<long long>(a.T) * g.group, static_cast<long long>(MERGE_Y)));
   cfg.blockDim = dim3(32 * MERGE_WARPS);
   cfg.dynamicSmemBytes = 0;
-  e = cudaLaunchKernelEx(&cfg, kv_merge_kernel<D>, a, g, ctas);
+  e = cudaLaunchKernelEx(&cfg, kv_merge_kernel<D>, g);
   note_launches(1);
   return e;
 }
@@ -837,7 +820,8 @@ int num_sms();
 unsigned long long wait_limit_ns();
 
 size_t kv_attention_workspace_bytes(int d) {
-  return 2 * static_cast<size_t>(num_sms()) * (d == 64 ? slot_floats<64>() : slot_floats<128>()) * sizeof(float);
+  const size_t slot = (d == 64 ? slot_floats<64>() : slot_floats<128>()) * sizeof(float);
+  return num_sms() * (sizeof(int4) + 2 * slot);
 }
 
 cudaError_t launch_kv_attention(const kv::Args& a, bool q8, const uint16_t* q, long long q_token, long long q_head,
@@ -848,7 +832,9 @@ cudaError_t launch_kv_attention(const kv::Args& a, bool q8, const uint16_t* q, l
   g.q_head = q_head;
   g.out = out;
   g.lse = lse;
-  g.part = static_cast<float*>(ws);
+  const int ctas = num_sms();
+  g.joins = static_cast<int4*>(ws);
+  g.part = reinterpret_cast<float*>(g.joins + ctas);
   g.scale_log2 = scale * 1.44269504088896341f;
   g.q_heads = q_heads;
   g.group = q_heads / a.heads;
@@ -864,7 +850,6 @@ cudaError_t launch_kv_attention(const kv::Args& a, bool q8, const uint16_t* q, l
   const long long rows = static_cast<long long>(a.num_pages) * a.heads * a.page_size;
   if (!encode_pool(&tk, a.k, rows, a.d, g.chunk, q8) || !encode_pool(&tv, a.v, rows, a.d, g.chunk, q8))
     return cudaErrorInvalidValue;
-  const int ctas = num_sms();
   if (a.d == 64) return q8 ? launch<64, true>(a, g, tk, tv, ctas, s) : launch<64, false>(a, g, tk, tv, ctas, s);
   return q8 ? launch<128, true>(a, g, tk, tv, ctas, s) : launch<128, false>(a, g, tk, tv, ctas, s);
 }

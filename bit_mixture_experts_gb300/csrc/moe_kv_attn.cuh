@@ -13,7 +13,8 @@ struct AttnArgs {
   long long q_token, q_head;
   uint16_t* out;
   float* lse;
-  float* part;  // workspace: two slots per CTA
+  int4* joins;  // workspace: per CTA, the item that its last part begins (parts, first row, tokens, KV head)
+  float* part;  // and two slots for parts of items
   float scale_log2;
   int q_heads, group, tpt, chunk;  // chunk: rows of one copy, divides page_size and TILE
   unsigned long long wait_cycles;
@@ -56,7 +57,7 @@ struct Layout {
   //    thin form that waits for tile i skipped the tiles of the other team, but released tile i - 3 or a
   //    later one of its own, whose slot was filled after tile i - 2 N had landed (N >= 3);
   //  - whoever waits for QFULL[0] (the MMA warp and the softmax warps) does so for every segment, and
-  //    QEMPTY[0] needs all of them.
+  //    QEMPTY[0] needs all of them; QFULL[0] needs both loading warps, who wait for every QEMPTY[0].
   static constexpr int LFULL = 0, LEMPTY = LFULL + 2 * NL, HFULL = Q8 ? LEMPTY + NL : LFULL,
                        HEMPTY = Q8 ? HFULL + 2 * NH_ : LEMPTY, FULL = HEMPTY + NH_, EMPTY = FULL + (Q8 ? NS : 0),
                        SFULL = EMPTY + (Q8 ? NS : 0), PREADY = SFULL + 2, QFULL = PREADY + 2, QEMPTY = QFULL + 2,
@@ -71,6 +72,7 @@ struct Layout {
     if (i < EMPTY) return 4;
     if (i < SFULL) return 1;
     if (i >= PREADY && i < QFULL) return 4;
+    if (i == QFULL) return 2;
     if (i >= QEMPTY && i < OFULL) return i == QEMPTY ? 9 : 8;
     if (i >= FIX && i < TEAM) return 4;
     if (i == TEAM) return 8;
@@ -82,8 +84,8 @@ struct Layout {
   static constexpr int ML_OFF = SEG_OFF + 48 * SEGS;        // row maxima and sums (2 x 128 floats), flags (128 bytes)
   static constexpr int BYTES = ML_OFF + 9 * TILE + 1024;    // + alignment
   // registers per thread: 128 (Q8) or 168 at launch, moved to the two softmax warpgroups
-  static constexpr int REGS_SOFTMAX = Q8 ? 176 : 208, REGS_OTHER = Q8 ? 80 : 88;
-  static_assert(256 * REGS_SOFTMAX + (THREADS - 256) * REGS_OTHER <= THREADS * (Q8 ? 128 : 168), "register split");
+  static constexpr int REGS_SOFTMAX = Q8 ? 176 : 208, REGS_ISSUE = Q8 ? 96 : 88, REGS_EXPAND = Q8 ? 64 : 0;
+  static_assert(256 * REGS_SOFTMAX + 128 * (REGS_ISSUE + REGS_EXPAND) <= THREADS * (Q8 ? 128 : 168), "register split");
   static_assert(BYTES <= 232448, "shared memory of one CTA");
 };
 

@@ -5,8 +5,9 @@
 // query head r % G of the head's group of G (tpt = 128 / G tokens per tile), so
 // every key is read once for all query heads that share it.  An item is one
 // (sequence, KV head, pair of tiles); its units are the 128-key tiles that the
-// pair's last token sees.  All units of a call in the order sequence, head,
-// pair, key tile are one line, of which CTA c of n takes [W c / n, W (c+1) / n):
+// pair's last token sees, after START more for what an item costs whatever its
+// length.  All units of a call in the order sequence, head, pair, key tile are
+// one line, of which CTA c of n takes [W c / n, W (c+1) / n):
 // even shares whatever the lengths, an item being cut where a share ends
 // (its parts are merged afterwards).  Where all items are short it goes whole to
 // the CTA whose share it starts in: nothing to merge.  A pair that sees no key counts one unit,
@@ -20,6 +21,7 @@ namespace moe {
 namespace kv {
 
 constexpr int TILE = 128;  // query rows of a tile, keys of a tile
+constexpr int START = 2;   // an item's start and end (its queries, its output), in key tiles
 
 // Sum of floor((a i + b) / TILE) for i = 0 .. n-1, n <= 2^20, a <= 2 TILE (the Euclid-like recursion
 // on the slope).  After the first step every term but the sum itself fits 32 bits.
@@ -61,10 +63,12 @@ struct Pairs {
     int z = 0;  // pairs that see nothing
     if (base < 0) z = min(mp, -base / tp);
     const long long first = base + (z + 1ll) * tp + TILE - 1;
-    return z + floor_sum(mp - z, tp, first);
+    return static_cast<long long>(mp) * START + z + floor_sum(mp - z, tp, first);
   }
 
-  __device__ __forceinline__ long long units() const { return M == 0 ? 0 : before(M - 1) + tiles(M - 1); }
+  __device__ __forceinline__ long long units() const {
+    return M == 0 ? 0 : before(M - 1) + START + tiles(M - 1);
+  }
 
   // The pair that unit r (of one head) belongs to.
   __device__ __forceinline__ int find(long long r) const {
@@ -94,46 +98,45 @@ __device__ __forceinline__ long long divide(long long x, long long y) {
 
 // Walks the segments of units [u, end), starting in sequence b whose first unit is b_lo.
 struct Walk {
-  const Args* ap;
+  const Args* a;
   int tp, b;
   long long u, end, b_lo, b_hi, per_head;
+  long long item_end;  // the last segment's item's last unit, plus one
   Seq s;
   bool whole;
 
   __device__ __forceinline__ Walk(const Args& a_, int tp_, long long u_, long long end_, int b_, long long b_lo_,
                                   bool whole_)
-      : ap(&a_), tp(tp_), b(b_ - 1), u(u_), end(end_), b_lo(0), b_hi(b_lo_), per_head(0), whole(whole_) {}
+      : a(&a_), tp(tp_), b(b_ - 1), u(u_), end(end_), b_lo(0), b_hi(b_lo_), per_head(0), item_end(0), whole(whole_) {}
 
-  // `whole`: items that start in [u, end), each in full; otherwise units [u, end).
+  // `whole`: items that start in [u, end), each in full; otherwise the key tiles among units [u, end).
   __device__ __forceinline__ bool next(Seg& g) {
     for (;;) {
       if (u >= end) return false;
-      step(g);
-      if (!whole || g.t0 == 0) return true;
+      while (u >= b_hi) {
+        s = load_seq(*a, ++b);
+        per_head = Pairs(s, tp).units();
+        b_lo = b_hi;
+        b_hi += per_head * a->heads;
+      }
+      const Pairs p(s, tp);
+      const long long v = u - b_lo, h = divide(v, per_head), r = v - h * per_head;
+      const int mp = p.find(r), off = static_cast<int>(r - p.before(mp));
+      g.row0 = s.row0;
+      g.len = s.len;
+      g.b = b;
+      g.h = static_cast<int>(h);
+      g.i0 = mp * tp;
+      g.ntok = min(tp, s.n - g.i0);
+      g.base = s.len - s.n + g.i0;
+      g.nt = p.tiles(mp);
+      item_end = u - off + START + g.nt;
+      const long long stop = whole ? item_end : min(item_end, end);
+      g.t0 = max(0, off - START);
+      g.t1 = static_cast<int>(off - START + (stop - u));
+      u = stop;
+      if (whole ? off == 0 : g.t1 > g.t0) return true;
     }
-  }
-
-  __device__ __forceinline__ void step(Seg& g) {
-    while (u >= b_hi) {
-      s = load_seq(*ap, ++b);
-      per_head = Pairs(s, tp).units();
-      b_lo = b_hi;
-      b_hi += per_head * ap->heads;
-    }
-    const Pairs p(s, tp);
-    const long long v = u - b_lo, h = divide(v, per_head), r = v - h * per_head;
-    const int mp = p.find(r);
-    g.row0 = s.row0;
-    g.len = s.len;
-    g.b = b;
-    g.h = static_cast<int>(h);
-    g.i0 = mp * tp;
-    g.ntok = min(tp, s.n - g.i0);
-    g.base = s.len - s.n + g.i0;
-    g.nt = p.tiles(mp);
-    g.t0 = static_cast<int>(r - p.before(mp));
-    g.t1 = whole ? g.nt : static_cast<int>(min(static_cast<long long>(g.nt), g.t0 + (end - u)));
-    u += g.t1 - g.t0;
   }
 };
 
@@ -155,6 +158,11 @@ struct Share {
     whole = longest <= WHOLE + each / 16;
   }
   __device__ __forceinline__ long long lo(int c) const { return each * c + min(c, more); }
+  // The CTA whose share holds unit u.
+  __device__ __forceinline__ int of(long long u) const {
+    const long long edge = (each + 1) * more;
+    return static_cast<int>(u < edge ? divide(u, each + 1) : more + divide(u - edge, each));
+  }
 };
 
 // A unit's sequence and that sequence's first unit.
@@ -164,7 +172,7 @@ struct Start {
 };
 
 // Sets `share` and finds the sequence that holds unit share.lo(cut), if there is such a share.  All
-// threads of the block; `scratch`: 50 long longs of shared memory, free again on return.  Up to 32
+// threads of the block, or up to 32 sequences any whole warps of it; `scratch`: 50 long longs of shared memory, free again on return.  Up to 32
 // sequences every warp works it out for itself, a sequence per lane; more are dealt to the block's threads.
 template <int NT>
 __device__ __forceinline__ Start locate(const Args& a, int tp, int grid, int cut, long long* scratch, Share& share) {
