@@ -29,6 +29,8 @@
 #include <cuda.h>
 #include <string.h>
 
+#include <type_traits>
+
 #include "moe_kv_attn.cuh"
 #include "moe_kv_thin.cuh"
 #include "moe_tmap.cuh"
@@ -217,90 +219,122 @@ __global__ void __launch_bounds__(Layout<D, Q8>::THREADS, 1)
     } else if (warp == 1) {
       // ---------------------------------------------- MMA issue, one unit behind for P V
       // A unit's tiles: a and b (a pair), or one of them (t alternates along the keys).
+      // All operands are warp-uniform, and the tiles known at compile time: an MMA whose operands have to
+      // be brought to the uniform registers lane by lane takes longer to issue than to run.
       const uint32_t id_s = ptx::idesc_bf16_f32(TILE, TILE), id_o = idesc_pv(D);
-      uint32_t p_ph[2] = {0, 0}, qb_ph = 0;
-      int ki = 0;  // the current unit's K in the bf16 ring, V next to it
-      struct {
-        int tiles, vi;     // bit mask of tiles whose P V is still to do; V in the ring
-        bool first, last;  // of the item's run for its tiles
-      } prev = {0, 0, false, false};
-      auto full = [&](int i) -> bool {
-        return Q8 ? wait(L::FULL + i % NS, (i / NS) & 1) : wait(L::LFULL + i % (2 * NS), (i / (2 * NS)) & 1);
+      const uint32_t tm = static_cast<uint32_t>(uniform(static_cast<int>(tmem)));
+      const uint64_t q_desc = ptx::smem_desc_sw128(sbase + L::Q_OFF), k_desc = ptx::smem_desc_sw128(sbase + L::KV_OFF);
+      const uint64_t v_desc = desc_mn_sw128(sbase + L::KV_OFF, PANEL);
+      uint32_t pa_ph = 0, pb_ph = 0, qb_ph = 0;
+      // the current unit's K: slot of the bf16 ring, its barrier (twice as many for bf16), the round's parity
+      constexpr int BARS = Q8 ? NS : 2 * NS, FULL0 = Q8 ? L::FULL : L::LFULL, EMPTY0 = Q8 ? L::EMPTY : L::LEMPTY;
+      int st = 0, fl = 0, ph = 0;
+      auto advance = [&](int by) {
+        st += by;
+        while (st >= NS) st -= NS;
+        fl += by;
+        while (fl >= BARS) {
+          fl -= BARS;
+          ph ^= 1;
+        }
       };
+      // the previous unit: tiles whose P V is still to do, V's slot, barrier and parity, first and last of
+      // the item's run for its tiles
+      int todo = 0, v_st = 0, v_fl = 0, v_ph = 0;
+      bool v_first = false, v_last = false;
       // releases a ring tile once the MMAs issued so far are done with it
-      auto release = [&](int i) {
-        const uint32_t b = bar((Q8 ? L::EMPTY : L::LEMPTY) + i % NS);
-        if (!Q8 && lane == 0) mbar_arrive_n(b, 7);
-        ptx::mma_commit_elect(b);
+      auto release = [&](int slot) {
+        if (!Q8 && lane == 0) mbar_arrive_n(bar(EMPTY0 + slot), 7);
+        ptx::mma_commit_elect(bar(EMPTY0 + slot));
       };
       // O += P V of the previous unit for tile t
-      auto finish = [&](int t) -> bool {
-        if (!(prev.tiles >> t & 1)) return true;
-        if (!full(prev.vi) || !wait(L::PREADY + t, p_ph[t])) return false;
-        p_ph[t] ^= 1;
+      auto finish = [&](auto tile) -> bool {
+        constexpr int t = decltype(tile)::value;
+        if (!(todo & (1 << t))) return true;
+        uint32_t& p_ph = t == 0 ? pa_ph : pb_ph;
+        if (!wait(FULL0 + v_fl, v_ph) || !wait(L::PREADY + t, p_ph)) return false;
+        p_ph ^= 1;
         ptx::tc_fence_after();
-        const uint32_t o = tmem + TM_O + t * D, p = tmem + TM_S + t * TILE;
-        const uint64_t d = desc_mn_sw128(sbase + L::KV_OFF + prev.vi % NS * TB, PANEL);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) mma_pv2_elect(o, p + 16 * j, d + 256 * j, id_o, (j > 0 || !prev.first) ? 1u : 0u);
-        if (prev.last) ptx::mma_commit_elect(bar(L::OFULL + t));
-        prev.tiles &= ~(1 << t);
-        if (prev.tiles == 0) release(prev.vi);
+        mma_pv_elect(tm + TM_O + t * D, tm + TM_S + t * TILE, v_desc + static_cast<uint32_t>(v_st * (TB >> 4)), id_o,
+                     v_first ? 0u : 1u);
+        if (v_last) ptx::mma_commit_elect(bar(L::OFULL + t));
+        todo &= ~(1 << t);
+        if (todo == 0) release(v_st);
         return true;
       };
       // S = Q K^T of the current unit into tile t's scores, from query tile q
-      auto scores = [&](int t, int q, bool last) {
-        const uint64_t dq = ptx::smem_desc_sw128(sbase + L::Q_OFF + q * TB);
-        const uint64_t dk = ptx::smem_desc_sw128(sbase + L::KV_OFF + ki % NS * TB);
-#pragma unroll
-        for (int hf = 0; hf < NH; ++hf)
-          ptx::mma_group_ss_elect(tmem + TM_S + t * TILE, dq + hf * (PANEL >> 4), dk + hf * (PANEL >> 4), id_s,
-                                  hf ? 1u : 0u);
+      auto scores = [&](auto tile, auto query, bool last) {
+        constexpr int t = decltype(tile)::value, q = decltype(query)::value;
+        ptx::tc_fence_after();
+        const uint64_t dk = k_desc + static_cast<uint32_t>(st * (TB >> 4));
+        if (NH == 2)
+          mma_qk2_elect(tm + TM_S + t * TILE, q_desc + q * (TB >> 4), dk, id_s);
+        else
+          ptx::mma_group_ss_elect(tm + TM_S + t * TILE, q_desc + q * (TB >> 4), dk, id_s, 0u);
         ptx::mma_commit_elect(bar(L::SFULL + t));
         if (last) {
           if (q == 1 && lane == 0) mbar_arrive_n(bar(L::QEMPTY + 1), 7);
           ptx::mma_commit_elect(bar(L::QEMPTY + q));
         }
       };
+      const std::integral_constant<int, 0> A;
+      const std::integral_constant<int, 1> B;
+      // the current unit becomes the previous one
+      auto pass = [&](int tiles, bool first, bool last) {
+        advance(1);
+        todo = tiles;
+        v_st = st;
+        v_fl = fl;
+        v_ph = ph;
+        v_first = first;
+        v_last = last;
+        advance(1);
+      };
       bool ok = true, tiles_before = false;  // tiles_before: the last segment was of the tile form
       while (ok && next(sg)) {
+        const uint32_t seg_ph = (segs - 1) & 1;
+        const int run = sg.t1 - sg.t0;
         if (thin(sg)) {
           // the softmax warps' own; its tiles pass by, and what is pending must not wait for it
-          ok = finish(0) && finish(1) && wait(L::QFULL, (segs - 1) & 1);
+          ok = finish(A) && finish(B) && wait(L::QFULL, seg_ph);
           if (ok && lane == 0) ptx::mbar_arrive(bar(L::QEMPTY));
           if (Q8 && tiles_before) ptx::mma_commit_elect(bar(L::TCDONE));
           tiles_before = false;
-          if (!Q8) ki += 2 * (sg.t1 - sg.t0);
+          if (!Q8) advance(2 * run % BARS), ph ^= 2 * run / BARS & 1;
           continue;
         }
         tiles_before = true;
-        const bool pair = sg.ntok > g.tpt;
-        for (int kt = sg.t0; kt < sg.t1; ++kt) {
-          const int j = kt - sg.t0;
-          const bool last = kt + 1 == sg.t1;
-          const int t = pair ? 0 : j & 1;
-          // the scores of the next unit come before the previous unit's P V, unless they share a buffer
-          ok = finish(t) && (j > 0 || wait(L::QFULL, (segs - 1) & 1)) && full(ki);
-          if (!ok) break;
-          ptx::tc_fence_after();
-          scores(t, 0, last);
-          if (pair) {
-            ok = finish(1) && (j > 0 || wait(L::QFULL + 1, qb_ph));
-            if (!ok) break;
+        if (sg.ntok > g.tpt) {
+          for (int j = 0; j < run; ++j) {
+            const bool last = j + 1 == run;
+            if (!(ok = finish(A) && (j > 0 || wait(L::QFULL, seg_ph)) && wait(FULL0 + fl, ph))) break;
+            scores(A, A, last);
+            if (!(ok = finish(B) && (j > 0 || wait(L::QFULL + 1, qb_ph)))) break;
             if (j == 0) qb_ph ^= 1;
-            ptx::tc_fence_after();
-            scores(1, 1, last);
+            scores(B, B, last);
+            release(st);
+            pass(3, j == 0, last);
           }
-          release(ki);
-          if (!pair && !(ok = finish(t ^ 1))) break;
-          prev.tiles = pair ? 3 : 1 << t;
-          prev.vi = ki + 1;
-          prev.first = j < (pair ? 1 : 2);
-          prev.last = kt + (pair ? 1 : 2) >= sg.t1;
-          ki += 2;
+        } else {
+          // the scores of the next unit come before the previous unit's P V, which has the other buffer
+          for (int j = 0; j < run; ++j) {
+            const bool last = j + 1 == run;
+            if (j & 1) {
+              if (!(ok = finish(B) && wait(FULL0 + fl, ph))) break;
+              scores(B, A, last);
+              release(st);
+              if (!(ok = finish(A))) break;
+            } else {
+              if (!(ok = finish(A) && (j > 0 || wait(L::QFULL, seg_ph)) && wait(FULL0 + fl, ph))) break;
+              scores(A, A, last);
+              release(st);
+              if (!(ok = finish(B))) break;
+            }
+            pass(1 << (j & 1), j < 2, j + 2 >= run);
+          }
         }
       }
-      if (ok) ok = finish(0) && finish(1);
+      if (ok) ok = finish(A) && finish(B);
       // all MMAs are done before the tensor memory is released
       ptx::mma_commit_elect(bar(L::DRAIN));
       tc_dev::wait_drain(bar(L::DRAIN), 0, 0);

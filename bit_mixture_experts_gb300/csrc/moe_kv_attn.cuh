@@ -106,18 +106,51 @@ __device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t saddr, uint32_t panel
   return d;
 }
 
-// Two K16 steps of O += P V: P columns a, a + 8; V keys 16 further (2048 bytes) per step.
-__device__ __forceinline__ void mma_pv2_elect(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+// O += P V: eight K16 steps, P columns 8 and V keys 16 (2048 bytes) further per step; the first step keeps
+// O only if `accumulate` is non-zero.
+__device__ __forceinline__ void mma_pv_elect(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p, q, e;\n\t.reg .b32 x;\n\t.reg .b64 c;\n\t"
+      "{\n\t.reg .pred p, q, e;\n\t.reg .b32 x1, x2, x3, x4, x5, x6, x7;\n\t"
+      ".reg .b64 c1, c2, c3, c4, c5, c6, c7;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
       "setp.ne.b32 q, %3, 0;\n\t"
-      "add.u32 x, %1, 8;\n\t"
-      "add.s64 c, %2, 128;\n\t"
+      "add.u32 x1, %1, 8;\n\tadd.u32 x2, %1, 16;\n\tadd.u32 x3, %1, 24;\n\tadd.u32 x4, %1, 32;\n\t"
+      "add.u32 x5, %1, 40;\n\tadd.u32 x6, %1, 48;\n\tadd.u32 x7, %1, 56;\n\t"
+      "add.s64 c1, %2, 128;\n\tadd.s64 c2, %2, 256;\n\tadd.s64 c3, %2, 384;\n\tadd.s64 c4, %2, 512;\n\t"
+      "add.s64 c5, %2, 640;\n\tadd.s64 c6, %2, 768;\n\tadd.s64 c7, %2, 896;\n\t"
       "elect.sync _|e, 0xffffffff;\n\t"
       "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], c, %3, q;\n\t}" ::"r"(d),
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x1], c1, %3, q;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x2], c2, %3, q;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x3], c3, %3, q;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x4], c4, %3, q;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x5], c5, %3, q;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x6], c6, %3, q;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x7], c7, %3, q;\n\t}" ::"r"(d),
       "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// S = Q K^T for d = 128: eight K16 steps over two panels (1024 descriptor units apart).
+__device__ __forceinline__ void mma_qk2_elect(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
+  asm volatile(
+      "{\n\t.reg .pred p, q, e;\n\t.reg .b64 a1, a2, a3, a4, a5, a6, a7, c1, c2, c3, c4, c5, c6, c7;\n\t"
+      "setp.eq.b32 p, %3, 0;\n\t"
+      "setp.ne.b32 q, %3, 0;\n\t"
+      "add.s64 a1, %1, 2;\n\tadd.s64 a2, %1, 4;\n\tadd.s64 a3, %1, 6;\n\tadd.s64 a4, %1, 1024;\n\t"
+      "add.s64 a5, %1, 1026;\n\tadd.s64 a6, %1, 1028;\n\tadd.s64 a7, %1, 1030;\n\t"
+      "add.s64 c1, %2, 2;\n\tadd.s64 c2, %2, 4;\n\tadd.s64 c3, %2, 6;\n\tadd.s64 c4, %2, 1024;\n\t"
+      "add.s64 c5, %2, 1026;\n\tadd.s64 c6, %2, 1028;\n\tadd.s64 c7, %2, 1030;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a1, c1, %3, q;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a2, c2, %3, q;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a3, c3, %3, q;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a4, c4, %3, q;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a5, c5, %3, q;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a6, c6, %3, q;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a7, c7, %3, q;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc)
       : "memory");
 }
 
