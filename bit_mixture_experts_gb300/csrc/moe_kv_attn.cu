@@ -90,7 +90,7 @@ __global__ void __launch_bounds__(Layout<D, Q8>::THREADS, 1)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   auto wait = [&](int i, uint32_t parity) -> bool {
-    return tc_dev::wait_warp(bar(i), parity, s_abort, a.err, g.wait_cycles, g.sleep_ns);
+    return wait_warp(bar(i), parity, s_abort, a.err, g);
   };
   // the CTA's segments, in order, as warp 0 publishes them
   int segs = 0;  // taken so far
@@ -307,7 +307,7 @@ __global__ void __launch_bounds__(Layout<D, Q8>::THREADS, 1)
         if (sg.ntok > g.tpt) {
           for (int j = 0; j < run; ++j) {
             const bool last = j + 1 == run;
-            if (!(ok = finish(A) && (j > 0 || wait(L::QFULL, seg_ph)) && wait(FULL0 + fl, ph))) break;
+            if (!(ok = (j > 0 || wait(L::QFULL, seg_ph)) && wait(FULL0 + fl, ph) && finish(A))) break;
             scores(A, A, last);
             if (!(ok = finish(B) && (j > 0 || wait(L::QFULL + 1, qb_ph)))) break;
             if (j == 0) qb_ph ^= 1;
@@ -877,7 +877,7 @@ cudaError_t launch_kv_attention(const kv::Args& a, bool q8, const uint16_t* q, l
   if (g.chunk > TILE) g.chunk = TILE;
   const unsigned long long ns = wait_limit_ns();
   g.wait_cycles = ns > (~0ull) / 3 ? ~0ull : ns * 21 / 10;
-  g.sleep_ns = ns < 20000ull ? static_cast<uint32_t>(ns > 0 ? ns : 1) : 20000u;
+  g.poll = ns < 20000ull;
   CUtensorMap tk, tv;
   memset(&tk, 0, sizeof(tk));
   memset(&tv, 0, sizeof(tv));

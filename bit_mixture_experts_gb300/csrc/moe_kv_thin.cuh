@@ -82,7 +82,7 @@ __device__ __forceinline__ bool thin_segment(const Args& a, const AttnArgs& g, c
   const uint32_t sbase = x.sbase;
   auto bar = [sbase](int i) -> uint32_t { return sbase + L::BAR_OFF + 8u * static_cast<uint32_t>(i); };
   auto wait = [&](int i, uint32_t parity) -> bool {
-    return tc_dev::wait_warp(bar(i), parity, x.s_abort, a.err, g.wait_cycles, g.sleep_ns);
+    return wait_warp(bar(i), parity, x.s_abort, a.err, g);
   };
   auto team = [&]() -> bool {
     __syncwarp();
