@@ -61,33 +61,58 @@ __device__ __forceinline__ int find_place(const kv::Args& a, int t) {
   return page < 0 ? -1 : page * a.heads * a.page_size + p - e * a.page_size;
 }
 
+constexpr int FLIGHT = 4;  // row loads of a lane in flight
+
+// Walks a warp's (token, group of RPW rows) pairs in order, FLIGHT at a time.
+struct Step {
+  int i, r0;  // token of the warp, first row
+  __device__ __forceinline__ void next(int rows, int rpw) {
+    r0 += rpw;
+    if (r0 >= rows) {
+      r0 = 0;
+      ++i;
+    }
+  }
+};
+
 template <int D, bool Q8>
 __global__ void __launch_bounds__(KV_THREADS) kv_append_kernel(const kv::Args a, const NewRows in, int tokens) {
   constexpr int C = D / 8, RPW = 32 / C;  // lanes of a row, rows at a time
   const int warp = (blockIdx.x * KV_THREADS + threadIdx.x) >> 5, lane = threadIdx.x & 31;
-  const int t0 = warp * tokens, c = lane % C;
+  const int t0 = warp * tokens, c = lane % C, rows = 2 * a.heads;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (t0 >= a.T) return;
   const int mine = lane < tokens ? find_place(a, t0 + lane) : -2;
-  for (int i = 0; i < tokens; ++i) {
-    const int place = __shfl_sync(0xffffffffu, mine, i), t = t0 + i;
-    if (place < 0) continue;
-#pragma unroll 4
-    for (int r0 = 0; r0 < 2 * a.heads; r0 += RPW) {
-      const int r = r0 + lane / C;
-      const bool live = r < 2 * a.heads, is_v = r >= a.heads;
-      const int h = is_v ? r - a.heads : r;
-      const uint16_t* src = is_v ? in.v + t * in.v_token + h * in.v_head : in.k + t * in.k_token + h * in.k_head;
-      const uint4 x = live ? __ldg(reinterpret_cast<const uint4*>(src) + c) : make_uint4(0, 0, 0, 0);
-      const size_t at = static_cast<size_t>(place) + h * a.page_size;
+  Step s = {0, 0};
+  while (s.i < tokens) {
+    uint4 x[FLIGHT];
+    int place[FLIGHT], row[FLIGHT];  // place: of the token, -1 for none; row: of the token's rows
+#pragma unroll
+    for (int u = 0; u < FLIGHT; ++u) {
+      const int r = s.r0 + lane / C, t = t0 + s.i;
+      place[u] = __shfl_sync(0xffffffffu, mine, s.i & 31);
+      if (s.i >= tokens || r >= rows) place[u] = -1;
+      row[u] = r;
+      x[u] = make_uint4(0, 0, 0, 0);
+      if (place[u] >= 0) {
+        const uint16_t* src =
+            r >= a.heads ? in.v + t * in.v_token + (r - a.heads) * in.v_head : in.k + t * in.k_token + r * in.k_head;
+        x[u] = __ldg(reinterpret_cast<const uint4*>(src) + c);
+      }
+      s.next(rows, RPW);
+    }
+#pragma unroll
+    for (int u = 0; u < FLIGHT; ++u) {
+      const bool live = place[u] >= 0, is_v = row[u] >= a.heads;
+      const size_t at = static_cast<size_t>(max(place[u], 0)) + (is_v ? row[u] - a.heads : row[u]) * a.page_size;
       if (!Q8) {
-        if (live) reinterpret_cast<uint4*>(is_v ? a.v : a.k)[at * C + c] = x;
+        if (live) reinterpret_cast<uint4*>(is_v ? a.v : a.k)[at * C + c] = x[u];
         continue;
       }
-      const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+      const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
       uint32_t amax = 0;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) amax = max(amax, max(u[j] & 0x7fffu, (u[j] >> 16) & 0x7fffu));
+      for (int j = 0; j < 4; ++j) amax = max(amax, max(w[j] & 0x7fffu, (w[j] >> 16) & 0x7fffu));
 #pragma unroll
       for (int m = C / 2; m >= 1; m >>= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, m));
       uint32_t inv_bits;
@@ -97,7 +122,7 @@ __global__ void __launch_bounds__(KV_THREADS) kv_append_kernel(const kv::Args a,
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         uint16_t lo, hi;
-        const uint32_t p = u[2 * j], q = u[2 * j + 1];
+        const uint32_t p = w[2 * j], q = w[2 * j + 1];
         asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;"
             : "=h"(lo)
             : "f"(__uint_as_float(p & 0xffff0000u) * inv), "f"(__uint_as_float(p << 16) * inv));
@@ -119,30 +144,44 @@ __global__ void __launch_bounds__(KV_THREADS) kv_read_kernel(const kv::Args a, u
                                                              uint16_t* __restrict__ v_out, int tokens) {
   constexpr int C = Q8 ? D / 16 : D / 8, RPW = 32 / C;  // 16-byte pieces of a stored row
   const int warp = (blockIdx.x * KV_THREADS + threadIdx.x) >> 5, lane = threadIdx.x & 31;
-  const int t0 = warp * tokens, c = lane % C;
+  const int t0 = warp * tokens, c = lane % C, rows = 2 * a.heads;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (t0 >= a.T) return;
   const int mine = lane < tokens ? find_place(a, t0 + lane) : -2;
-  for (int i = 0; i < tokens; ++i) {
-    const int place = __shfl_sync(0xffffffffu, mine, i), t = t0 + i;
-    if (place == -2) continue;
-#pragma unroll 4
-    for (int r = lane / C; r < 2 * a.heads; r += RPW) {
+  Step s = {0, 0};
+  while (s.i < tokens) {
+    uint4 x[FLIGHT];
+    float scale[FLIGHT];
+    int token[FLIGHT], row[FLIGHT];  // token -1: nothing to do
+#pragma unroll
+    for (int u = 0; u < FLIGHT; ++u) {
+      const int r = s.r0 + lane / C, place = __shfl_sync(0xffffffffu, mine, s.i & 31);
       const bool is_v = r >= a.heads;
-      const int h = is_v ? r - a.heads : r;
-      const size_t at = static_cast<size_t>(max(place, 0)) + h * a.page_size;
+      token[u] = s.i < tokens && r < rows && place != -2 ? t0 + s.i : -1;
+      row[u] = r;
+      x[u] = make_uint4(0, 0, 0, 0);
+      scale[u] = 1.f;
+      if (token[u] >= 0 && place >= 0) {
+        const size_t at = static_cast<size_t>(place) + (is_v ? r - a.heads : r) * a.page_size;
+        x[u] = __ldg(reinterpret_cast<const uint4*>(is_v ? a.v : a.k) + at * C + c);
+        if (Q8) scale[u] = __ldg((is_v ? a.v_scale : a.k_scale) + at);
+      }
+      s.next(rows, RPW);
+    }
+#pragma unroll
+    for (int u = 0; u < FLIGHT; ++u) {
+      if (token[u] < 0) continue;
+      const bool is_v = row[u] >= a.heads;
       uint4* dst = reinterpret_cast<uint4*>(is_v ? v_out : k_out) +
-                   (static_cast<size_t>(t) * a.heads + h) * (D / 8) + (Q8 ? 2 * c : c);
-      uint4 x = make_uint4(0, 0, 0, 0);
-      if (place >= 0) x = reinterpret_cast<const uint4*>(is_v ? a.v : a.k)[at * C + c];
+                   (static_cast<size_t>(token[u]) * a.heads + (is_v ? row[u] - a.heads : row[u])) * (D / 8) + (Q8 ? 2 * c : c);
       if (!Q8) {
-        *dst = x;
+        *dst = x[u];
         continue;
       }
-      uint32_t s1 = 0, s2 = 0;
-      if (place >= 0) kv::scale_pairs((is_v ? a.v_scale : a.k_scale)[at], &s1, &s2);
-      const uint2 v0 = kv::expand4(x.x, s1), v1 = kv::expand4(x.y, s1);
-      const uint2 v2 = kv::expand4(x.z, s1), v3 = kv::expand4(x.w, s1);
+      uint32_t s1, s2;
+      kv::scale_pairs(scale[u], &s1, &s2);
+      const uint2 v0 = kv::expand4(x[u].x, s1), v1 = kv::expand4(x[u].y, s1);
+      const uint2 v2 = kv::expand4(x[u].z, s1), v3 = kv::expand4(x[u].w, s1);
       dst[0] = make_uint4(kv::bf16x2_mul(v0.x, s2), kv::bf16x2_mul(v0.y, s2), kv::bf16x2_mul(v1.x, s2),
                           kv::bf16x2_mul(v1.y, s2));
       dst[1] = make_uint4(kv::bf16x2_mul(v2.x, s2), kv::bf16x2_mul(v2.y, s2), kv::bf16x2_mul(v3.x, s2),
@@ -151,8 +190,13 @@ __global__ void __launch_bounds__(KV_THREADS) kv_read_kernel(const kv::Args a, u
   }
 }
 
-// Tokens per warp: as many as leave every SM a few dozen warps.
-int tokens_per_warp(int T) { return T >= 16 * 4096 ? 16 : T >= 4 * 2048 ? 4 : 1; }
+// Tokens per warp: 1 to 16, as many as leave 16384 warps or more (about 100 per SM: with half as many the
+// read of 131071 e4m3 tokens takes 41 us, not 36).
+int tokens_per_warp(int T) {
+  int n = 1;
+  while (n < 16 && T / (2 * n) >= 16384) n *= 2;
+  return n;
+}
 
 // A grid of one warp per `tokens` tokens, started while the kernel before it in the stream ends (the
 // kernels wait for its results themselves).

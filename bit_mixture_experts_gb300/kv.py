@@ -102,9 +102,9 @@ class PagedKVCache:
     def _empty(self, shape, dtype, stream):
         """An output for a call on `stream`: allocated as memory of that stream."""
         if stream is None:
-            return self.k.new_empty(shape, dtype=dtype)
+            return torch.empty(shape, dtype=dtype, device=self.device)
         with torch.cuda.stream(stream):
-            return self.k.new_empty(shape, dtype=dtype)
+            return torch.empty(shape, dtype=dtype, device=self.device)
 
     def _workspace(self, stream):
         """(pointer, bytes) of the attention's scratch for calls on `stream`: one per stream, so that calls on
@@ -143,7 +143,8 @@ class PagedKVCache:
         ``moe_kv_attention_workspace_size(d)``) replaces the cache's own scratch of the stream."""
         self._rows(q, "q", batch)
         if out is None:
-            out = self._empty(q.shape, torch.bfloat16, stream)
+            out = (torch.empty_like(q, memory_format=torch.contiguous_format) if stream is None
+                   else self._empty(q.shape, torch.bfloat16, stream))
         else:
             self._rows(out, "out", batch, q.shape[1])
             if not out.is_contiguous():
