@@ -93,7 +93,7 @@ _SIGS = {
     "moe_kv_append": ([_vp, _i64, _i64, _vp, _i64, _i64] + _kv + [_vp], _i),
     "moe_kv_read": ([_vp, _vp] + _kv + [_vp], _i),
     "moe_kv_attention": ([_vp, _i64, _i64, _i, ctypes.c_float] + _kv + [_vp, _vp, _vp, _sz, _vp], _i),
-    "moe_kv_attention_workspace_size": ([_i], _sz),
+    "moe_kv_attention_workspace_size": (_kv + [_i], _sz),
     "moe_get_device_error": ([ctypes.POINTER(ctypes.c_int32)], _i),
     "moe_set_wait_limit_ns": ([ctypes.c_uint64], None),
     "moe_trace_words": ([], ctypes.c_size_t),
@@ -290,8 +290,8 @@ def moe_kv_read(k, v, cache: KVCache, batch: KVBatch, stream=None):
     _call("moe_kv_read", k.data_ptr(), v.data_ptr(), cache, batch, _stream(stream))
 
 
-def moe_kv_attention_workspace_size(d) -> int:
-    return int(load().moe_kv_attention_workspace_size(d))
+def moe_kv_attention_workspace_size(cache: KVCache, batch: KVBatch, q_heads) -> int:
+    return int(load().moe_kv_attention_workspace_size(cache, batch, q_heads))
 
 
 def moe_kv_attention(q, scale, cache: KVCache, batch: KVBatch, out, lse, workspace, stream=None):

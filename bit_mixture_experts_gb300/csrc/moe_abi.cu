@@ -107,7 +107,7 @@ cudaError_t launch_kv_append(const kv::Args& a, bool q8, const uint16_t* k, long
 cudaError_t launch_kv_read(const kv::Args& a, bool q8, uint16_t* k, uint16_t* v, cudaStream_t s);
 cudaError_t launch_kv_attention(const kv::Args& a, bool q8, const uint16_t* q, long long q_token, long long q_head,
                                 int q_heads, float scale, uint16_t* out, float* lse, void* ws, cudaStream_t s);
-size_t kv_attention_workspace_bytes(int d);
+size_t kv_attention_workspace_bytes(const kv::Args& a, bool q8, int q_heads);
 
 namespace {
 
@@ -145,6 +145,8 @@ int kv_args(const moe_kv_cache_t* c, const moe_kv_batch_t* b, kv::Args* a) {
   a->B = b->B;
   a->table_width = b->table_width;
   a->T = b->T;
+  a->most = b->table_width * c->page_size;
+  a->in_order = false;
   return MOE_OK;
 }
 
@@ -420,7 +422,11 @@ int moe_kv_read(uint16_t* k, uint16_t* v, const moe_kv_cache_t* cache, const moe
       launch_kv_read(a, cache->format == MOE_KV_E4M3, k, v, reinterpret_cast<cudaStream_t>(stream)));
 }
 
-size_t moe_kv_attention_workspace_size(int d) { return d == 64 || d == 128 ? kv_attention_workspace_bytes(d) : 0; }
+size_t moe_kv_attention_workspace_size(const moe_kv_cache_t* cache, const moe_kv_batch_t* batch, int q_heads) {
+  kv::Args a;
+  if (kv_args(cache, batch, &a) || q_heads < 1 || q_heads % a.heads != 0) return 0;
+  return kv_attention_workspace_bytes(a, cache->format == MOE_KV_E4M3, q_heads);
+}
 
 int moe_kv_attention(const uint16_t* q, int64_t q_token_stride, int64_t q_head_stride, int q_heads, float scale,
                      const moe_kv_cache_t* cache, const moe_kv_batch_t* batch, uint16_t* out, float* lse,
@@ -435,12 +441,10 @@ int moe_kv_attention(const uint16_t* q, int64_t q_token_stride, int64_t q_head_s
   rc = check_ptrs(q, out);
   if (rc) return rc;
   if (reinterpret_cast<uintptr_t>(lse) & 3u) return MOE_ERR_ALIGN;
-  const size_t need = kv_attention_workspace_bytes(a.d);
-  if (need > 0) {
-    if (workspace_bytes < need) return MOE_ERR_WORKSPACE;
-    rc = check_ptrs(workspace);
-    if (rc) return rc;
-  }
+  if (workspace_bytes < kv_attention_workspace_bytes(a, cache->format == MOE_KV_E4M3, q_heads))
+    return MOE_ERR_WORKSPACE;
+  rc = check_ptrs(workspace);
+  if (rc) return rc;
   if (!(a.err = device_error_ptr())) return MOE_ERR_CUDA;
   return cuda_status(launch_kv_attention(a, cache->format == MOE_KV_E4M3, q, q_token_stride, q_head_stride, q_heads,
                                          scale, out, lse, workspace, reinterpret_cast<cudaStream_t>(stream)));

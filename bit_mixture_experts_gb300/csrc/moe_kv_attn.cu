@@ -154,18 +154,13 @@ __global__ void __launch_bounds__(Layout<D, Q8>::THREADS, 1)
         Ring rg = now ? thin_ring : tile_ring;
         const int slots = now ? L::NH_ : L::NL, full0 = now ? L::HFULL : L::LFULL, empty0 = now ? L::HEMPTY : L::LEMPTY;
         const uint32_t ring0 = sbase + (now ? L::H_OFF : L::L_OFF);
-        const int32_t* table = a.page_table + static_cast<size_t>(sg.b) * a.table_width;
         const int last = ceil_div(sg.len, g.chunk);  // chunks of the sequence
         int c0 = sg.t0 * per_tile;
         // the pool's rows where chunks c0 .. c0 + 31 start, and the 32 after them, one per lane
         auto rows_of = [&](int c) -> int {
           if (c >= last) return 0;
           const int e = c / per_page;
-          int page = __ldg(table + e);
-          if (page < 0 || page >= a.num_pages) {
-            set_device_error(a.err, MOE_DEV_BAD_INDEX);
-            page = 0;
-          }
+          const int page = max(kv::page_of(a, sg.b, e), 0);  // (a bad one is recorded, and not followed)
           return (page * a.heads + sg.h) * a.page_size + (c - e * per_page) * g.chunk;
         };
         int rows = rows_of(c0 + lane), rows2 = rows_of(c0 + 32 + lane);
@@ -839,7 +834,7 @@ cudaError_t launch(const kv::Args& a, const AttnArgs& g, const CUtensorMap& tk, 
   e = cudaLaunchKernelEx(&cfg, kv_attention_kernel<D, Q8>, a, g, tk, tv);
   note_launches(1);
   // items of up to WHOLE key tiles are never cut
-  if (e != cudaSuccess || static_cast<long long>(a.table_width) * a.page_size <= WHOLE * TILE) return e;
+  if (e != cudaSuccess || a.most <= WHOLE * TILE) return e;
   cfg.gridDim = dim3(ctas - 1, min(static_cast<long long>(a.T) * g.group, static_cast<long long>(MERGE_Y)));
   cfg.blockDim = dim3(32 * MERGE_WARPS);
   cfg.dynamicSmemBytes = 0;
@@ -853,13 +848,42 @@ cudaError_t launch(const kv::Args& a, const AttnArgs& g, const CUtensorMap& tk, 
 int num_sms();
 unsigned long long wait_limit_ns();
 
-size_t kv_attention_workspace_bytes(int d) {
-  const size_t slot = (d == 64 ? slot_floats<64>() : slot_floats<128>()) * sizeof(float);
-  return num_sms() * (sizeof(int4) + 2 * slot);
+cudaError_t launch_kv_expand(const kv::Args& a, uint16_t* k, uint16_t* v, int tile, int tiles, cudaStream_t s);
+
+// Bytes of keys (or values) when an e4m3 cache is to be expanded to bf16 before an attention, else 0.  The
+// attention of a pair of query tiles expands its keys and values on chip, every pair the same ones: from two
+// pairs per sequence on, on average, one pass over the cache before it costs less (six chunks of 440 to 1777
+// tokens over 1K to 10K: 457 us on chip).  What the sequences' tables have room for is reserved, up to 8 GiB.
+size_t kv_expanded_bytes(const kv::Args& a, bool q8, int q_heads) {
+  if (!q8 || a.B > 65535 || static_cast<long long>(a.T) * (q_heads / a.heads) < 4ll * TILE * a.B) return 0;
+  const long long rows = static_cast<long long>(a.B) * ((a.most + TILE - 1) / TILE) * TILE * a.heads;
+  return rows < (1ll << 31) && rows * a.d <= (1ll << 31) ? rows * a.d * 2 : 0;
 }
 
-cudaError_t launch_kv_attention(const kv::Args& a, bool q8, const uint16_t* q, long long q_token, long long q_head,
+size_t kv_attention_workspace_bytes(const kv::Args& a, bool q8, int q_heads) {
+  const size_t slot = (a.d == 64 ? slot_floats<64>() : slot_floats<128>()) * sizeof(float);
+  return num_sms() * (sizeof(int4) + 2 * slot) + 2 * kv_expanded_bytes(a, q8, q_heads);
+}
+
+cudaError_t launch_kv_attention(const kv::Args& args, bool q8, const uint16_t* q, long long q_token, long long q_head,
                                 int q_heads, float scale, uint16_t* out, float* lse, void* ws, cudaStream_t s) {
+  kv::Args a = args;
+  const size_t wide = kv_expanded_bytes(a, q8, q_heads);
+  if (wide) {
+    // the expanded cache: pages of TILE tokens in order
+    uint16_t* k = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(ws) + kv_attention_workspace_bytes(a, false, q_heads));
+    uint16_t* v = k + wide / 2;
+    const int tiles = (a.most + TILE - 1) / TILE;
+    const cudaError_t e = launch_kv_expand(a, k, v, TILE, tiles, s);
+    if (e != cudaSuccess) return e;
+    a.k = k;
+    a.v = v;
+    a.page_size = TILE;
+    a.table_width = tiles;
+    a.num_pages = a.B * tiles;
+    a.in_order = true;
+    q8 = false;
+  }
   AttnArgs g;
   g.q = q;
   g.q_token = q_token;

@@ -61,6 +61,18 @@ __device__ __forceinline__ int find_place(const kv::Args& a, int t) {
   return page < 0 ? -1 : page * a.heads * a.page_size + p - e * a.page_size;
 }
 
+// Sixteen codes as bf16 values, 32 bytes.
+__device__ __forceinline__ void store_expanded(uint4* dst, uint4 x, float scale) {
+  uint32_t s1, s2;
+  kv::scale_pairs(scale, &s1, &s2);
+  const uint2 v0 = kv::expand4(x.x, s1), v1 = kv::expand4(x.y, s1);
+  const uint2 v2 = kv::expand4(x.z, s1), v3 = kv::expand4(x.w, s1);
+  dst[0] = make_uint4(kv::bf16x2_mul(v0.x, s2), kv::bf16x2_mul(v0.y, s2), kv::bf16x2_mul(v1.x, s2),
+                      kv::bf16x2_mul(v1.y, s2));
+  dst[1] = make_uint4(kv::bf16x2_mul(v2.x, s2), kv::bf16x2_mul(v2.y, s2), kv::bf16x2_mul(v3.x, s2),
+                      kv::bf16x2_mul(v3.y, s2));
+}
+
 constexpr int FLIGHT = 4;  // row loads of a lane in flight
 
 // Walks a warp's (token, group of RPW rows) pairs in order, FLIGHT at a time.
@@ -178,14 +190,56 @@ __global__ void __launch_bounds__(KV_THREADS) kv_read_kernel(const kv::Args a, u
         *dst = x[u];
         continue;
       }
-      uint32_t s1, s2;
-      kv::scale_pairs(scale[u], &s1, &s2);
-      const uint2 v0 = kv::expand4(x[u].x, s1), v1 = kv::expand4(x[u].y, s1);
-      const uint2 v2 = kv::expand4(x[u].z, s1), v3 = kv::expand4(x[u].w, s1);
-      dst[0] = make_uint4(kv::bf16x2_mul(v0.x, s2), kv::bf16x2_mul(v0.y, s2), kv::bf16x2_mul(v1.x, s2),
-                          kv::bf16x2_mul(v1.y, s2));
-      dst[1] = make_uint4(kv::bf16x2_mul(v2.x, s2), kv::bf16x2_mul(v2.y, s2), kv::bf16x2_mul(v3.x, s2),
-                          kv::bf16x2_mul(v3.y, s2));
+      store_expanded(dst, x[u], scale[u]);
+    }
+  }
+}
+
+// Expands what the sequences with new tokens have cached to bf16 pages of TILE tokens in order: block
+// (tile, b), a warp per 16 tokens.  For an attention of many query rows, each tile of which would expand
+// the same codes again.
+template <int D>
+__global__ void __launch_bounds__(KV_THREADS) kv_expand_kernel(const kv::Args a, uint16_t* __restrict__ k_out,
+                                                               uint16_t* __restrict__ v_out, int tile) {
+  constexpr int C = D / 16, RPW = 32 / C, TOKENS = 16;
+  const int b = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int c = lane % C, rows = 2 * a.heads, t0 = warp * TOKENS;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const kv::Seq q = kv::load_seq(a, b);
+  const int p0 = blockIdx.x * tile + t0;
+  if (q.n == 0 || p0 >= q.len) return;
+  int mine = -2;
+  if (lane < TOKENS && p0 + lane < q.len) {
+    const int p = p0 + lane, e = p / a.page_size, page = kv::page_of(a, b, e);
+    mine = page < 0 ? -1 : page * a.heads * a.page_size + p - e * a.page_size;
+  }
+  const size_t out0 = (static_cast<size_t>(b) * gridDim.x + blockIdx.x) * a.heads * tile + t0;
+  Step s = {0, 0};
+  while (s.i < TOKENS) {
+    uint4 x[FLIGHT];
+    float scale[FLIGHT];
+    int token[FLIGHT], row[FLIGHT];
+#pragma unroll
+    for (int u = 0; u < FLIGHT; ++u) {
+      const int r = s.r0 + lane / C, place = __shfl_sync(0xffffffffu, mine, s.i & 31);
+      const bool is_v = r >= a.heads;
+      token[u] = s.i < TOKENS && r < rows && place != -2 ? s.i : -1;
+      row[u] = r;
+      x[u] = make_uint4(0, 0, 0, 0);
+      scale[u] = 1.f;
+      if (token[u] >= 0 && place >= 0) {
+        const size_t at = static_cast<size_t>(place) + (is_v ? r - a.heads : r) * a.page_size;
+        x[u] = __ldg(reinterpret_cast<const uint4*>(is_v ? a.v : a.k) + at * C + c);
+        scale[u] = __ldg((is_v ? a.v_scale : a.k_scale) + at);
+      }
+      s.next(rows, RPW);
+    }
+#pragma unroll
+    for (int u = 0; u < FLIGHT; ++u) {
+      if (token[u] < 0) continue;
+      const bool is_v = row[u] >= a.heads;
+      const size_t at = out0 + static_cast<size_t>(is_v ? row[u] - a.heads : row[u]) * tile + token[u];
+      store_expanded(reinterpret_cast<uint4*>(is_v ? v_out : k_out) + at * (D / 8) + 2 * c, x[u], scale[u]);
     }
   }
 }
@@ -198,13 +252,12 @@ int tokens_per_warp(int T) {
   return n;
 }
 
-// A grid of one warp per `tokens` tokens, started while the kernel before it in the stream ends (the
-// kernels wait for its results themselves).
+// A grid that is started while the kernel before it in the stream ends (the kernels wait for its results
+// themselves).
 template <typename... P, typename... Q>
-cudaError_t launch_warps(void (*kernel)(P...), int T, int tokens, cudaStream_t s, Q... args) {
-  const int warps = ceil_div(T, tokens);
+cudaError_t launch_early(void (*kernel)(P...), dim3 grid, cudaStream_t s, Q... args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ceil_div(warps, KV_THREADS / 32));
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(KV_THREADS);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -217,26 +270,38 @@ cudaError_t launch_warps(void (*kernel)(P...), int T, int tokens, cudaStream_t s
   return e;
 }
 
+// One warp per `tokens` tokens.
+dim3 warps_for(int T, int tokens) { return dim3(ceil_div(ceil_div(T, tokens), KV_THREADS / 32)); }
+
 }  // namespace
 
 cudaError_t launch_kv_append(const kv::Args& a, bool q8, const uint16_t* k, long long k_token, long long k_head,
                              const uint16_t* v, long long v_token, long long v_head, cudaStream_t s) {
   const NewRows in = {k, v, k_token, k_head, v_token, v_head};
   const int n = tokens_per_warp(a.T);
+  const dim3 grid = warps_for(a.T, n);
   if (a.d == 64)
-    return q8 ? launch_warps(kv_append_kernel<64, true>, a.T, n, s, a, in, n)
-              : launch_warps(kv_append_kernel<64, false>, a.T, n, s, a, in, n);
-  return q8 ? launch_warps(kv_append_kernel<128, true>, a.T, n, s, a, in, n)
-            : launch_warps(kv_append_kernel<128, false>, a.T, n, s, a, in, n);
+    return q8 ? launch_early(kv_append_kernel<64, true>, grid, s, a, in, n)
+              : launch_early(kv_append_kernel<64, false>, grid, s, a, in, n);
+  return q8 ? launch_early(kv_append_kernel<128, true>, grid, s, a, in, n)
+            : launch_early(kv_append_kernel<128, false>, grid, s, a, in, n);
 }
 
 cudaError_t launch_kv_read(const kv::Args& a, bool q8, uint16_t* k, uint16_t* v, cudaStream_t s) {
   const int n = tokens_per_warp(a.T);
+  const dim3 grid = warps_for(a.T, n);
   if (a.d == 64)
-    return q8 ? launch_warps(kv_read_kernel<64, true>, a.T, n, s, a, k, v, n)
-              : launch_warps(kv_read_kernel<64, false>, a.T, n, s, a, k, v, n);
-  return q8 ? launch_warps(kv_read_kernel<128, true>, a.T, n, s, a, k, v, n)
-            : launch_warps(kv_read_kernel<128, false>, a.T, n, s, a, k, v, n);
+    return q8 ? launch_early(kv_read_kernel<64, true>, grid, s, a, k, v, n)
+              : launch_early(kv_read_kernel<64, false>, grid, s, a, k, v, n);
+  return q8 ? launch_early(kv_read_kernel<128, true>, grid, s, a, k, v, n)
+            : launch_early(kv_read_kernel<128, false>, grid, s, a, k, v, n);
+}
+
+// Pages of `tile` = 128 tokens, `tiles` per sequence.
+cudaError_t launch_kv_expand(const kv::Args& a, uint16_t* k, uint16_t* v, int tile, int tiles, cudaStream_t s) {
+  const dim3 grid(tiles, a.B);
+  return a.d == 64 ? launch_early(kv_expand_kernel<64>, grid, s, a, k, v, tile)
+                   : launch_early(kv_expand_kernel<128>, grid, s, a, k, v, tile);
 }
 
 }  // namespace moe

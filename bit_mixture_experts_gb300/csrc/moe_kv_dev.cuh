@@ -18,6 +18,8 @@ struct Args {
   int* err;
   int num_pages, page_size, heads, d;
   int B, table_width, T;
+  int most;       // tokens of a sequence that its table has pages for
+  bool in_order;  // no table: sequence b's pages are b * table_width and on
 };
 
 // One sequence: its first row in the dense tensors, its new tokens, its tokens in all.
@@ -28,12 +30,11 @@ struct Seq {
 __device__ __forceinline__ Seq load_seq(const Args& a, int b) {
   Seq s;
   int lo = __ldg(a.cu_q + b), hi = __ldg(a.cu_q + b + 1), len = __ldg(a.kv_len + b);
-  const int most = a.table_width * a.page_size;
-  if (lo < 0 || hi < lo || hi > a.T || len < 0 || len > most) {
+  if (lo < 0 || hi < lo || hi > a.T || len < 0 || len > a.most) {
     set_device_error(a.err, MOE_DEV_BAD_INDEX);
     lo = min(max(lo, 0), a.T);
     hi = min(max(hi, lo), a.T);
-    len = min(max(len, 0), most);
+    len = min(max(len, 0), a.most);
   }
   s.row0 = lo;
   s.n = hi - lo;
@@ -55,15 +56,18 @@ __device__ __forceinline__ int find_seq(const Args& a, int t) {
   return b >= 0 && t < __ldg(a.cu_q + b + 1) ? b : -1;
 }
 
-// Page of position p of sequence b, or -1 (recorded) where the table holds none.
-__device__ __forceinline__ int find_page(const Args& a, int b, int p) {
-  const int page = __ldg(a.page_table + static_cast<size_t>(b) * a.table_width + p / a.page_size);
+// Page e of sequence b, or -1 (recorded) where the table holds none.
+__device__ __forceinline__ int page_of(const Args& a, int b, int e) {
+  if (a.in_order) return b * a.table_width + e;
+  const int page = __ldg(a.page_table + static_cast<size_t>(b) * a.table_width + e);
   if (page < 0 || page >= a.num_pages) {
     set_device_error(a.err, MOE_DEV_BAD_INDEX);
     return -1;
   }
   return page;
 }
+
+__device__ __forceinline__ int find_page(const Args& a, int b, int p) { return page_of(a, b, p / a.page_size); }
 
 // Two e4m3 bytes (low 16 bits of x, the first in the low byte) -> floats, exact.
 __device__ __forceinline__ float2 e4m3x2_to_float2(uint32_t x) {

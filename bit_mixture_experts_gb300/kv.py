@@ -29,6 +29,7 @@ class KVBatch:
         if cu_q.shape[0] != B + 1 or kv_len.shape[0] != B:
             raise ValueError(f"{B} sequences in page_table need cu_q of {B + 1} and kv_len of {B} elements")
         self.T = int(T)
+        self.workspace = {}  # bytes of scratch that an attention needs, by cache and query heads
         self.tensors = (page_table, cu_q, kv_len)
         self.struct = _lib.KVBatch(page_table.data_ptr(), cu_q.data_ptr(), kv_len.data_ptr(), B, width, self.T)
 
@@ -106,14 +107,20 @@ class PagedKVCache:
         with torch.cuda.stream(stream):
             return torch.empty(shape, dtype=dtype, device=self.device)
 
-    def _workspace(self, stream):
+    def _workspace(self, batch, q_heads, stream):
         """(pointer, bytes) of the attention's scratch for calls on `stream`: one per stream, so that calls on
-        two streams share none.  Allocated at the first call there: make that one before a graph capture."""
+        two streams share none, grown to the largest call's need.  A first call of its size allocates: make it
+        before a graph capture."""
+        need = batch.workspace.get((self, q_heads))
+        if need is None:
+            need = max(_lib.moe_kv_attention_workspace_size(self.struct, batch.struct, q_heads), 16)
+            batch.workspace[(self, q_heads)] = need
         key = _lib._stream(stream)
-        if key not in self._workspaces:
-            t = self._empty((max(_lib.moe_kv_attention_workspace_size(self.d), 16),), torch.uint8, stream)
-            self._workspaces[key] = (t, (t.data_ptr(), t.nbytes))
-        return self._workspaces[key][1]
+        have = self._workspaces.get(key)
+        if have is None or have[1][1] < need:
+            t = self._empty((need,), torch.uint8, stream)
+            have = self._workspaces[key] = (t, (t.data_ptr(), t.nbytes))
+        return have[1]
 
     def append(self, k, v, batch, stream=None):
         """Write the new tokens' keys and values (bf16 [T, heads, d], strided views welcome) into the cache."""
@@ -140,7 +147,7 @@ class PagedKVCache:
         q_heads is a multiple of the cache's heads; scale defaults to 1/sqrt(d).  Returns bf16
         [T, q_heads, d], with ``return_lse`` also the scores' natural log-sum-exp, float32 [T, q_heads]
         (-inf for a token that sees no key; its output is 0).  `workspace` (uint8, at least
-        ``moe_kv_attention_workspace_size(d)``) replaces the cache's own scratch of the stream."""
+        ``moe_kv_attention_workspace_size``) replaces the cache's own scratch of the stream."""
         self._rows(q, "q", batch)
         if out is None:
             out = (torch.empty_like(q, memory_format=torch.contiguous_format) if stream is None
@@ -151,5 +158,5 @@ class PagedKVCache:
                 raise ValueError("out must be contiguous")
         lse = self._empty(q.shape[:2], torch.float32, stream) if return_lse else None
         _lib.moe_kv_attention(q, self.d ** -0.5 if scale is None else scale, self.struct, batch.struct, out, lse,
-                              self._workspace(stream) if workspace is None else workspace, stream)
+                              self._workspace(batch, q.shape[1], stream) if workspace is None else workspace, stream)
         return (out, lse) if return_lse else out

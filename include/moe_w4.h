@@ -527,10 +527,13 @@ int moe_kv_read(uint16_t* k, uint16_t* v, const moe_kv_cache_t* cache, const moe
  * token's own, and rows of its pages past kv_len, do not enter its result
  * whatever they hold.  Scores, sums and the output are accumulated in FP32.
  * scale is finite and > 0.
- * workspace: moe_kv_attention_workspace_size(d) bytes of scratch that no other
- * call uses at the same time; its contents need no preparation.
+ * workspace: moe_kv_attention_workspace_size() bytes of scratch that no other
+ * call uses at the same time; its contents need no preparation.  It grows with
+ * B * table_width where an e4m3 cache is first expanded to bf16 (many query
+ * rows per sequence; at most 8 GiB), and is otherwise fixed (some 40 MB).
+ * One to three launches.
  */
-size_t moe_kv_attention_workspace_size(int d);
+size_t moe_kv_attention_workspace_size(const moe_kv_cache_t* cache, const moe_kv_batch_t* batch, int q_heads);
 int moe_kv_attention(const uint16_t* q, int64_t q_token_stride, int64_t q_head_stride, int q_heads, float scale,
                      const moe_kv_cache_t* cache, const moe_kv_batch_t* batch, uint16_t* out, float* lse,
                      void* workspace, size_t workspace_bytes, moe_stream_t stream);
