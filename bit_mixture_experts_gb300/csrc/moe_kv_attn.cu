@@ -73,13 +73,13 @@ __global__ void __launch_bounds__(Layout<D, Q8>::THREADS, 1)
   kv::Share share;
   kv::Start from;
   if (a.B > 32 || warp == 0)
-    from = kv::locate<L::THREADS>(a, 2 * g.tpt, static_cast<int>(gridDim.x), cta,
+    from = kv::locate<L::THREADS>(a, g.tokens, static_cast<int>(gridDim.x), g.merge, cta,
                                   reinterpret_cast<long long*>(smem + L::KV_OFF), share);
   Seg sg;
-  kv::Walk walk(a, 2 * g.tpt, 0, 0, 0, 0, false);
+  kv::Walk walk(a, g.tokens, 0, 0, 0, 0, false);
   if (warp == 0) {  // works the segments out; the first while the CTA starts up
     if (cta < share.ctas)
-      walk = kv::Walk(a, 2 * g.tpt, share.lo(cta), share.lo(cta + 1), from.b, from.b_lo, share.whole);
+      walk = kv::Walk(a, g.tokens, share.lo(cta), share.lo(cta + 1), from.b, from.b_lo, share.whole);
     if (!walk.next(sg)) sg.ntok = 0;  // the end
   }
   ptx::fence_proxy_async_smem();  // the scratch is overwritten by copies
@@ -833,8 +833,8 @@ cudaError_t launch(const kv::Args& a, const AttnArgs& g, const CUtensorMap& tk, 
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, kv_attention_kernel<D, Q8>, a, g, tk, tv);
   note_launches(1);
-  // items of up to WHOLE key tiles are never cut
-  if (e != cudaSuccess || a.most <= WHOLE * TILE) return e;
+  // items of up to that many key tiles are never cut
+  if (e != cudaSuccess || a.most <= g.merge * TILE) return e;
   cfg.gridDim = dim3(ctas - 1, min(static_cast<long long>(a.T) * g.group, static_cast<long long>(MERGE_Y)));
   cfg.blockDim = dim3(32 * MERGE_WARPS);
   cfg.dynamicSmemBytes = 0;
@@ -897,6 +897,13 @@ cudaError_t launch_kv_attention(const kv::Args& args, bool q8, const uint16_t* q
   g.q_heads = q_heads;
   g.group = q_heads / a.heads;
   g.tpt = TILE / g.group;
+  // pairs of tiles; but with so few of them that half of the SMs would have none, single tiles (a 512-token
+  // prompt 20.5 -> 18.0 us, over 8000 cached tokens 64 -> 57 us; a 2048-token one 50 us as pairs, 58 single)
+  const long long pairs = (a.T + 2ll * g.tpt - 1) / (2 * g.tpt) * a.heads;
+  g.tokens = pairs <= num_sms() / 2 ? g.tpt : 2 * g.tpt;
+  // cutting costs a tile's rows written, read and joined: 10 where 16 is taken, 2048 tokens 49.8 -> 43.3 us,
+  // four chunks of 300 over 3000 39.7 -> 36.4; the few rows of decoding cost little (1 to 6 measure alike)
+  g.merge = static_cast<long long>(a.T) * g.group <= static_cast<long long>(THIN_ROWS) * a.B ? 3 : 16;
   g.chunk = a.page_size & -a.page_size;  // the largest power of two that divides the page
   if (g.chunk > TILE) g.chunk = TILE;
   const unsigned long long ns = wait_limit_ns();

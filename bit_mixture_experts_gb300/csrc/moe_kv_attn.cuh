@@ -16,7 +16,10 @@ struct AttnArgs {
   int4* joins;  // workspace: per CTA, the item that its last part begins (parts, first row, tokens, KV head)
   float* part;  // and two slots for parts of items
   float scale_log2;
-  int q_heads, group, tpt, chunk;  // chunk: rows of one copy, divides page_size and TILE
+  int q_heads, group, tpt;  // tpt: tokens per query tile
+  int tokens;               // per item: of a pair of tiles, or of one
+  int merge;                // what cutting items costs, in key tiles
+  int chunk;                // rows of one copy, divides page_size and TILE
   unsigned long long wait_cycles;
   bool poll;  // the limit is too short for waits inside an instruction
 };

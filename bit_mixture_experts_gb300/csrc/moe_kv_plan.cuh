@@ -140,22 +140,20 @@ struct Walk {
   }
 };
 
-// Items of up to WHOLE units are not cut (merging their parts costs more than they do), nor items that are
-// small beside a share.
-constexpr int WHOLE = 5;
-
 // How a call's line of units is dealt out: as evenly as can be.
 struct Share {
   long long total, each;
   int ctas, more;  // CTAs with work; how many of them take one unit more than `each`
   bool whole;
 
-  __device__ __forceinline__ void set(long long units, int longest, int grid) {
+  // `merge`: what writing and merging parts costs, in key tiles.  Cut, the call takes about an even share
+  // and that; whole, the longest item where every item has a CTA, and up to that more than a share else.
+  __device__ __forceinline__ void set(long long units, int longest, int items, int grid, int merge) {
     total = units;
     ctas = static_cast<int>(min(static_cast<long long>(grid), units));
     each = ctas ? divide(units, ctas) : 0;
     more = static_cast<int>(units - each * ctas);
-    whole = longest <= WHOLE + each / 16;
+    whole = longest <= merge + (items <= grid ? each : each / 16);
   }
   __device__ __forceinline__ long long lo(int c) const { return each * c + min(c, more); }
   // The CTA whose share holds unit u.
@@ -172,22 +170,26 @@ struct Start {
 };
 
 // Sets `share` and finds the sequence that holds unit share.lo(cut), if there is such a share.  All
-// threads of the block, or up to 32 sequences any whole warps of it; `scratch`: 50 long longs of shared memory, free again on return.  Up to 32
-// sequences every warp works it out for itself, a sequence per lane; more are dealt to the block's threads.
+// threads of the block, or up to 32 sequences any whole warps of it; `scratch`: 66 long longs of shared
+// memory, free again on return.  Up to 32 sequences every warp works it out for itself, a sequence per lane;
+// more are dealt to the block's threads.
 template <int NT>
-__device__ __forceinline__ Start locate(const Args& a, int tp, int grid, int cut, long long* scratch, Share& share) {
+__device__ __forceinline__ Start locate(const Args& a, int tp, int grid, int merge, int cut, long long* scratch,
+                                        Share& share) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const bool small = a.B <= 32;
   const int per = small ? 1 : ceil_div(a.B, NT);
   const int b0 = min((small ? lane : tid) * per, a.B), b1 = min(b0 + per, a.B);
   long long mine = 0;
-  int longest = 0;
+  int longest = 0, items = 0;
   for (int b = b0; b < b1; ++b) {
     const Pairs p(load_seq(a, b), tp);
     mine += p.units() * a.heads;
     if (p.M > 0) longest = max(longest, p.tiles(p.M - 1));
+    items += p.M * a.heads;
   }
   longest = __reduce_max_sync(0xffffffffu, longest);
+  items = __reduce_add_sync(0xffffffffu, items);
   long long incl = mine;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
@@ -196,7 +198,7 @@ __device__ __forceinline__ Start locate(const Args& a, int tp, int grid, int cut
   }
   Start found = {0, 0};
   if (small) {
-    share.set(__shfl_sync(0xffffffffu, incl, 31), longest, grid);
+    share.set(__shfl_sync(0xffffffffu, incl, 31), longest, items, grid, merge);
     const long long want = share.lo(cut);
     const uint32_t past = __ballot_sync(0xffffffffu, incl > want);  // sequences that end after it
     if (cut < share.ctas) {
@@ -205,24 +207,27 @@ __device__ __forceinline__ Start locate(const Args& a, int tp, int grid, int cut
     }
     return found;
   }
-  int* longests = reinterpret_cast<int*>(scratch + 32);
+  int* more = reinterpret_cast<int*>(scratch + 32);
   if (lane == 31) {
     scratch[warp] = incl;
-    longests[warp] = longest;
+    more[warp] = longest;
+    more[32 + warp] = items;
   }
   __syncthreads();
   long long off = 0, total = 0;
+  items = 0;
 #pragma unroll
   for (int w = 0; w < NT / 32; ++w) {
     const long long x = scratch[w];
     if (w < warp) off += x;
     total += x;
-    longest = max(longest, longests[w]);
+    longest = max(longest, more[w]);
+    items += more[32 + w];
   }
-  share.set(total, longest, grid);
+  share.set(total, longest, items, grid, merge);
   const long long want = share.lo(cut);
   long long lo = off + incl - mine;
-  Start* shared = reinterpret_cast<Start*>(scratch + 48);
+  Start* shared = reinterpret_cast<Start*>(scratch + 64);
   if (cut < share.ctas && want >= lo && want < lo + mine) {
     int b = b0;
     for (;; ++b) {
