@@ -209,10 +209,14 @@ __device__ __forceinline__ bool thin_segment(const Args& a, const AttnArgs& g, c
       l1 += e2 + e3;
       if (Q8) {
         const float2 sc = lds_float2(sbase + L::SCALE_OFF + (vs * TILE + first_key + 8 * n + 2 * q) * 4);
-        e0 = e0 == 0.f ? 0.f : e0 * sc.x;  // a hidden key's scale may be anything
-        e1 = e1 == 0.f ? 0.f : e1 * sc.y;
-        e2 = e2 == 0.f ? 0.f : e2 * sc.x;
-        e3 = e3 == 0.f ? 0.f : e3 * sc.y;
+        e0 *= sc.x, e1 *= sc.y, e2 *= sc.x, e3 *= sc.y;
+        if (fix) {  // a hidden key's scale may be anything
+          const int pos = k0 + first_key + 8 * n + 2 * q;
+          if (pos >= see0) e0 = 0.f;
+          if (pos + 1 >= see0) e1 = 0.f;
+          if (pos >= see1) e2 = 0.f;
+          if (pos + 1 >= see1) e3 = 0.f;
+        }
       }
       p[n][0] = pack_bf16x2(e0, e1);
       p[n][1] = pack_bf16x2(e2, e3);
