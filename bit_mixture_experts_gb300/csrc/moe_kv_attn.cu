@@ -334,9 +334,10 @@ __global__ void __launch_bounds__(Layout<D, Q8>::THREADS, 1)
       ptx::mma_commit_elect(bar(L::DRAIN));
       tc_dev::wait_drain(bar(L::DRAIN), 0, 0);
     } else {
-      // ---------------------------------------------- query tile t of every item
+      // ---------------------------------------------- queries: tile t of a pair, or half of a lone tile's rows
       const int t = warp - 2;
-      constexpr int C = D / 8;
+      constexpr int C = D / 8, R = 32 / C;  // a row's pieces of 8 values, a lane each; rows at a time
+      const long long by_token = g.q_token - g.group * g.q_head;
       uint32_t ph = 1, phb = 1;  // of QEMPTY: the first use waits for nothing
       while (next(sg)) {
         const bool pair = sg.ntok > g.tpt;
@@ -348,30 +349,30 @@ __global__ void __launch_bounds__(Layout<D, Q8>::THREADS, 1)
             if (!wait(L::QEMPTY + 1, phb)) break;
             phb ^= 1;
           }
-          if (lane == 0) ptx::mbar_arrive(bar(L::QFULL));
-          if (!pair) continue;
+          if (pair && lane == 0) ptx::mbar_arrive(bar(L::QFULL));
         }
-        // a lane's column of 8 values, 32 / C rows at a time, in the order token, head
-        const int tok0 = t * g.tpt, rows = min(g.tpt, sg.ntok - tok0) * g.group;
-        const long long by_token = g.q_token - g.group * g.q_head;
-        int hd = lane / C;
-        const uint16_t* src = g.q + static_cast<long long>(sg.row0 + sg.i0 + tok0) * g.q_token +
+        const int tile = pair ? t : 0, tok0 = tile * g.tpt, rows = min(g.tpt, sg.ntok - tok0) * g.group;
+        // rows in the order token, head: from r every `step` rows, that is `dt` tokens and `dh` heads on
+        const int step = pair ? R : 2 * R, dt = step / g.group, dh = step - dt * g.group;
+        int r = (pair ? 0 : t * R) + lane / C;
+        const int tok = r / g.group;
+        int hd = r - tok * g.group;
+        const uint16_t* src = g.q + (sg.row0 + sg.i0 + tok0 + tok) * g.q_token +
                               (static_cast<long long>(sg.h) * g.group + hd) * g.q_head + lane % C * 8;
-        const uint32_t col = sbase + L::Q_OFF + t * TB + (lane % C >> 3) * PANEL;
-#pragma unroll 4
-        for (int r = lane / C; r < rows; r += 32 / C) {
-          while (hd >= g.group) {
-            hd -= g.group;
-            src += by_token;
-          }
+        const long long jump = dt * g.q_token + dh * g.q_head;
+        const uint32_t col = sbase + L::Q_OFF + tile * TB + (lane % C >> 3) * PANEL;
+#pragma unroll 8
+        for (; r < rows; r += step) {
           ptx::cp_async_16(col + r * 128 + (((lane & 7) ^ (r & 7)) << 4), src);
-          hd += 32 / C;
-          src += 32 / C * g.q_head;
+          hd += dh;
+          const bool over = hd >= g.group;
+          hd -= over ? g.group : 0;
+          src += jump + (over ? by_token : 0);
         }
         ptx::cp_async_wait_all();
         ptx::fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(bar(L::QFULL + t));
+        if (lane == 0) ptx::mbar_arrive(bar(L::QFULL + tile));
       }
     }
   } else if (warp < 12) {
@@ -457,7 +458,7 @@ __global__ void __launch_bounds__(Layout<D, Q8>::THREADS, 1)
             if (nonfinite || p >= sg.len) {
 #pragma unroll
               for (int c = 0; c < NH * 8; ++c)
-                sts128(row + (c >> 3) * PANEL + (c << 4 & 127), make_uint4(0, 0, 0, 0));
+                sts128(row + (c >> 3) * PANEL + (((c & 7) ^ (r & 7)) << 4), make_uint4(0, 0, 0, 0));
             }
             const uint32_t mask = __ballot_sync(0xffffffffu, nonfinite);
             if (lane == 0) s_bad[(un & 1) * 4 + w] = mask;
