@@ -400,7 +400,8 @@ __global__ void __launch_bounds__(Layout<D, Q8>::THREADS, 1)
           lent = false;
         }
         const ThinCtx ctx = {sbase, smem, s_abort, warp - 4, lane};
-        ok = thin_segment<D, Q8>(a, g, sg, ctx, cta, Q8 ? all - n : all, team_ph);
+        ok = sg.ntok * g.group <= 8 ? thin_segment<D, Q8, true>(a, g, sg, ctx, cta, Q8 ? all - n : all, team_ph)
+                                    : thin_segment<D, Q8, false>(a, g, sg, ctx, cta, Q8 ? all - n : all, team_ph);
         all += run;
         continue;
       }

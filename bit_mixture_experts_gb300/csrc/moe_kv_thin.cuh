@@ -42,6 +42,19 @@ __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t a, uint32_t (&v)[4]) 
                : "memory");
 }
 
+// The transpose of an 8 x 8 matrix of 16-bit values, a row's pair per lane.
+__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t a) {
+  uint32_t d;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+
+__device__ __forceinline__ float lds_float(uint32_t a) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+  return v;
+}
+
 __device__ __forceinline__ uint2 lds64(uint32_t a) {
   uint2 v;
   asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
@@ -73,11 +86,12 @@ struct ThinCtx {
 
 // One segment by the team's eight warps, whose query rows have landed.  units: ring units before it;
 // team_ph: phases of the TEAM barrier so far.  False when a wait gave up.
-template <int D, bool Q8>
+template <int D, bool Q8, bool NARROW>
 __device__ __forceinline__ bool thin_segment(const Args& a, const AttnArgs& g, const Seg& sg, const ThinCtx& x, int cta,
                                              int units, uint32_t& team_ph) {
   using L = Layout<D, Q8>;
   constexpr int STEPS = D / 16, DQ = D / 4, QC = DQ / 8, NT = D / 8;
+  constexpr int NO = NARROW ? D / 16 : NT, NF = NARROW ? 2 : 4;  // fragments of the output, of 32 keys
   const int lane = x.lane, gr = lane >> 2, q = lane & 3;
   const uint32_t sbase = x.sbase;
   auto bar = [sbase](int i) -> uint32_t { return sbase + L::BAR_OFF + 8u * static_cast<uint32_t>(i); };
@@ -96,7 +110,7 @@ __device__ __forceinline__ bool thin_segment(const Args& a, const AttnArgs& g, c
   const int groups = rows <= 16 ? 1 : 2;
   const int mg = groups == 1 ? 0 : x.warp >> 2, first_tile = groups == 1 ? x.warp >> 2 : 0, step = 3 - groups;
   const int first_key = (x.warp & 3) * 32;
-  const int r0 = mg * 16 + gr, r1 = r0 + 8;
+  const int r0 = NARROW ? 2 * q : mg * 16 + gr, r1 = NARROW ? r0 + 1 : r0 + 8;
   const bool ok0 = r0 < rows, ok1 = r1 < rows;
   const int vis0 = sg.base + 1;  // keys that all rows see; row r sees those before vis0 + its token
   const int see0 = ok0 ? vis0 + r0 / g.group : 0, see1 = ok1 ? vis0 + r1 / g.group : 0;
@@ -109,20 +123,25 @@ __device__ __forceinline__ bool thin_segment(const Args& a, const AttnArgs& g, c
   };
 
   // Q's fragments
-  uint32_t qa[STEPS][4];
+  uint32_t qa[STEPS][NARROW ? 2 : 4];
 #pragma unroll
   for (int c = 0; c < QC; ++c) {
     const int d = DQ * q + 8 * c;
     const uint32_t at = sbase + L::Q_OFF + (d >> 6) * L::PANEL, ch = (d & 63) >> 3;
+    const int ra = NARROW ? gr : r0;
     uint4 v0 = make_uint4(0, 0, 0, 0), v1 = v0;
-    if (ok0) v0 = lds128(at + r0 * 128 + ((ch ^ (r0 & 7)) << 4));
-    if (ok1) v1 = lds128(at + r1 * 128 + ((ch ^ (r1 & 7)) << 4));
-    qa[2 * c][0] = v0.x, qa[2 * c][2] = v0.y, qa[2 * c + 1][0] = v0.z, qa[2 * c + 1][2] = v0.w;
-    qa[2 * c][1] = v1.x, qa[2 * c][3] = v1.y, qa[2 * c + 1][1] = v1.z, qa[2 * c + 1][3] = v1.w;
+    if (ra < rows) v0 = lds128(at + ra * 128 + ((ch ^ (ra & 7)) << 4));
+    if constexpr (NARROW) {
+      qa[2 * c][0] = v0.x, qa[2 * c][1] = v0.y, qa[2 * c + 1][0] = v0.z, qa[2 * c + 1][1] = v0.w;
+    } else {
+      if (ok1) v1 = lds128(at + r1 * 128 + ((ch ^ (r1 & 7)) << 4));
+      qa[2 * c][0] = v0.x, qa[2 * c][2] = v0.y, qa[2 * c + 1][0] = v0.z, qa[2 * c + 1][2] = v0.w;
+      qa[2 * c][1] = v1.x, qa[2 * c][3] = v1.y, qa[2 * c + 1][1] = v1.z, qa[2 * c + 1][3] = v1.w;
+    }
   }
-  float o[NT][4];
+  float o[NO][4];
 #pragma unroll
-  for (int j = 0; j < NT; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
+  for (int j = 0; j < NO; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
   float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
   bool bad0 = false, bad1 = false;
 
@@ -132,54 +151,105 @@ __device__ __forceinline__ bool thin_segment(const Args& a, const AttnArgs& g, c
     const uint32_t kbase = sbase + L::H_OFF + ks * L::LAND, vbase = sbase + L::H_OFF + vs * L::LAND;
     const bool fix = k0 + TILE > min(vis0, sg.len);
     if (!landed(ki)) return false;
-    // ---- scores of 32 keys: four fragments of 8
-    float s[4][4];
+    // ---- scores of 32 keys
+    float s[NF][4];
+    if constexpr (NARROW) {  // keys gr and gr + 8 of each 16, rows r0 and r1
 #pragma unroll
-    for (int n = 0; n < 4; ++n) {
-      s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
-      const int kr = first_key + 8 * n + gr;
-      if (!Q8) {
+      for (int n = 0; n < 2; ++n) {
+        s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+        const int kr = first_key + 16 * n + gr;
+        if (!Q8) {
 #pragma unroll
-        for (int c = 0; c < QC; ++c) {
-          const int d = DQ * q + 8 * c;
-          const uint4 v = lds128(kbase + (d >> 6) * L::PANEL + kr * 128 + ((((d & 63) >> 3) ^ (kr & 7)) << 4));
-          mma16816(s[n], qa[2 * c][0], qa[2 * c][1], qa[2 * c][2], qa[2 * c][3], v.x, v.y);
-          mma16816(s[n], qa[2 * c + 1][0], qa[2 * c + 1][1], qa[2 * c + 1][2], qa[2 * c + 1][3], v.z, v.w);
-        }
-      } else {
-#pragma unroll
-        for (int c = 0; c < D / 64; ++c) {
-          const uint32_t at = D == 128 ? kr * 128 + (((2 * q + c) ^ (kr & 7)) << 4)
-                                       : kr * 64 + ((q ^ ((kr >> 1) & 3)) << 4);
-          const uint4 v = lds128(kbase + at);
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint2 b = expand4(w[e], 0x7b807b80u);
-            const int st = 4 * c + e;
-            mma16816(s[n], qa[st][0], qa[st][1], qa[st][2], qa[st][3], b.x, b.y);
+          for (int c = 0; c < QC; ++c) {
+            const int d = DQ * q + 8 * c;
+            const uint32_t at = kbase + (d >> 6) * L::PANEL + kr * 128 + ((((d & 63) >> 3) ^ gr) << 4);
+            const uint4 v = lds128(at), u = lds128(at + 8 * 128);
+            mma16816(s[n], v.x, u.x, v.y, u.y, qa[2 * c][0], qa[2 * c][1]);
+            mma16816(s[n], v.z, u.z, v.w, u.w, qa[2 * c + 1][0], qa[2 * c + 1][1]);
           }
+        } else {
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c) {
+            const uint32_t at = kbase + (D == 128 ? kr * 128 + (((2 * q + c) ^ gr) << 4)
+                                                  : kr * 64 + ((q ^ ((kr >> 1) & 3)) << 4));
+            const uint4 v = lds128(at), u = lds128(at + 8 * D);
+            const uint32_t vw[4] = {v.x, v.y, v.z, v.w}, uw[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const uint2 a = expand4(vw[e], 0x7b807b80u), b = expand4(uw[e], 0x7b807b80u);
+              mma16816(s[n], a.x, b.x, a.y, b.y, qa[4 * c + e][0], qa[4 * c + e][1]);
+            }
+          }
+          const uint32_t at = sbase + L::SCALE_OFF + (ks * TILE + kr) * 4;
+          const float sa = lds_float(at), sb = lds_float(at + 32);
+          s[n][0] *= sa, s[n][1] *= sa, s[n][2] *= sb, s[n][3] *= sb;
         }
-        const float2 sc = lds_float2(sbase + L::SCALE_OFF + (ks * TILE + first_key + 8 * n + 2 * q) * 4);
-        s[n][0] *= sc.x, s[n][1] *= sc.y, s[n][2] *= sc.x, s[n][3] *= sc.y;
+      }
+    } else {  // keys 2q and 2q + 1 of each 8
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+        const int kr = first_key + 8 * n + gr;
+        if (!Q8) {
+#pragma unroll
+          for (int c = 0; c < QC; ++c) {
+            const int d = DQ * q + 8 * c;
+            const uint4 v = lds128(kbase + (d >> 6) * L::PANEL + kr * 128 + ((((d & 63) >> 3) ^ (kr & 7)) << 4));
+            mma16816(s[n], qa[2 * c][0], qa[2 * c][1], qa[2 * c][2], qa[2 * c][3], v.x, v.y);
+            mma16816(s[n], qa[2 * c + 1][0], qa[2 * c + 1][1], qa[2 * c + 1][2], qa[2 * c + 1][3], v.z, v.w);
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c) {
+            const uint32_t at = D == 128 ? kr * 128 + (((2 * q + c) ^ (kr & 7)) << 4)
+                                         : kr * 64 + ((q ^ ((kr >> 1) & 3)) << 4);
+            const uint4 v = lds128(kbase + at);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const uint2 b = expand4(w[e], 0x7b807b80u);
+              const int st = 4 * c + e;
+              mma16816(s[n], qa[st][0], qa[st][1], qa[st][2], qa[st][3], b.x, b.y);
+            }
+          }
+          const float2 sc = lds_float2(sbase + L::SCALE_OFF + (ks * TILE + first_key + 8 * n + 2 * q) * 4);
+          s[n][0] *= sc.x, s[n][1] *= sc.y, s[n][2] *= sc.x, s[n][3] *= sc.y;
+        }
       }
     }
     release(ks);
     // ---- weights
-    if (fix) {
+    float x0, x1;
+    if constexpr (NARROW) {
+      if (fix) {
 #pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        const int p = k0 + first_key + 8 * n + 2 * q;
-        if (p >= see0) s[n][0] = -INFINITY;
-        if (p + 1 >= see0) s[n][1] = -INFINITY;
-        if (p >= see1) s[n][2] = -INFINITY;
-        if (p + 1 >= see1) s[n][3] = -INFINITY;
+        for (int n = 0; n < 2; ++n) {
+          const int p = k0 + first_key + 16 * n + gr;
+          if (p >= see0) s[n][0] = -INFINITY;
+          if (p >= see1) s[n][1] = -INFINITY;
+          if (p + 8 >= see0) s[n][2] = -INFINITY;
+          if (p + 8 >= see1) s[n][3] = -INFINITY;
+        }
       }
-    }
-    float x0 = max3(max3(s[0][0], s[0][1], s[1][0]), max3(s[1][1], s[2][0], s[2][1]), fmaxf(s[3][0], s[3][1]));
-    float x1 = max3(max3(s[0][2], s[0][3], s[1][2]), max3(s[1][3], s[2][2], s[2][3]), fmaxf(s[3][2], s[3][3]));
+      x0 = max3(fmaxf(s[0][0], s[0][2]), s[1][0], s[1][2]);
+      x1 = max3(fmaxf(s[0][1], s[0][3]), s[1][1], s[1][3]);
+    } else {
+      if (fix) {
 #pragma unroll
-    for (int w = 1; w <= 2; w <<= 1) {
+        for (int n = 0; n < 4; ++n) {
+          const int p = k0 + first_key + 8 * n + 2 * q;
+          if (p >= see0) s[n][0] = -INFINITY;
+          if (p + 1 >= see0) s[n][1] = -INFINITY;
+          if (p >= see1) s[n][2] = -INFINITY;
+          if (p + 1 >= see1) s[n][3] = -INFINITY;
+        }
+      }
+      x0 = max3(max3(s[0][0], s[0][1], s[1][0]), max3(s[1][1], s[2][0], s[2][1]), fmaxf(s[3][0], s[3][1]));
+      x1 = max3(max3(s[0][2], s[0][3], s[1][2]), max3(s[1][3], s[2][2], s[2][3]), fmaxf(s[3][2], s[3][3]));
+    }
+    // a row's keys are spread over the lanes of a quad, or over the eight quads
+#pragma unroll
+    for (int w = NARROW ? 4 : 1; w <= (NARROW ? 16 : 2); w <<= 1) {
       x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, w));
       x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, w));
     }
@@ -192,7 +262,8 @@ __device__ __forceinline__ bool thin_segment(const Args& a, const AttnArgs& g, c
       const float f0 = x0 == m0 ? 1.f : ex2((m0 - x0) * g.scale_log2);
       const float f1 = x1 == m1 ? 1.f : ex2((m1 - x1) * g.scale_log2);
 #pragma unroll
-      for (int j = 0; j < NT; ++j) o[j][0] *= f0, o[j][1] *= f0, o[j][2] *= f1, o[j][3] *= f1;
+      for (int j = 0; j < NO; ++j)
+        o[j][0] *= f0, o[j][1] *= NARROW ? f1 : f0, o[j][2] *= NARROW ? f0 : f1, o[j][3] *= f1;
       l0 *= f0;
       l1 *= f1;
       m0 = x0;
@@ -200,26 +271,50 @@ __device__ __forceinline__ bool thin_segment(const Args& a, const AttnArgs& g, c
     }
     const float n0 = m0 == -INFINITY ? 0.f : -m0 * g.scale_log2, n1 = m1 == -INFINITY ? 0.f : -m1 * g.scale_log2;
     if (!landed(ki + 1)) return false;
-    uint32_t p[4][2];  // weights as bf16 pairs: fragment n, row r0 / r1
+    uint32_t p[NF][2];  // weights as bf16 pairs: of fragment n, row r0 / r1, or (narrow) row gr
+    if constexpr (NARROW) {
 #pragma unroll
-    for (int n = 0; n < 4; ++n) {
-      float e0 = ex2(fmaf(s[n][0], g.scale_log2, n0)), e1 = ex2(fmaf(s[n][1], g.scale_log2, n0));
-      float e2 = ex2(fmaf(s[n][2], g.scale_log2, n1)), e3 = ex2(fmaf(s[n][3], g.scale_log2, n1));
-      l0 += e0 + e1;
-      l1 += e2 + e3;
-      if (Q8) {
-        const float2 sc = lds_float2(sbase + L::SCALE_OFF + (vs * TILE + first_key + 8 * n + 2 * q) * 4);
-        e0 *= sc.x, e1 *= sc.y, e2 *= sc.x, e3 *= sc.y;
-        if (fix) {  // a hidden key's scale may be anything
-          const int pos = k0 + first_key + 8 * n + 2 * q;
-          if (pos >= see0) e0 = 0.f;
-          if (pos + 1 >= see0) e1 = 0.f;
-          if (pos >= see1) e2 = 0.f;
-          if (pos + 1 >= see1) e3 = 0.f;
+      for (int n = 0; n < 2; ++n) {
+        float e0 = ex2(fmaf(s[n][0], g.scale_log2, n0)), e1 = ex2(fmaf(s[n][1], g.scale_log2, n1));
+        float e2 = ex2(fmaf(s[n][2], g.scale_log2, n0)), e3 = ex2(fmaf(s[n][3], g.scale_log2, n1));
+        l0 += e0 + e2;
+        l1 += e1 + e3;
+        if (Q8) {
+          const uint32_t at = sbase + L::SCALE_OFF + (vs * TILE + first_key + 16 * n + gr) * 4;
+          const float sa = lds_float(at), sb = lds_float(at + 32);
+          e0 *= sa, e1 *= sa, e2 *= sb, e3 *= sb;
+          if (fix) {  // a hidden key's scale may be anything
+            const int pos = k0 + first_key + 16 * n + gr;
+            if (pos >= see0) e0 = 0.f;
+            if (pos >= see1) e1 = 0.f;
+            if (pos + 8 >= see0) e2 = 0.f;
+            if (pos + 8 >= see1) e3 = 0.f;
+          }
         }
+        p[n][0] = movmatrix_trans(pack_bf16x2(e0, e1));
+        p[n][1] = movmatrix_trans(pack_bf16x2(e2, e3));
       }
-      p[n][0] = pack_bf16x2(e0, e1);
-      p[n][1] = pack_bf16x2(e2, e3);
+    } else {
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        float e0 = ex2(fmaf(s[n][0], g.scale_log2, n0)), e1 = ex2(fmaf(s[n][1], g.scale_log2, n0));
+        float e2 = ex2(fmaf(s[n][2], g.scale_log2, n1)), e3 = ex2(fmaf(s[n][3], g.scale_log2, n1));
+        l0 += e0 + e1;
+        l1 += e2 + e3;
+        if (Q8) {
+          const float2 sc = lds_float2(sbase + L::SCALE_OFF + (vs * TILE + first_key + 8 * n + 2 * q) * 4);
+          e0 *= sc.x, e1 *= sc.y, e2 *= sc.x, e3 *= sc.y;
+          if (fix) {  // a hidden key's scale may be anything
+            const int pos = k0 + first_key + 8 * n + 2 * q;
+            if (pos >= see0) e0 = 0.f;
+            if (pos + 1 >= see0) e1 = 0.f;
+            if (pos >= see1) e2 = 0.f;
+            if (pos + 1 >= see1) e3 = 0.f;
+          }
+        }
+        p[n][0] = pack_bf16x2(e0, e1);
+        p[n][1] = pack_bf16x2(e2, e3);
+      }
     }
     if (!Q8 && fix) {
       // Values that must not reach a row through its zero weights (0 x NaN) are replaced by zeros in
@@ -261,16 +356,20 @@ __device__ __forceinline__ bool thin_segment(const Args& a, const AttnArgs& g, c
     }
     // ---- O += P V
 #pragma unroll
-    for (int n = 0; n < 4; n += 2) {
-      const int kb = first_key + 8 * n;
+    for (int n = 0; n < NF; n += NF / 2) {
+      const int kb = first_key + 32 / NF * n;
       if (!Q8) {
 #pragma unroll
         for (int j = 0; j < D / 16; ++j) {
           const int row = kb + ((lane >> 3) & 1) * 8 + (lane & 7), ch = 2 * j + (lane >> 4);
           uint32_t v[4];
           ldmatrix_x4_trans(vbase + (ch >> 3) * L::PANEL + row * 128 + (((ch & 7) ^ (row & 7)) << 4), v);
-          mma16816(o[2 * j], p[n][0], p[n][1], p[n + 1][0], p[n + 1][1], v[0], v[1]);
-          mma16816(o[2 * j + 1], p[n][0], p[n][1], p[n + 1][0], p[n + 1][1], v[2], v[3]);
+          if constexpr (NARROW) {
+            mma16816(o[j], v[0], v[2], v[1], v[3], p[n][0], p[n][1]);
+          } else {
+            mma16816(o[2 * j], p[n][0], p[n][1], p[n + 1][0], p[n + 1][1], v[0], v[1]);
+            mma16816(o[2 * j + 1], p[n][0], p[n][1], p[n + 1][0], p[n + 1][1], v[2], v[3]);
+          }
         }
       } else {
         uint32_t v[4][D / 32];
@@ -287,21 +386,26 @@ __device__ __forceinline__ bool thin_segment(const Args& a, const AttnArgs& g, c
         }
 #pragma unroll
         for (int w = 0; w < D / 32; ++w) {
-          mma16816(o[4 * w], p[n][0], p[n][1], p[n + 1][0], p[n + 1][1], expand_pair<0>(v[0][w], v[1][w]),
-                   expand_pair<0>(v[2][w], v[3][w]));
-          mma16816(o[4 * w + 1], p[n][0], p[n][1], p[n + 1][0], p[n + 1][1], expand_pair<1>(v[0][w], v[1][w]),
-                   expand_pair<1>(v[2][w], v[3][w]));
-          mma16816(o[4 * w + 2], p[n][0], p[n][1], p[n + 1][0], p[n + 1][1], expand_pair<2>(v[0][w], v[1][w]),
-                   expand_pair<2>(v[2][w], v[3][w]));
-          mma16816(o[4 * w + 3], p[n][0], p[n][1], p[n + 1][0], p[n + 1][1], expand_pair<3>(v[0][w], v[1][w]),
-                   expand_pair<3>(v[2][w], v[3][w]));
+          const uint32_t a0 = expand_pair<0>(v[0][w], v[1][w]), a1 = expand_pair<1>(v[0][w], v[1][w]);
+          const uint32_t a2 = expand_pair<2>(v[0][w], v[1][w]), a3 = expand_pair<3>(v[0][w], v[1][w]);
+          const uint32_t b0 = expand_pair<0>(v[2][w], v[3][w]), b1 = expand_pair<1>(v[2][w], v[3][w]);
+          const uint32_t b2 = expand_pair<2>(v[2][w], v[3][w]), b3 = expand_pair<3>(v[2][w], v[3][w]);
+          if constexpr (NARROW) {
+            mma16816(o[2 * w], a0, a1, b0, b1, p[n][0], p[n][1]);
+            mma16816(o[2 * w + 1], a2, a3, b2, b3, p[n][0], p[n][1]);
+          } else {
+            mma16816(o[4 * w], p[n][0], p[n][1], p[n + 1][0], p[n + 1][1], a0, b0);
+            mma16816(o[4 * w + 1], p[n][0], p[n][1], p[n + 1][0], p[n + 1][1], a1, b1);
+            mma16816(o[4 * w + 2], p[n][0], p[n][1], p[n + 1][0], p[n + 1][1], a2, b2);
+            mma16816(o[4 * w + 3], p[n][0], p[n][1], p[n + 1][0], p[n + 1][1], a3, b3);
+          }
         }
       }
     }
     release(vs);
   }
 #pragma unroll
-  for (int w = 1; w <= 2; w <<= 1) {
+  for (int w = NARROW ? 4 : 1; w <= (NARROW ? 16 : 2); w <<= 1) {
     l0 += __shfl_xor_sync(0xffffffffu, l0, w);
     l1 += __shfl_xor_sync(0xffffffffu, l1, w);
   }
@@ -310,36 +414,44 @@ __device__ __forceinline__ bool thin_segment(const Args& a, const AttnArgs& g, c
   float* s_l = s_m + 128;
   uint8_t* s_b = x.smem + L::ML_OFF + 8 * TILE;
   float* region = reinterpret_cast<float*>(x.smem + L::Q_OFF);
-  // column of o[j][0]: bf16 fragments are natural, e4m3's column 2q of step j is d = j + (D/8) 2q; its
-  // place in the region is swizzled so that a warp's 32 stores go to 32 banks
+  // column of o[j][0]: bf16 fragments are natural, e4m3's column 2q of step j is d = j + (D/8) 2q (narrow:
+  // row gr of step pair j is d = 2 j + (D/8) gr); its place in the region is swizzled so that a warp's 32
+  // stores go to 32 banks
   auto place = [](int row, int col) {
-    return row * D + (Q8 ? col ^ ((col >> 5 & 3) << 3) ^ (row & 7) : col ^ ((row & 3) << 3) ^ (row >> 2 & 1));
+    if constexpr (NARROW)
+      return row * D + (Q8 ? col ^ ((col >> 5 & 3) << 2) ^ (row >> 1 & 3) : col ^ ((row >> 1 & 3) << 3));
+    else
+      return row * D + (Q8 ? col ^ ((col >> 5 & 3) << 3) ^ (row & 7) : col ^ ((row & 3) << 3) ^ (row >> 2 & 1));
   };
   auto at = [&](int j, int e) {
-    return place(gr + (e >> 1) * 8, Q8 ? j + NT * (2 * q + (e & 1)) : 8 * j + 2 * q + (e & 1));
+    if constexpr (NARROW)
+      return place(r0 + (e & 1), Q8 ? 2 * j + (e >> 1) + NT * gr : 16 * j + gr + 8 * (e >> 1));
+    else
+      return place(gr + (e >> 1) * 8, Q8 ? j + NT * (2 * q + (e & 1)) : 8 * j + 2 * q + (e & 1));
   };
   // every warp has read its query rows (the first barrier), then their memory is written (the second)
   if (!team()) return false;
   float* mine = region + x.warp * 16 * D;
 #pragma unroll
-  for (int j = 0; j < NT; ++j) {
+  for (int j = 0; j < NO; ++j) {
     mine[at(j, 0)] = o[j][0];
     mine[at(j, 1)] = o[j][1];
   }
-  if (rows > 8) {
+  if (NARROW || rows > 8) {
 #pragma unroll
-    for (int j = 0; j < NT; ++j) {
+    for (int j = 0; j < NO; ++j) {
       mine[at(j, 2)] = o[j][2];
       mine[at(j, 3)] = o[j][3];
     }
   }
-  if (q == 0) {
-    s_m[x.warp * 16 + gr] = m0 == -INFINITY ? m0 : m0 * g.scale_log2;
-    s_m[x.warp * 16 + gr + 8] = m1 == -INFINITY ? m1 : m1 * g.scale_log2;
-    s_l[x.warp * 16 + gr] = l0;
-    s_l[x.warp * 16 + gr + 8] = l1;
-    s_b[x.warp * 16 + gr] = bad0;
-    s_b[x.warp * 16 + gr + 8] = bad1;
+  if (NARROW ? gr == 0 : q == 0) {
+    const int a0 = x.warp * 16 + (r0 & 15), a1 = x.warp * 16 + (r1 & 15);
+    s_m[a0] = m0 == -INFINITY ? m0 : m0 * g.scale_log2;
+    s_m[a1] = m1 == -INFINITY ? m1 : m1 * g.scale_log2;
+    s_l[a0] = l0;
+    s_l[a1] = l1;
+    s_b[a0] = bad0;
+    s_b[a1] = bad1;
   }
   if (!team()) return false;
   const bool whole = sg.t0 == 0 && sg.t1 == sg.nt;
