@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(Layout<D, Q8>::THREADS, 1)
     reg_dec<L::REGS_ISSUE>();
     if (warp == 0) {
       // ---------------------------------------------- segments, and copies: K and V of every key tile
-      const int per_page = a.page_size / g.chunk, per_tile = TILE / g.chunk;
+      const int per_page = g.per_page, per_tile = TILE >> g.chunk_log;
       // per ring (tile form, thin form): tiles issued, next slot, its round's parity, landing barrier
       struct Ring {
         int n, st, ph, fl;
@@ -154,14 +154,14 @@ __global__ void __launch_bounds__(Layout<D, Q8>::THREADS, 1)
         Ring rg = now ? thin_ring : tile_ring;
         const int slots = now ? L::NH_ : L::NL, full0 = now ? L::HFULL : L::LFULL, empty0 = now ? L::HEMPTY : L::LEMPTY;
         const uint32_t ring0 = sbase + (now ? L::H_OFF : L::L_OFF);
-        const int last = ceil_div(sg.len, g.chunk);  // chunks of the sequence
+        const int last = (sg.len + g.chunk - 1) >> g.chunk_log;  // chunks of the sequence
         int c0 = sg.t0 * per_tile;
         // the pool's rows where chunks c0 .. c0 + 31 start, and the 32 after them, one per lane
         auto rows_of = [&](int c) -> int {
           if (c >= last) return 0;
           const int e = c / per_page;
           const int page = max(kv::page_of(a, sg.b, e), 0);  // (a bad one is recorded, and not followed)
-          return (page * a.heads + sg.h) * a.page_size + (c - e * per_page) * g.chunk;
+          return (page * a.heads + sg.h) * a.page_size + ((c - e * per_page) << g.chunk_log);
         };
         int rows = rows_of(c0 + lane), rows2 = rows_of(c0 + 32 + lane);
         for (int kt = sg.t0; ok && kt < sg.t1; ++kt) {
@@ -908,6 +908,8 @@ cudaError_t launch_kv_attention(const kv::Args& args, bool q8, const uint16_t* q
   g.merge = static_cast<long long>(a.T) * g.group <= static_cast<long long>(THIN_ROWS) * a.B ? 3 : 16;
   g.chunk = a.page_size & -a.page_size;  // the largest power of two that divides the page
   if (g.chunk > TILE) g.chunk = TILE;
+  g.chunk_log = __builtin_ctz(static_cast<unsigned>(g.chunk));
+  g.per_page = a.page_size / g.chunk;
   const unsigned long long ns = wait_limit_ns();
   g.wait_cycles = ns > (~0ull) / 3 ? ~0ull : ns * 21 / 10;
   g.poll = ns < 20000ull;

@@ -19,7 +19,8 @@ struct AttnArgs {
   int q_heads, group, tpt;  // tpt: tokens per query tile
   int tokens;               // per item: of a pair of tiles, or of one
   int merge;                // what cutting items costs, in key tiles
-  int chunk;                // rows of one copy, divides page_size and TILE
+  int chunk, chunk_log;     // rows of one copy (a power of two), divides page_size and TILE
+  int per_page;             // copies of a page
   unsigned long long wait_cycles;
   bool poll;  // the limit is too short for waits inside an instruction
 };
