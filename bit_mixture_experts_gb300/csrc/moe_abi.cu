@@ -1,7 +1,8 @@
 // extern "C" entry points of libmoe_w4.so: argument checks, the device error
 // word, and the launch sequence of the layer.  Every compute step runs in the
-// kernels of moe_route.cu, moe_gemm_tc.cu, moe_gemm_gemv.cu, moe_decode.cu and
-// moe_combine.cu; nothing here touches tensor data on the host.
+// kernels of moe_route.cu, moe_gemm_tc.cu, moe_gemm_gemv.cu, moe_decode.cu,
+// moe_combine.cu, moe_kv_cache.cu and moe_kv_attn.cu; nothing here touches
+// tensor data on the host.
 #include <atomic>
 #include <mutex>
 

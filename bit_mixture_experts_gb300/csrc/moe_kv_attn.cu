@@ -17,15 +17,27 @@
 // 2^8, which bf16 holds as accurately as numbers below one): rare after the
 // first tiles, and it saves a pass over O per key tile.
 //
-// Roles (warps): 0 copies keys and values (TMA boxes of up to 128 rows of a
-// page into 128-byte swizzled tiles), 1 issues the MMAs, 2 and 3 load the two
-// query tiles, 4-7 and 8-11 the softmax of the pair's tiles.  With an e4m3
+// Roles (warps): 0 works out the CTA's segments and copies keys and values (TMA
+// boxes of up to 128 rows of a page into 128-byte swizzled tiles), 1 issues the
+// MMAs, 2 and 3 load the queries, 4-7 and 8-11 the softmax of the pair's tiles.
+// Items of one tile alternate key tiles between the two halves; items of at most
+// 32 rows take the form of moe_kv_thin.cuh in the same kernel.  With an e4m3
 // cache warps 12-15 expand the tiles to bf16: e4m3 times a power of two is
 // exact in bf16, so everything after that is the same as for a bf16 cache, to
 // the bit.  Every wait is bounded (MOE_DEV_TIMEOUT).
 //
 // Roundings: P to bf16 (the tensor core's operand; sums are taken of the
 // unrounded values), the output to bf16.  All else is FP32.
+//
+// What bounds it, by calls in a row from a CUDA graph (16 query heads over 2 KV
+// heads of 128): 4096 tokens over 32K cached ones take 0.79 ms, 1.51 PFLOP/s, 0.78
+// of the rate of a large plain product; the tensor pipe is active 62 % of the
+// time and waits for the softmax threads, whose tile takes them longer (the
+// loads from TMEM, 128 exponentials and the conversions of a row, one after
+// another in one thread) than its two products.  Six chunks of 440 to 1777
+// tokens over an e4m3 cache 0.32 ms.  A 512-token prompt takes 16 us and one
+// token over 4K keys 11 us, nearly all of it a chain of latencies that no size
+// enters: launch, plan, first page, first keys, scores, output, merge.
 #include <cuda.h>
 #include <string.h>
 
@@ -855,7 +867,8 @@ cudaError_t launch_kv_expand(const kv::Args& a, uint16_t* k, uint16_t* v, int ti
 // Bytes of keys (or values) when an e4m3 cache is to be expanded to bf16 before an attention, else 0.  The
 // attention of a pair of query tiles expands its keys and values on chip, every pair the same ones: from two
 // pairs per sequence on, on average, one pass over the cache before it costs less (six chunks of 440 to 1777
-// tokens over 1K to 10K: 457 us on chip).  What the sequences' tables have room for is reserved, up to 8 GiB.
+// tokens over 1K to 10K: 457 us on chip, 335 us expanded first).  What the sequences' tables have room for is
+// reserved, up to 8 GiB.
 size_t kv_expanded_bytes(const kv::Args& a, bool q8, int q_heads) {
   if (!q8 || a.B > 65535 || static_cast<long long>(a.T) * (q_heads / a.heads) < 4ll * TILE * a.B) return 0;
   const long long rows = static_cast<long long>(a.B) * ((a.most + TILE - 1) / TILE) * TILE * a.heads;
@@ -903,8 +916,9 @@ cudaError_t launch_kv_attention(const kv::Args& args, bool q8, const uint16_t* q
   // prompt 20.5 -> 18.0 us, over 8000 cached tokens 64 -> 57 us; a 2048-token one 50 us as pairs, 58 single)
   const long long pairs = (a.T + 2ll * g.tpt - 1) / (2 * g.tpt) * a.heads;
   g.tokens = pairs <= num_sms() / 2 ? g.tpt : 2 * g.tpt;
-  // cutting costs a tile's rows written, read and joined: 10 where 16 is taken, 2048 tokens 49.8 -> 43.3 us,
-  // four chunks of 300 over 3000 39.7 -> 36.4; the few rows of decoding cost little (1 to 6 measure alike)
+  // cutting costs a tile's rows written, read and joined: with 16 in place of 10 (single tiles) and 6 (pairs)
+  // 2048 tokens 49.8 -> 43.3 us, four chunks of 300 over 3000 39.7 -> 36.4 us, six e4m3 chunks 335 -> 328 us; the
+  // few rows of decoding cost little (1, 3 and 6 measure alike)
   g.merge = static_cast<long long>(a.T) * g.group <= static_cast<long long>(THIN_ROWS) * a.B ? 3 : 16;
   g.chunk = a.page_size & -a.page_size;  // the largest power of two that divides the page
   if (g.chunk > TILE) g.chunk = TILE;

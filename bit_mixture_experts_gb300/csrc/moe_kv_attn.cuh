@@ -244,8 +244,8 @@ __device__ __forceinline__ int uniform(int x) {
 
 // Bounded wait of a whole warp on phase `parity` of `bar`; false when it gave up (recorded) or another role
 // has.  The waiting is done by try_wait with its own time limit, which wakes sooner than one that is told to
-// sleep for longer (832 -> 798 us at 4096 tokens over 32K): the barriers here are handed over every
-// thousand cycles.
+// sleep for longer (4096 tokens over 32K, 832 us with that, 798 without): the barriers here are handed over
+// every thousand cycles.
 __device__ __forceinline__ bool wait_warp_untraced(uint32_t bar, uint32_t parity, volatile int* s_abort, int* err,
                                                    const AttnArgs& g) {
   if (__all_sync(0xffffffffu, g.poll ? ptx::mbar_test_wait(bar, parity) : ptx::mbar_try_wait(bar, parity))) return true;

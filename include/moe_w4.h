@@ -472,8 +472,10 @@ int moe_layer_forward_host(const uint16_t* x_host, const float* logits_host, uin
  */
 enum {
   MOE_KV_BF16 = 0, /* k, v bf16 */
-  MOE_KV_E4M3 = 1  /* k, v 8-bit floats (1-4-3, bias 7, no infinity) times a float32 scale, a power
-                      of two, per token and head */
+  MOE_KV_E4M3 = 1  /* k, v 8-bit floats (1-4-3, bias 7, no infinity) times a float32 scale per token
+                      and head: a power of two, or NaN (the whole row is NaN then).  moe_kv_append
+                      never writes the codes 127 and 255 under a finite scale; a cache filled in
+                      another way must not hold them either (their value is not defined). */
 };
 
 typedef struct {
