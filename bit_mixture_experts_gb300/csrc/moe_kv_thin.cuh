@@ -27,7 +27,7 @@
 // j + (D/8) gr belongs to step j.
 //
 // Measured (calls in a row from a CUDA graph, 2 KV heads of 128, 8 query heads
-// each): 64 bf16 sequences over 300 to 8K tokens 57 us (floor 45: the keys and
+// each): 64 bf16 sequences over 1K to 8K tokens 57 us (floor 45: the keys and
 // values at the copy rate), 8 e4m3 sequences 29.7 us (floor 13), of which copies
 // alone, nothing computed, take 23, and launch, plan and merge 10.
 #pragma once
