@@ -332,36 +332,39 @@ __device__ __forceinline__ bool thin_segment(const Args& a, const AttnArgs& g, c
       // this warp's 32 rows: those past the sequence's end, and those that some row does not see yet
       // and that are not finite (rows that do see one take note).  An e4m3 code is always finite.
       constexpr int LANES = D / 8, RPI = 32 / LANES;  // 16-byte pieces of a row, rows at a time
-      const int piece = lane % LANES;
+      const int piece = lane % LANES, sub = lane / LANES;
       const int end = min(32, sg.len - k0 - first_key);  // this warp's rows before the sequence's end
-      const uint32_t at = vbase + (piece >> 3) * L::PANEL + first_key * 128, sub = lane / LANES;
+      const uint32_t at = vbase + (piece >> 3) * L::PANEL + first_key * 128;
+      uint32_t wipe = 0;  // the rows that are not finite
 #pragma unroll 1
       for (int rb = max(0, vis0 - k0 - first_key) / RPI * RPI; rb < end; rb += RPI) {
-        const int rr = rb + sub, key = k0 + first_key + rr;
-        const uint32_t p = at + rr * 128 + (((piece & 7) ^ (rr & 7)) << 4);
-        bool wipe = false;
-        if (key >= vis0 && rr < end) {
-          const uint4 v = lds128(p);
-          uint32_t acc = ptx::bf16x2_fma(v.x, 0u, 0u);
+        const int rr = rb + sub;
+        uint32_t acc = 0;
+        if (k0 + first_key + rr >= vis0 && rr < end) {
+          const uint4 v = lds128(at + rr * 128 + (((piece & 7) ^ (rr & 7)) << 4));
+          acc = ptx::bf16x2_fma(v.x, 0u, 0u);
           acc = ptx::bf16x2_fma(v.y, 0u, acc);
           acc = ptx::bf16x2_fma(v.z, 0u, acc);
           acc = ptx::bf16x2_fma(v.w, 0u, acc);
-          wipe = (acc & 0x7fff7fffu) != 0;  // 0 x Inf, 0 x NaN: NaN
         }
-        const uint32_t hit = __ballot_sync(0xffffffffu, wipe);
-        if (hit >> (lane / LANES * LANES) & ((1u << LANES) - 1u)) sts128(p, make_uint4(0, 0, 0, 0));
+        const uint32_t hit = __ballot_sync(0xffffffffu, (acc & 0x7fff7fffu) != 0);  // 0 x Inf, 0 x NaN: NaN
 #pragma unroll
         for (int h = 0; h < RPI; ++h) {
           if (hit >> (h * LANES) & ((1u << LANES) - 1u)) {
-            const int other = k0 + first_key + rb + h;
-            bad0 |= other < see0;
-            bad1 |= other < see1;
+            const int key = k0 + first_key + rb + h;
+            wipe |= 1u << (rb + h);
+            bad0 |= key < see0;
+            bad1 |= key < see1;
           }
         }
       }
+      // where two warps have the same keys, both have looked at them before either replaces any
+      if (groups == 2 && !team()) return false;
 #pragma unroll
-      for (int rb = 0; rb < 32; rb += RPI)
-        if (rb + static_cast<int>(sub) >= end) sts128(at + (rb + sub) * 128 + (piece & 7) * 16, make_uint4(0, 0, 0, 0));
+      for (int rb = 0; rb < 32; rb += RPI) {
+        const int rr = rb + sub;
+        if (rr >= end || (wipe >> rr & 1)) sts128(at + rr * 128 + (piece & 7) * 16, make_uint4(0, 0, 0, 0));
+      }
       ptx::fence_proxy_async_smem();  // the copies overwrite what was written here
       __syncwarp();
     }

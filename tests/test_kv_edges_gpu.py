@@ -58,6 +58,25 @@ def test_value_that_is_not_finite_under_a_zero_weight(fmt, d, new):
     assert torch.isnan(out).all()
 
 
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("new,g", [(8, 4), (4, 8), (3, 8), (5, 5)])
+def test_value_that_is_not_finite_and_only_some_rows_see(fmt, new, g):
+    """More than 16 query rows: two warps have the same keys, for different rows, and both must notice a value
+    that is not finite whichever comes first.  Many calls, since it is a matter of time."""
+    import torch
+    s = K.Setup([new], [700], heads=2, g=g, d=128, page=16, fmt=fmt, seed=9)
+    for p in range(700 - new + 1, 700):  # position p: seen by the new tokens from p on
+        at = (int(s.table[0, p // 16]), slice(None), p % 16)
+        if fmt == "bf16":
+            s.cache.v[at] = float("nan")
+        else:
+            s.cache.v_scale[at] = float("nan")
+    outs = [s.cache.attention(s.q, s.batch) for _ in range(200)]
+    _ok()
+    for out in outs:
+        assert torch.isfinite(out[0]).all() and torch.isnan(out[1:]).all()
+
+
 @pytest.mark.parametrize("q_lens,kv_lens,g,d,page", [([700], [900], 2, 128, 16), ([600, 1, 580], [600, 1, 1100], 4, 64, 48),
                                                      ([300, 299, 0], [300, 200, 70], 8, 128, 64)])
 def test_many_rows_over_an_e4m3_cache(q_lens, kv_lens, g, d, page):
