@@ -35,7 +35,7 @@
 // time and waits for the softmax threads, whose tile takes them longer (the
 // loads from TMEM, 128 exponentials and the conversions of a row, one after
 // another in one thread) than its two products.  Six chunks of 440 to 1777
-// tokens over an e4m3 cache 0.32 ms.  A 512-token prompt takes 16 us and one
+// tokens over an e4m3 cache 0.32 ms.  A 512-token prompt takes 15 us and one
 // token over 4K keys 11 us, nearly all of it a chain of latencies that no size
 // enters: launch, plan, first page, first keys, scores, output, merge.
 #include <cuda.h>
@@ -915,7 +915,7 @@ cudaError_t launch_kv_attention(const kv::Args& args, bool q8, const uint16_t* q
   g.group = q_heads / a.heads;
   g.tpt = TILE / g.group;
   // pairs of tiles; but with so few of them that half of the SMs would have none, single tiles (a 512-token
-  // prompt 20.5 -> 18.0 us, over 8000 cached tokens 64 -> 57 us; a 2048-token one 50 us as pairs, 58 single)
+  // prompt 20.5 -> 18.0 us, over 8000 cached tokens 64 -> 57 us, a 2048-token one 50 us as pairs, 58 single)
   const long long pairs = (a.T + 2ll * g.tpt - 1) / (2 * g.tpt) * a.heads;
   g.tokens = pairs <= num_sms() / 2 ? g.tpt : 2 * g.tpt;
   // cutting costs a tile's rows written, read and joined: with 16 in place of 10 (single tiles) and 6 (pairs)
