@@ -53,6 +53,17 @@ namespace {
 
 using namespace kv;
 
+// Zeros in place of the elements that are not finite of row `row` (r: its swizzle) of a bf16 tile.  A call,
+// so that what hardly ever runs stays out of the loop over the key tiles.
+template <int NH>
+__device__ __noinline__ void keep_finite(uint32_t row, int r) {
+#pragma unroll 1
+  for (int c = 0; c < NH * 8; ++c) {
+    const uint32_t at = row + (c >> 3) * (TILE * 128) + (((c & 7) ^ r) << 4);
+    sts128(at, bf16x8_finite(lds128(at)));
+  }
+}
+
 template <int D, bool Q8>
 __global__ void __launch_bounds__(Layout<D, Q8>::THREADS, 1)
     kv_attention_kernel(const kv::Args a, const AttnArgs g, const __grid_constant__ CUtensorMap tmap_k,
@@ -446,8 +457,9 @@ __global__ void __launch_bounds__(Layout<D, Q8>::THREADS, 1)
         s_ph ^= 1;
         ptx::tc_fence_after();
         // Values that must not reach a row through its zero weights (0 x NaN): rows of V past the
-        // sequence's end, and rows that some query of the pair does not see yet and that are not
-        // finite, are replaced by zeros; the latter's mask lets the rows that do see them know.
+        // sequence's end, and the elements that are not finite of rows that some query of the pair does
+        // not see yet, are replaced by zeros; the mask of the latter's rows lets those that do see them
+        // know.
         const bool fix = k0 + TILE > min(vis0, sg.len);
         if (t == 0 || !pair) {
           if (fix) {
@@ -468,13 +480,14 @@ __global__ void __launch_bounds__(Layout<D, Q8>::THREADS, 1)
               }
             }
             const bool nonfinite = (acc & 0x7fff7fffu) != 0;  // 0 x Inf, 0 x NaN: NaN
-            if (nonfinite || p >= sg.len) {
+            if (p >= sg.len) {
 #pragma unroll
               for (int c = 0; c < NH * 8; ++c)
                 sts128(row + (c >> 3) * PANEL + (((c & 7) ^ (r & 7)) << 4), make_uint4(0, 0, 0, 0));
             }
             const uint32_t mask = __ballot_sync(0xffffffffu, nonfinite);
             if (lane == 0) s_bad[(un & 1) * 4 + w] = mask;
+            if (nonfinite) keep_finite<NH>(row, r & 7);
             ptx::fence_proxy_async_smem();
             __syncwarp();
           }
@@ -612,7 +625,7 @@ __global__ void __launch_bounds__(Layout<D, Q8>::THREADS, 1)
             ptx::tmem_wait_ld();
           }
           if (bad) {
-            // values that are not finite and that this row sees enter the sums as they are
+            // elements that are not finite and that this row sees enter the sums as they are
             for (int p = max(vis0, sg.t0 * TILE); p < min(vis, sg.t1 * TILE); ++p) {
               const int page = kv::find_page(a, sg.b, p);
               if (page < 0) continue;

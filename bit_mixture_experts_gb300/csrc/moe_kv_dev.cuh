@@ -86,6 +86,15 @@ __device__ __forceinline__ uint32_t bf16x2_mul(uint32_t a, uint32_t b) {
   return d;
 }
 
+// A bf16 pair with zeros in place of infinities and NaN.
+__device__ __forceinline__ uint32_t bf16x2_finite(uint32_t x) {
+  return x & (((x & 0x7f80u) != 0x7f80u ? 0xffffu : 0u) | ((x & 0x7f800000u) != 0x7f800000u ? 0xffff0000u : 0u));
+}
+
+__device__ __forceinline__ uint4 bf16x8_finite(uint4 x) {
+  return make_uint4(bf16x2_finite(x.x), bf16x2_finite(x.y), bf16x2_finite(x.z), bf16x2_finite(x.w));
+}
+
 // Four e4m3 codes -> four bf16 values times s (a bf16 pair).  The code's bits s eeee mmm become
 // s 0000eeee mmm0000, a bf16 that is 2^-120 of the code's value (its subnormals are bf16 subnormals);
 // s holds 2^120 times the scale as far as bf16 goes.  The product is exact short of bf16's own

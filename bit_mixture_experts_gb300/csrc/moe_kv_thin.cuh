@@ -329,13 +329,13 @@ __device__ __forceinline__ bool thin_segment(const Args& a, const AttnArgs& g, c
     }
     if (!Q8 && fix) {
       // Values that must not reach a row through its zero weights (0 x NaN) are replaced by zeros in
-      // this warp's 32 rows: those past the sequence's end, and those that some row does not see yet
-      // and that are not finite (rows that do see one take note).  An e4m3 code is always finite.
+      // this warp's 32 keys: all past the sequence's end, and the elements that are not finite of those
+      // that some row does not see yet (rows that do see one take note).  An e4m3 code is always finite.
       constexpr int LANES = D / 8, RPI = 32 / LANES;  // 16-byte pieces of a row, rows at a time
       const int piece = lane % LANES, sub = lane / LANES;
       const int end = min(32, sg.len - k0 - first_key);  // this warp's rows before the sequence's end
       const uint32_t at = vbase + (piece >> 3) * L::PANEL + first_key * 128;
-      uint32_t wipe = 0;  // the rows that are not finite
+      uint32_t wipe = 0;  // the keys whose values are not all finite
 #pragma unroll 1
       for (int rb = max(0, vis0 - k0 - first_key) / RPI * RPI; rb < end; rb += RPI) {
         const int rr = rb + sub;
@@ -358,12 +358,20 @@ __device__ __forceinline__ bool thin_segment(const Args& a, const AttnArgs& g, c
           }
         }
       }
-      // where two warps have the same keys, both have looked at them before either replaces any
+      // where two warps have the same keys, both have looked at them before either replaces any (then both
+      // replace the same: it does not matter whose reads and writes come first)
       if (groups == 2 && !team()) return false;
 #pragma unroll
       for (int rb = 0; rb < 32; rb += RPI) {
         const int rr = rb + sub;
-        if (rr >= end || (wipe >> rr & 1)) sts128(at + rr * 128 + (piece & 7) * 16, make_uint4(0, 0, 0, 0));
+        if (rr >= end) sts128(at + rr * 128 + (piece & 7) * 16, make_uint4(0, 0, 0, 0));
+      }
+      if (wipe) {
+#pragma unroll 1
+        for (int rr = sub; rr < end; rr += RPI) {
+          const uint32_t place = at + rr * 128 + (((piece & 7) ^ (rr & 7)) << 4);
+          if (wipe >> rr & 1) sts128(place, bf16x8_finite(lds128(place)));
+        }
       }
       ptx::fence_proxy_async_smem();  // the copies overwrite what was written here
       __syncwarp();
@@ -493,7 +501,7 @@ __device__ __forceinline__ bool thin_segment(const Args& a, const AttnArgs& g, c
     }
     const int tok = r / g.group;
     if (!Q8 && bad) {
-      // values that are not finite and that this row sees enter the sums as they are
+      // elements that are not finite and that this row sees enter the sums as they are
       for (int p = max(vis0, sg.t0 * TILE); p < min(vis0 + tok, sg.t1 * TILE); ++p) {
         const int page = find_page(a, sg.b, p);
         if (page < 0) continue;
