@@ -108,19 +108,30 @@ class PagedKVCache:
             return torch.empty(shape, dtype=dtype, device=self.device)
 
     def _workspace(self, batch, q_heads, stream):
-        """(pointer, bytes) of the attention's scratch for calls on `stream`: one per stream, so that calls on
-        two streams share none, grown to the largest call's need.  A first call of its size allocates: make it
-        before a graph capture."""
+        """The attention's scratch for a call on `stream`, a tensor or (pointer, bytes).  Calls outside graph
+        captures have one per stream, which grows to the largest call's need.  A call that torch.cuda.graph
+        captures has its own, from the graph's memory: no later call frees or shares what the graph's replays
+        write to."""
         need = batch.workspace.get((self, q_heads))
         if need is None:
             need = max(_lib.moe_kv_attention_workspace_size(self.struct, batch.struct, q_heads), 16)
             batch.workspace[(self, q_heads)] = need
+        if self._capturing(stream):
+            return self._empty((need,), torch.uint8, stream)
         key = _lib._stream(stream)
         have = self._workspaces.get(key)
         if have is None or have[1][1] < need:
             t = self._empty((need,), torch.uint8, stream)
             have = self._workspaces[key] = (t, (t.data_ptr(), t.nbytes))
         return have[1]
+
+    @staticmethod
+    def _capturing(stream):
+        """Whether calls on `stream` are being captured into a graph."""
+        if stream is None:
+            return torch.cuda.is_current_stream_capturing()
+        with torch.cuda.stream(stream):
+            return torch.cuda.is_current_stream_capturing()
 
     def append(self, k, v, batch, stream=None):
         """Write the new tokens' keys and values (bf16 [T, heads, d], strided views welcome) into the cache."""
@@ -147,7 +158,11 @@ class PagedKVCache:
         q_heads is a multiple of the cache's heads; scale defaults to 1/sqrt(d).  Returns bf16
         [T, q_heads, d], with ``return_lse`` also the scores' natural log-sum-exp, float32 [T, q_heads]
         (-inf for a token that sees no key; its output is 0).  `workspace` (uint8, at least
-        ``moe_kv_attention_workspace_size``) replaces the cache's own scratch of the stream."""
+        ``moe_kv_attention_workspace_size``) replaces the cache's own scratch of the stream.
+
+        In a ``torch.cuda.graph`` capture scratch and outputs come from the graph's memory.  A capture made in
+        another way has no memory of its own: give it `workspace` and `out`, keep them as long as the graph,
+        and replay no two graphs that were given the same ones at the same time."""
         self._rows(q, "q", batch)
         if out is None:
             out = (torch.empty_like(q, memory_format=torch.contiguous_format) if stream is None
