@@ -100,11 +100,17 @@ class PagedKVCache:
             raise ValueError(f"{name} must be bfloat16 [{batch.T}, {want}, {self.d}] on {self.device} with contiguous "
                              f"rows: got {t.dtype} {tuple(sh)} on {t.device}, strides {t.stride()}")
 
+    def _on(self, stream):
+        """Makes `stream`, a torch stream or a raw handle, the current one for a `with` block."""
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream, device=self.device)
+        return torch.cuda.stream(stream)
+
     def _empty(self, shape, dtype, stream):
         """An output for a call on `stream`: allocated as memory of that stream."""
         if stream is None:
             return torch.empty(shape, dtype=dtype, device=self.device)
-        with torch.cuda.stream(stream):
+        with self._on(stream):
             return torch.empty(shape, dtype=dtype, device=self.device)
 
     def _workspace(self, batch, q_heads, stream):
@@ -125,12 +131,11 @@ class PagedKVCache:
             have = self._workspaces[key] = (t, (t.data_ptr(), t.nbytes))
         return have[1]
 
-    @staticmethod
-    def _capturing(stream):
+    def _capturing(self, stream):
         """Whether calls on `stream` are being captured into a graph."""
         if stream is None:
             return torch.cuda.is_current_stream_capturing()
-        with torch.cuda.stream(stream):
+        with self._on(stream):
             return torch.cuda.is_current_stream_capturing()
 
     def append(self, k, v, batch, stream=None):
