@@ -64,6 +64,8 @@ class PagedKVCache:
         _lib.load()
         if k.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
             raise ValueError(f"pages must be bfloat16 or float8_e4m3fn, not {k.dtype}")
+        if k.device.type != "cuda":
+            raise ValueError(f"the cache's tensors must be on a CUDA device, not on {k.device}")
         self.fmt = "bf16" if k.dtype == torch.bfloat16 else "e4m3"
         if k.dim() != 4 or v.shape != k.shape or v.dtype != k.dtype or v.device != k.device:
             raise ValueError("k and v must be alike: [num_pages, heads, page_size, d]")
@@ -78,7 +80,7 @@ class PagedKVCache:
         if not all(t.is_contiguous() for t in pools):
             raise ValueError("the cache's tensors must be contiguous")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
-        self.device = k.device
+        self.device, self.device_index = k.device, k.device.index
         self.num_pages, self.heads, self.page_size, self.d = k.shape
         self._workspaces = {}
         self.struct = _lib.KVCache(k.data_ptr(), v.data_ptr(), _lib._ptr(k_scale), _lib._ptr(v_scale), self.num_pages,
@@ -99,6 +101,11 @@ class PagedKVCache:
             want = "heads" if heads is None else heads
             raise ValueError(f"{name} must be bfloat16 [{batch.T}, {want}, {self.d}] on {self.device} with contiguous "
                              f"rows: got {t.dtype} {tuple(sh)} on {t.device}, strides {t.stride()}")
+
+    def _check_device(self):
+        """Kernels are launched on the current device: it must be the cache's."""
+        if torch.cuda.current_device() != self.device_index:
+            raise ValueError(f"the cache is on {self.device}, but device {torch.cuda.current_device()} is the current one")
 
     def _on(self, stream):
         """Makes `stream`, a torch stream or a raw handle, the current one for a `with` block."""
@@ -140,12 +147,14 @@ class PagedKVCache:
 
     def append(self, k, v, batch, stream=None):
         """Write the new tokens' keys and values (bf16 [T, heads, d], strided views welcome) into the cache."""
+        self._check_device()
         self._rows(k, "k", batch, self.heads)
         self._rows(v, "v", batch, self.heads)
         _lib.moe_kv_append(k, v, self.struct, batch.struct, stream)
 
     def read(self, batch, out=None, stream=None):
         """What the cache holds at the new tokens' positions: bf16 (k, v), each [T, heads, d]."""
+        self._check_device()
         if out is None:
             shape = (batch.T, self.heads, self.d)
             out = (self._empty(shape, torch.bfloat16, stream), self._empty(shape, torch.bfloat16, stream))
@@ -168,6 +177,7 @@ class PagedKVCache:
         In a ``torch.cuda.graph`` capture scratch and outputs come from the graph's memory.  A capture made in
         another way has no memory of its own: give it `workspace` and `out`, keep them as long as the graph,
         and replay no two graphs that were given the same ones at the same time."""
+        self._check_device()
         self._rows(q, "q", batch)
         if out is None:
             out = (torch.empty_like(q, memory_format=torch.contiguous_format) if stream is None
@@ -177,6 +187,8 @@ class PagedKVCache:
             if not out.is_contiguous():
                 raise ValueError("out must be contiguous")
         lse = self._empty(q.shape[:2], torch.float32, stream) if return_lse else None
+        if workspace is None:
+            workspace = self._workspace(batch, q.shape[1], stream)
         _lib.moe_kv_attention(q, self.d ** -0.5 if scale is None else scale, self.struct, batch.struct, out, lse,
-                              self._workspace(batch, q.shape[1], stream) if workspace is None else workspace, stream)
+                              workspace, stream)
         return (out, lse) if return_lse else out
