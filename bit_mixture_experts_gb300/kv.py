@@ -189,6 +189,9 @@ class PagedKVCache:
         lse = self._empty(q.shape[:2], torch.float32, stream) if return_lse else None
         if workspace is None:
             workspace = self._workspace(batch, q.shape[1], stream)
+        elif torch.is_tensor(workspace) and (workspace.device != self.device or not workspace.is_contiguous()):
+            raise ValueError(f"workspace must be contiguous on {self.device}: it is on {workspace.device}, strides "
+                             f"{workspace.stride()}")
         _lib.moe_kv_attention(q, self.d ** -0.5 if scale is None else scale, self.struct, batch.struct, out, lse,
                               workspace, stream)
         return (out, lse) if return_lse else out

@@ -1,5 +1,5 @@
-"""What the paged cache refuses because a kernel could not reach it, without a GPU: pools in host memory
-and calls while another device is the current one."""
+"""What the paged cache refuses because a kernel could not reach it, without a GPU: pools in host memory,
+calls while another device is the current one, scratch that is no device memory or not what it says."""
 import types
 
 import pytest
@@ -44,11 +44,11 @@ def cache(launched, monkeypatch):
     return self
 
 
-def _calls(cache):
+def _calls(cache, **kw):
     batch = types.SimpleNamespace(T=3, struct=None)
     new = torch.zeros((3, 2, 64), dtype=torch.bfloat16)
     return {"append": lambda: cache.append(new, new, batch), "read": lambda: cache.read(batch),
-            "attention": lambda: cache.attention(new, batch)}
+            "attention": lambda: cache.attention(new, batch, **kw)}
 
 
 @pytest.mark.parametrize("call", ["append", "read", "attention"])
@@ -60,3 +60,12 @@ def test_another_device_is_current(cache, launched, monkeypatch, call):
         _calls(cache)[call]()
     assert launched == ["moe_kv_" + call]
 
+
+def test_scratch_of_the_wrong_kind_is_refused(cache, launched):
+    ws = torch.zeros(4096, dtype=torch.uint8)
+    _calls(cache, workspace=ws)["attention"]()
+    assert launched == ["moe_kv_attention"]
+    for bad in (ws[::2], ws.to("meta")):
+        with pytest.raises(ValueError, match="workspace"):
+            _calls(cache, workspace=bad)["attention"]()
+    assert launched == ["moe_kv_attention"]
