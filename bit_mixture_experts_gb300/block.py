@@ -88,8 +88,13 @@ def synthetic(shape, q_heads=16, kv_heads=2, d=128, fmt="bf16", num_pages=256, p
 def serve(block, prompts, chunk, steps):
     """Runs `prompts` (one bf16 [n, H] each) in chunks of up to `chunk` tokens per sequence, then `steps`
     steps of one token per sequence, the block's last output of each sequence being its next input.  Yields
-    (x, new tokens per sequence, kv_len, page table, output) of every step."""
+    (x, new tokens per sequence, kv_len, page table, output) of every step.  Every prompt has a token: its
+    output is what the next steps go on from."""
     import torch
+    if not prompts or not all(len(p) for p in prompts):
+        raise ValueError(f"prompts of at least one token are needed, got lengths {[len(p) for p in prompts]}")
+    if chunk < 1 or steps < 0:
+        raise ValueError(f"chunk {chunk} must be at least 1 and steps {steps} not negative")
     cache, dev = block.cache, prompts[0].device
     need = [-(-(len(p) + steps) // cache.page_size) for p in prompts]
     if sum(need) > cache.num_pages:
