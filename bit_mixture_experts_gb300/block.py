@@ -31,6 +31,9 @@ class DecoderBlockW4:
             raise ValueError(f"w_qkv must be {want}, w_o [{moe.H}, q_heads * {cache.d}], w_router "
                              f"[{moe.E}, {moe.H}]: got {tuple(w_qkv.shape)}, {tuple(w_o.shape)}, "
                              f"{tuple(w_router.shape)}")
+        if w_o.shape[1] % cache.d or self.q_heads % cache.heads:
+            raise ValueError(f"w_o's {w_o.shape[1]} columns must be q_heads * {cache.d}, q_heads a multiple of the cache's "
+                             f"{cache.heads} heads")
         self.w_qkv, self.w_o, self.w_router, self.moe, self.cache = w_qkv, w_o, w_router, moe, cache
 
     def project(self, x):

@@ -1,4 +1,4 @@
-"""What the decoder block's serving loop refuses before it does anything, without a GPU."""
+"""What the decoder block and its serving loop refuse before they do anything, without a GPU."""
 import types
 
 import pytest
@@ -27,3 +27,15 @@ def test_serve_refuses_what_it_cannot_serve(lens, chunk, steps):
     with pytest.raises(ValueError):
         next(_serve(lens, chunk, steps))
 
+
+@pytest.mark.parametrize("q_heads,kv_heads,extra", [(4, 2, 1), (3, 2, 0)])
+def test_block_refuses_projections_that_are_no_heads(q_heads, kv_heads, extra):
+    """w_o of no whole number of heads, and query heads that the KV heads cannot be shared out to."""
+    from bit_mixture_experts_gb300 import block
+    d, E = 64, 4
+    moe, cache = types.SimpleNamespace(H=H, E=E), types.SimpleNamespace(d=d, heads=kv_heads)
+    w = [torch.zeros(s) for s in (((q_heads + 2 * kv_heads) * d, H), (H, q_heads * d + extra), (E, H))]
+    with pytest.raises(ValueError, match="q_heads"):
+        block.DecoderBlockW4(*w, moe, cache)
+    ok = [torch.zeros(s) for s in ((8 * d, H), (H, 4 * d), (E, H))]
+    assert block.DecoderBlockW4(*ok, moe, types.SimpleNamespace(d=d, heads=2)).q_heads == 4
