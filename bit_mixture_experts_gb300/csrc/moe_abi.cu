@@ -3,6 +3,8 @@
 // kernels of moe_route.cu, moe_gemm_tc.cu, moe_gemm_gemv.cu, moe_decode.cu,
 // moe_combine.cu, moe_kv_cache.cu and moe_kv_attn.cu; nothing here touches
 // tensor data on the host.
+#include <float.h>
+
 #include <atomic>
 #include <mutex>
 
@@ -437,7 +439,8 @@ int moe_kv_attention(const uint16_t* q, int64_t q_token_stride, int64_t q_head_s
   if (rc) return rc;
   if (q_heads < 1 || q_heads % a.heads != 0 || q_heads / a.heads > 128) return MOE_ERR_SHAPE;
   if (!kv_strides_ok(q_token_stride, q_head_stride, a.T, q_heads)) return MOE_ERR_SHAPE;
-  if (!(scale > 0.0f) || scale > 3.0e38f) return MOE_ERR_SHAPE;
+  // scores are multiplied by scale * log2(e), which an infinite one would make NaN where they are 0
+  if (!(scale > 0.0f) || !(scale * 1.44269504088896341f <= FLT_MAX)) return MOE_ERR_SHAPE;
   if (a.T == 0) return MOE_OK;
   rc = check_ptrs(q, out);
   if (rc) return rc;

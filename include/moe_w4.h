@@ -528,7 +528,7 @@ int moe_kv_read(uint16_t* k, uint16_t* v, const moe_kv_cache_t* cache, const moe
  * token that sees no key gets out = 0 and lse = -infinity.  Positions after a
  * token's own, and rows of its pages past kv_len, do not enter its result
  * whatever they hold.  Scores, sums and the output are accumulated in FP32.
- * scale is finite and > 0.
+ * scale is > 0, and scale * log2(e) finite in FP32 (scale up to 2.358e38).
  * workspace: moe_kv_attention_workspace_size() bytes of scratch that no other
  * call uses at the same time; its contents need no preparation.  It grows with
  * B * table_width where an e4m3 cache is first expanded to bf16 (many query
