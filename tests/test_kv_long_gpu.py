@@ -33,3 +33,23 @@ def test_long_caches(new, n, g, d, fmt):
         torch.cuda.synchronize()
         assert _lib.moe_get_device_error() == 0
         R.check_rows(s, out, lse, R.spread(0, new, 2), scale=scale, chain=chain, what=f"scale {scale}")
+
+
+@pytest.mark.parametrize("power", [-90, 80])
+@pytest.mark.parametrize("new,g", [(1, 4), (4, 4), (8, 4), (60, 4)])
+def test_e4m3_values_of_extreme_scales_equal_bf16_ones(new, g, power):
+    """Over the scales that the comment of the form for few rows names, weights times scales lose no bits."""
+    import torch
+    from bit_mixture_experts_gb300 import PagedKVCache, _lib
+    s = K.Setup([new], [1500], heads=2, g=g, d=64, page=32, seed=power + 100)
+    _quantised(s, new)
+    s.cache.v_scale.mul_(2.0 ** power)
+    wide = [(x.float() * sc[..., None]).bfloat16() for x, sc in ((s.cache.k, s.cache.k_scale),
+                                                                 (s.cache.v, s.cache.v_scale))]
+    a = s.cache.attention(s.q, s.batch)
+    c2 = PagedKVCache.from_tensors(*wide)
+    b = c2.attention(s.q, c2.batch(*s.idx, s.T))
+    torch.cuda.synchronize()
+    assert _lib.moe_get_device_error() == 0
+    assert torch.isfinite(a).all() and a.any(-1).all()
+    assert torch.equal(a.view(torch.int16), b.view(torch.int16))
