@@ -30,14 +30,17 @@
 // unrounded values), the output to bf16.  All else is FP32.
 //
 // What bounds it, by calls in a row from a CUDA graph (16 query heads over 2 KV
-// heads of 128): 4096 tokens over 32K cached ones take 0.79 ms, 1.51 PFLOP/s, 0.78
-// of the rate of a large plain product; the tensor pipe is active 62 % of the
-// time and waits for the softmax threads, whose tile takes them longer (the
-// loads from TMEM, 128 exponentials and the conversions of a row, one after
-// another in one thread) than its two products.  Six chunks of 440 to 1777
-// tokens over an e4m3 cache 0.32 ms.  A 512-token prompt takes 15 us and one
-// token over 4K keys 11 us, nearly all of it a chain of latencies that no size
-// enters: launch, plan, first page, first keys, scores, output, merge.
+// heads of 128): 4096 tokens over 32K cached ones take 0.80 ms (0.82 to 0.84 in
+// calls that go on for longer), 1.46 PFLOP/s, 0.75 of the rate of a large plain
+// product; the tensor pipe is active 63 % of the time and waits for the softmax
+// threads, whose tile takes them longer (the loads from TMEM, 128 exponentials
+// and the conversions of a row, one after another in one thread) than its two
+// products.  Six chunks of 440 to 1777 tokens over an e4m3 cache 0.32 ms.  A
+// 512-token prompt takes 15 us and one token over 4K keys 11 us, nearly all of
+// it a chain of latencies that no size enters: launch, plan, first page, first
+// keys, scores, output, merge.  With an e4m3 cache 512 threads leave 128
+// registers each, and the compiler spills a few (206 bytes stored at D = 128,
+// 142 at D = 64); the bf16 kernels spill none.
 #include <cuda.h>
 #include <string.h>
 
@@ -883,7 +886,8 @@ cudaError_t launch_kv_expand(const kv::Args& a, uint16_t* k, uint16_t* v, int ti
 // attention of a pair of query tiles expands its keys and values on chip, every pair the same ones: from two
 // pairs per sequence on, on average, one pass over the cache before it costs less (six chunks of 440 to 1777
 // tokens over 1K to 10K: 457 us on chip, 335 us expanded first).  What the sequences' tables have room for is
-// reserved, up to 8 GiB.
+// reserved, up to 8 GiB.  Going by the average has a price where one long chunk comes with single tokens over
+// long caches, which are expanded too (4096 tokens and 15 single ones over 32K: 336 us, in two calls 190).
 size_t kv_expanded_bytes(const kv::Args& a, bool q8, int q_heads) {
   if (!q8 || a.B > 65535 || static_cast<long long>(a.T) * (q_heads / a.heads) < 4ll * TILE * a.B) return 0;
   const long long rows = static_cast<long long>(a.B) * ((a.most + TILE - 1) / TILE) * TILE * a.heads;

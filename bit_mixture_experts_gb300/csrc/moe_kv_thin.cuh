@@ -8,8 +8,10 @@
 // they take the other 16 rows), each warp with its own running maximum, sum and
 // output, joined once at the end of the item's run.  Keys and values come
 // straight from where the copies land: e4m3 codes are expanded in registers,
-// their scales applied to the scores and to the weights (exact: powers of two),
-// so the result is that of a bf16 cache with the same values, bit for bit.
+// their scales applied to the scores and to the weights (powers of two), so the
+// result is that of a bf16 cache with the same values, bit for bit while the
+// value scales lie between 2^-90 and 2^90: weights are up to 2^8 and then
+// rounded to bf16 times the scale, which has to stay a normal number.
 //
 // Two shapes of the products.  Up to 8 rows (NARROW): S^T = K Q^T and
 // O^T = V^T P^T, the queries as the 8-wide operand; a row's scores lie in the

@@ -527,12 +527,25 @@ int moe_kv_read(uint16_t* k, uint16_t* v, const moe_kv_cache_t* cache, const moe
  * out bf16 [T, q_heads, d], lse float32 [T, q_heads] or NULL, both dense.  A
  * token that sees no key gets out = 0 and lse = -infinity.  Positions after a
  * token's own, and rows of its pages past kv_len, do not enter its result
- * whatever they hold.  Scores, sums and the output are accumulated in FP32.
+ * whatever they hold.  An element of a visible value row that is not finite
+ * goes to its own column; an infinity under a weight below 2^-126 may come out
+ * as NaN.  A token whose visible scores are all -infinity is treated as one
+ * that sees no key.
+ * Roundings: scores, sums, maxima and the output's accumulation are FP32; a
+ * weight is rounded to bf16 for its product with the value (MOE_KV_E4M3 with at
+ * most 32 query rows per sequence and KV head: weight times value scale is),
+ * while the sum that the output is divided by is of the unrounded weights; the
+ * output is rounded to bf16 once.  Weights are taken relative to a running
+ * maximum that may be short of the last one, so they are up to 2^8 and values
+ * of more than 2^90 may overflow the sums; with MOE_KV_E4M3 value scales under
+ * 2^-90 lose accuracy (bf16 has no exponent for their product with a weight).
  * scale is > 0, and scale * log2(e) finite in FP32 (scale up to 2.358e38).
  * workspace: moe_kv_attention_workspace_size() bytes of scratch that no other
  * call uses at the same time; its contents need no preparation.  It grows with
- * B * table_width where an e4m3 cache is first expanded to bf16 (many query
- * rows per sequence; at most 8 GiB), and is otherwise fixed (some 40 MB).
+ * B * table_width where an e4m3 cache is first expanded to bf16 (T * q_heads /
+ * heads >= 512 * B; at most 8 GiB), and is otherwise fixed (some 40 MB).  The
+ * expansion takes in every sequence with new tokens: long chunks and single
+ * tokens over long e4m3 caches are faster in two calls.
  * One to three launches.
  */
 size_t moe_kv_attention_workspace_size(const moe_kv_cache_t* cache, const moe_kv_batch_t* batch, int q_heads);
