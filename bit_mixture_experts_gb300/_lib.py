@@ -16,18 +16,21 @@ LIB_PATH = os.path.join(PKG, "libmoe_w4.so")
 
 MOE_OK = 0
 ERRORS = {-1: "MOE_ERR_NULL", -2: "MOE_ERR_ALIGN", -3: "MOE_ERR_SHAPE", -4: "MOE_ERR_WORKSPACE",
-          -5: "MOE_ERR_CUDA", -6: "MOE_ERR_DEVICE", -7: "MOE_ERR_MODE"}
+          -5: "MOE_ERR_CUDA", -6: "MOE_ERR_DEVICE", -7: "MOE_ERR_MODE", -8: "MOE_ERR_OVERLAP"}
 DEVICE_ERRORS = {0: "ok", 1: "MOE_DEV_BAD_BLOCK", 2: "MOE_DEV_BAD_INDEX", 3: "MOE_DEV_TIMEOUT", 4: "MOE_DEV_BAD_WORKSPACE"}
 
 GATE_UP, DOWN = 0, 1
 IMPL_AUTO, IMPL_TC, IMPL_GEMV, IMPL_TC2, IMPL_TC_BF16 = 0, 2, 3, 4, 5
 KV_BF16, KV_E4M3 = 0, 1
+SCORES = {"softmax": 0, "sigmoid": 1}
+GROUP_SCORES = {"max": 0, "top2": 1}
 IMPLS = {"auto": IMPL_AUTO, "tc": IMPL_TC, "gemv": IMPL_GEMV, "tc2": IMPL_TC2, "tc_bf16": IMPL_TC_BF16}
 
 # Exported symbols of include/moe_w4.h (checked by the CPU tests).
 SYMBOLS = ["moe_version", "moe_launch_count", "moe_route_noalloc", "moe_route_x", "moe_router", "moe_rms_norm", "moe_norm_router",
            "moe_down_combine", "moe_down_combine_workspace_size", "moe_expert_ffn_w4", "moe_block_map_capacity", "moe_route_workspace_size", "moe_route",
            "moe_repacked_bytes", "moe_repack_w4", "moe_expanded_bytes", "moe_expand_w4", "moe_expert_gemm_w4", "moe_combine", "moe_decode_workspace_size",
+           "moe_gate", "moe_route_gated", "moe_residual_norm", "moe_combine_residual_norm", "moe_layer_forward_gated",
            "moe_kv_append", "moe_kv_read", "moe_kv_attention", "moe_kv_attention_workspace_size",
            "moe_layer_forward", "moe_layer_forward_host", "moe_get_device_error", "moe_set_wait_limit_ns",
            "moe_trace_words", "moe_trace_reset", "moe_trace_read"]
@@ -51,6 +54,19 @@ class Buffers(ctypes.Structure):
                 ("inv_perm", _vp), ("block_map", _vp), ("num_blocks", _vp), ("h", _vp), ("y", _vp),
                 ("workspace", _vp), ("workspace_bytes", _sz), ("decode_ws", _vp), ("decode_ws_bytes", _sz),
                 ("combine_ws", _vp), ("combine_ws_bytes", _sz)]
+
+
+class Gate(ctypes.Structure):
+    _fields_ = [("bias", _vp), ("score", ctypes.c_int32), ("groups", ctypes.c_int32), ("top_groups", ctypes.c_int32),
+                ("group_score", ctypes.c_int32), ("renorm", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class Residual(ctypes.Structure):
+    _fields_ = [("x", _vp), ("x_stride", ctypes.c_int64), ("r", _vp), ("r_stride", ctypes.c_int64), ("n", _vp),
+                ("n_stride", ctypes.c_int64), ("w_pre", _vp), ("w_post", _vp), ("gate", _vp),
+                ("gate_token_stride", ctypes.c_int64), ("gate_per_channel", ctypes.c_int32), ("post", ctypes.c_int32),
+                ("stream_f32", ctypes.c_int32), ("param_f32", ctypes.c_int32), ("gate_f32", ctypes.c_int32),
+                ("offset", ctypes.c_float), ("scale", ctypes.c_float), ("eps", ctypes.c_float)]
 
 
 class KVCache(ctypes.Structure):
@@ -90,6 +106,12 @@ _SIGS = {
     "moe_decode_workspace_size": ([_i, _i], _sz),
     "moe_layer_forward": ([_vp, _vp, _vp] + [_i] * 7 + [ctypes.POINTER(Weights), ctypes.POINTER(Buffers), _vp], _i),
     "moe_layer_forward_host": ([_vp] * 6 + [_i] * 7 + [ctypes.POINTER(Weights), ctypes.POINTER(Buffers), _vp], _i),
+    "moe_gate": ([_vp, _i, _i, _i, ctypes.POINTER(Gate), _vp, _vp, _vp], _i),
+    "moe_route_gated": ([_vp, _i, _i, _i, ctypes.POINTER(Gate), _i] + [_vp] * 9 + [_sz, _vp], _i),
+    "moe_residual_norm": ([_vp, _i64, _i, _i, ctypes.POINTER(Residual), _vp], _i),
+    "moe_combine_residual_norm": ([_vp, _vp, _vp, _i, _i, _i, ctypes.POINTER(Residual), _vp], _i),
+    "moe_layer_forward_gated": ([_vp, _vp, ctypes.POINTER(Gate), _vp, ctypes.POINTER(Residual)] + [_i] * 7
+                                + [ctypes.POINTER(Weights), ctypes.POINTER(Buffers), _vp], _i),
     "moe_kv_append": ([_vp, _i64, _i64, _vp, _i64, _i64] + _kv + [_vp], _i),
     "moe_kv_read": ([_vp, _vp] + _kv + [_vp], _i),
     "moe_kv_attention": ([_vp, _i64, _i64, _i, ctypes.c_float] + _kv + [_vp, _vp, _vp, _sz, _vp], _i),
@@ -277,6 +299,39 @@ def moe_layer_forward_host(x_host, logits_host, out_host, x_dev, logits_dev, out
     _call("moe_layer_forward_host", _ptr(x_host), _ptr(logits_host), _ptr(out_host), _ptr(x_dev), _ptr(logits_dev),
           _ptr(out_dev), T, H, F, E, k, block_n, impl, ctypes.byref(weights), ctypes.byref(buffers),
           _stream(stream))
+
+
+def moe_gate(logits, k, gate: Gate, topk_ids, topk_w, stream=None):
+    """Router logits float32 [T, E] to k experts a token and their weights, by a gate."""
+    T, E = logits.shape
+    _call("moe_gate", logits.data_ptr(), T, E, k, gate, topk_ids.data_ptr(), topk_w.data_ptr(), _stream(stream))
+
+
+def moe_route_gated(logits, T, E, k, gate: Gate, block_n, topk_ids, topk_w, counts, offsets, perm, inv_perm, block_map,
+                    num_blocks, workspace, stream=None):
+    """moe_route with the experts chosen by a gate (logits None: topk_ids and topk_w hold the choice)."""
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _call("moe_route_gated", _ptr(logits), T, E, k, gate, block_n, _ptr(topk_ids), _ptr(topk_w), _ptr(counts),
+          _ptr(offsets), _ptr(perm), _ptr(inv_perm), _ptr(block_map), _ptr(num_blocks), _ptr(workspace), ws_bytes,
+          _stream(stream))
+
+
+def moe_residual_norm(y, y_stride, T, H, residual: Residual, stream=None):
+    """A block's residual addition between the norm of its output and the next block's norm."""
+    _call("moe_residual_norm", _ptr(y), y_stride, T, H, residual, _stream(stream))
+
+
+def moe_combine_residual_norm(y, inv_perm, topk_w, T, H, k, residual: Residual, stream=None):
+    """The same where y is the weighted sum of each token's expert rows (bf16 [T k + T, H])."""
+    _call("moe_combine_residual_norm", _ptr(y), _ptr(inv_perm), _ptr(topk_w), T, H, k, residual, _stream(stream))
+
+
+def moe_layer_forward_gated(x, logits, gate, out, residual, T, H, F, E, k, block_n, impl, weights: Weights,
+                            buffers: Buffers, stream=None):
+    """The layer with the experts chosen by a gate (logits None: the buffers hold the choice) and, with a Residual
+    for None, what follows the block in place of out."""
+    _call("moe_layer_forward_gated", _ptr(x), _ptr(logits), gate, _ptr(out), residual, T, H, F, E, k, block_n, impl,
+          weights, buffers, _stream(stream))
 
 
 def moe_kv_append(k, v, cache: KVCache, batch: KVBatch, stream=None):

@@ -1,8 +1,8 @@
 // extern "C" entry points of libmoe_w4.so: argument checks, the device error
 // word, and the launch sequence of the layer.  Every compute step runs in the
 // kernels of moe_route.cu, moe_gemm_tc.cu, moe_gemm_gemv.cu, moe_decode.cu,
-// moe_combine.cu, moe_kv_cache.cu and moe_kv_attn.cu; nothing here touches
-// tensor data on the host.
+// moe_combine.cu, moe_gate.cu, moe_residual.cu, moe_kv_cache.cu and
+// moe_kv_attn.cu; nothing here touches tensor data on the host.
 #include <float.h>
 
 #include <atomic>
@@ -10,6 +10,7 @@
 
 #include "moe_common.cuh"
 #include "moe_kv_dev.cuh"
+#include "moe_residual.cuh"
 #ifdef MOE_TRACE
 #include "moe_tc_dev.cuh"  // the trace words' layout (TRACE_ERR_INTS, TRACE_CTAS, trace_wait)
 #endif
@@ -111,8 +112,106 @@ cudaError_t launch_kv_read(const kv::Args& a, bool q8, uint16_t* k, uint16_t* v,
 cudaError_t launch_kv_attention(const kv::Args& a, bool q8, const uint16_t* q, long long q_token, long long q_head,
                                 int q_heads, float scale, uint16_t* out, float* lse, void* ws, cudaStream_t s);
 size_t kv_attention_workspace_bytes(const kv::Args& a, bool q8, int q_heads);
+cudaError_t launch_gate(const float* logits, int T, const moe_gate_t* p, int E, int k, int32_t* ids, float* w,
+                        cudaStream_t s);
+int residual_max_h();
+cudaError_t launch_residual(const ResidualArgs& p, bool combine, bool x32, cudaStream_t s);
 
 namespace {
+
+int check_gate(const moe_gate_t* g, int E, int k) {
+  if (!g) return MOE_ERR_NULL;
+  if ((g->score != MOE_SCORE_SOFTMAX && g->score != MOE_SCORE_SIGMOID) ||
+      (g->group_score != MOE_GROUP_MAX && g->group_score != MOE_GROUP_TOP2))
+    return MOE_ERR_MODE;
+  if (g->groups < 1 || g->groups > 32 || E % g->groups != 0) return MOE_ERR_SHAPE;
+  if (g->top_groups < 1 || g->top_groups > g->groups || g->top_groups * (E / g->groups) < k) return MOE_ERR_SHAPE;
+  if (!(g->scale >= -FLT_MAX && g->scale <= FLT_MAX)) return MOE_ERR_SHAPE;
+  if (reinterpret_cast<uintptr_t>(g->bias) & 3u) return MOE_ERR_ALIGN;
+  return MOE_OK;
+}
+
+// Rows of a tensor in bytes: first row, distance of rows, length and number of rows.
+struct Rows {
+  uintptr_t at;
+  unsigned long long stride, len;
+  long long n;
+  uintptr_t end() const { return at + (n - 1) * stride + len; }
+};
+
+Rows rows_of(const void* p, long long stride, long long cols, int size, long long n) {
+  return {reinterpret_cast<uintptr_t>(p), n > 1 ? static_cast<unsigned long long>(stride) * size : 0ull,
+          static_cast<unsigned long long>(cols) * size, p ? n : 0};
+}
+
+// Whether two sets of rows have a byte in common.
+bool overlap(const Rows& a, const Rows& b) {
+  if (a.n == 0 || b.n == 0 || a.end() <= b.at || b.end() <= a.at) return false;
+  if (a.stride != b.stride || a.stride == 0) return true;
+  // columns of one wider tensor
+  const unsigned long long d = b.at >= a.at ? (b.at - a.at) % a.stride : (a.stride - (a.at - b.at) % a.stride) % a.stride;
+  return d < a.len || d + b.len > a.stride;
+}
+
+bool same(const Rows& a, const Rows& b) { return a.at == b.at && a.stride == b.stride && a.len == b.len && a.n == b.n; }
+
+bool aligned(const void* p, int size) { return reinterpret_cast<uintptr_t>(p) % size == 0; }
+
+// Checks a residual addition of T rows of H channels and fills the kernels' description of it; y: the
+// block's output, `y_rows` rows of it (each read by its own row of x, or all by any).
+int residual_args(const uint16_t* y, long long y_stride, long long y_rows, bool combine, int T, int H,
+                  const moe_residual_t* p, ResidualArgs* a) {
+  if (!p) return MOE_ERR_NULL;
+  if (T < 0 || T > (1 << 20) || H < 1 || H > residual_max_h()) return MOE_ERR_SHAPE;
+  if (!(p->eps >= 0.0f) || !(p->eps <= FLT_MAX) || !(p->scale >= -FLT_MAX && p->scale <= FLT_MAX) ||
+      !(p->offset >= -FLT_MAX && p->offset <= FLT_MAX))
+    return MOE_ERR_SHAPE;
+  const long long most = 1ll << 40;
+  for (long long s : {static_cast<long long>(p->x_stride), y_stride, static_cast<long long>(p->gate_token_stride)})
+    if (s < 0 || s >= most) return MOE_ERR_SHAPE;
+  if (T > 1 && ((p->r && (p->r_stride < H || p->r_stride >= most)) || (p->n && (p->n_stride < H || p->n_stride >= most))))
+    return MOE_ERR_SHAPE;
+  if (T == 0) return MOE_OK;
+  if (!p->x || (!p->r && !p->n)) return MOE_ERR_NULL;
+  const int xs = p->stream_f32 ? 4 : 2, ps = p->param_f32 ? 4 : 2, gs = p->gate_f32 ? 4 : 2;
+  if (!aligned(p->x, xs) || !aligned(p->r, xs) || !aligned(p->n, 2) || !aligned(y, 2) || !aligned(p->w_pre, ps) ||
+      !aligned(p->w_post, ps) || !aligned(p->gate, gs))
+    return MOE_ERR_ALIGN;
+  const Rows r = rows_of(p->r, p->r_stride, H, xs, T), n = rows_of(p->n, p->n_stride, H, 2, T);
+  const Rows in[5] = {rows_of(p->x, p->x_stride, H, xs, T), rows_of(y, y_stride, H, 2, y_rows),
+                      rows_of(p->gate, p->gate_token_stride, p->gate_per_channel ? H : 1, gs, T),
+                      rows_of(p->w_pre, 0, H, ps, 1), rows_of(p->w_post, 0, H, ps, 1)};
+  if (overlap(r, n)) return MOE_ERR_OVERLAP;
+  for (const Rows& i : in)
+    for (const Rows& o : {r, n})
+      // an output in the place of an input: each value is read before it is written, by the same thread
+      if (overlap(i, o) && !(same(i, o) && (!combine || &i != &in[1]))) return MOE_ERR_OVERLAP;
+  a->y = y;
+  a->y_stride = y_stride;
+  a->inv_perm = nullptr;
+  a->topk_w = nullptr;
+  a->k = 0;
+  a->T = T;
+  a->H = H;
+  a->x = p->x;
+  a->x_stride = p->x_stride;
+  a->r = p->r;
+  a->r_stride = p->r_stride;
+  a->n = p->n;
+  a->n_stride = p->n_stride;
+  a->w_pre = p->w_pre;
+  a->w_post = p->w_post;
+  a->gate = y ? p->gate : nullptr;
+  a->gate_token = p->gate_token_stride;
+  a->gate_channel = p->gate_per_channel != 0;
+  a->offset = p->offset;
+  a->scale = p->scale;
+  a->eps = p->eps;
+  a->post = y && p->post;
+  a->param_f32 = p->param_f32 != 0;
+  a->gate_f32 = p->gate_f32 != 0;
+  return MOE_OK;
+}
 
 // Checks a cache and a batch and fills the kernels' description of them.  Sizes before pointers, as
 // elsewhere.  T = 0 passes (the entry points then return before they look at the dense tensors).
@@ -235,6 +334,61 @@ int moe_router(const uint16_t* x, const uint16_t* w_router, int T, int H, int E,
                                    reinterpret_cast<cudaStream_t>(stream)));
 }
 
+int moe_gate(const float* logits, int T, int E, int k, const moe_gate_t* gate, int32_t* topk_ids, float* topk_w,
+             moe_stream_t stream) {
+  int rc = check_route_shape(T == 0 ? 1 : T, E, k, 1);
+  if (rc || (rc = check_gate(gate, E, k))) return rc;
+  if (T == 0) return MOE_OK;
+  rc = check_ptrs(logits, topk_ids, topk_w);
+  if (rc) return rc;
+  return cuda_status(launch_gate(logits, T, gate, E, k, topk_ids, topk_w, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int moe_route_gated(const float* logits, int T, int E, int k, const moe_gate_t* gate, int block_n, int32_t* topk_ids,
+                    float* topk_w, int32_t* counts, int32_t* offsets, int32_t* perm, int32_t* inv_perm,
+                    int32_t* block_map, int32_t* num_blocks, void* workspace, size_t workspace_bytes,
+                    moe_stream_t stream) {
+  int rc = check_route_shape(T, E, k, block_n);
+  if (rc || (logits && (rc = check_gate(gate, E, k)))) return rc;
+  rc = check_ptrs(topk_ids, topk_w, counts, offsets, perm, inv_perm, block_map, num_blocks);
+  if (rc) return rc;
+  if (!aligned16(logits)) return MOE_ERR_ALIGN;
+  const size_t need = route_workspace_bytes(T, E, k);
+  if (need > 0) {
+    if (workspace_bytes < need) return MOE_ERR_WORKSPACE;
+    rc = check_ptrs(workspace);
+    if (rc) return rc;
+  }
+  if (!device_error_ptr()) return MOE_ERR_CUDA;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (logits && (rc = cuda_status(launch_gate(logits, T, gate, E, k, topk_ids, topk_w, s)))) return rc;
+  return cuda_status(launch_route(logits, T, E, k, block_n, topk_ids, topk_w, counts, offsets, perm, inv_perm,
+                                  block_map, num_blocks, workspace, workspace_bytes, s, 1));
+}
+
+int moe_residual_norm(const uint16_t* y, int64_t y_stride, int T, int H, const moe_residual_t* p, moe_stream_t stream) {
+  ResidualArgs a;
+  int rc = residual_args(y, y ? y_stride : 0, T, false, T, H, p, &a);
+  if (rc || T == 0) return rc;
+  if (!(a.err = device_error_ptr())) return MOE_ERR_CUDA;
+  return cuda_status(launch_residual(a, false, p->stream_f32 != 0, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int moe_combine_residual_norm(const uint16_t* y, const int32_t* inv_perm, const float* topk_w, int T, int H, int k,
+                              const moe_residual_t* p, moe_stream_t stream) {
+  if (k < 1 || k > 32) return MOE_ERR_SHAPE;
+  ResidualArgs a;
+  int rc = residual_args(y, H, (k + 1ll) * T, true, T, H, p, &a);
+  if (rc || T == 0) return rc;
+  rc = check_ptrs(y, inv_perm, topk_w);
+  if (rc) return rc;
+  a.inv_perm = inv_perm;
+  a.topk_w = topk_w;
+  a.k = k;
+  if (!(a.err = device_error_ptr())) return MOE_ERR_CUDA;
+  return cuda_status(launch_residual(a, true, p->stream_f32 != 0, reinterpret_cast<cudaStream_t>(stream)));
+}
+
 int moe_route_x(const uint16_t* x, const uint16_t* w_router, int T, int H, int E, int k, int block_n, float* logits,
                 int32_t* topk_ids, float* topk_w, int32_t* counts, int32_t* offsets, int32_t* perm,
                 int32_t* inv_perm, int32_t* block_map, int32_t* num_blocks, void* workspace,
@@ -350,49 +504,86 @@ size_t moe_decode_workspace_size(int T, int H) {
   return decode_workspace_bytes(T, H);
 }
 
-int moe_layer_forward(const uint16_t* x, const float* logits, uint16_t* out, int T, int H, int F, int E, int k,
-                      int block_n, int impl, const moe_weights_t* w, const moe_buffers_t* b, moe_stream_t stream) {
-  if (!w || !b) return MOE_ERR_NULL;
+// The layer.  chosen: the experts are chosen by `gate`, or without logits have been and stand in the buffers;
+// else moe_route's way.  residual: what follows the combine's sum (null: it is written to out).
+static int layer_forward(const uint16_t* x, const float* logits, bool chosen, const moe_gate_t* gate, uint16_t* out,
+                         const moe_residual_t* residual, int T, int H, int F, int E, int k, int block_n, int impl,
+                         const moe_weights_t* w, const moe_buffers_t* b, moe_stream_t stream) {
+  auto combine = [&]() -> int {
+    if (residual) return moe_combine_residual_norm(b->y, b->inv_perm, b->topk_w, T, H, k, residual, stream);
+    return moe_combine(b->y, b->inv_perm, b->topk_w, out, T, H, k, stream);
+  };
   const bool gemv = impl == MOE_IMPL_GEMV || (impl == MOE_IMPL_AUTO && block_n <= gemv_max_rows());
   if (gemv && b->decode_ws && T <= decode_max_tokens() && k <= 32) {
     // the fused decode kernel: routing, both GEMVs and the combine in one launch
     int rc = check_shape(T, H, F, E, k, block_n);
     if (rc) return rc;
     if (block_n > gemv_max_rows() || H % 128 != 0 || F % 128 != 0) return MOE_ERR_SHAPE;
-    rc = check_ptrs(x, logits, out, w->w13, w->w2, b->topk_ids, b->topk_w, b->counts, b->offsets, b->perm,
-                    b->inv_perm, b->block_map, b->num_blocks, b->h, b->y, b->decode_ws);
+    rc = check_ptrs(x, w->w13, w->w2, b->topk_ids, b->topk_w, b->counts, b->offsets, b->perm, b->inv_perm,
+                    b->block_map, b->num_blocks, b->h, b->y, b->decode_ws);
+    if (rc) return rc;
+    // (in the place of what the call does without: x)
+    rc = check_ptrs(chosen && !logits ? static_cast<const void*>(x) : logits,
+                    residual ? static_cast<const void*>(x) : out);
     if (rc) return rc;
     if (b->decode_ws_bytes < decode_workspace_bytes(T, H)) return MOE_ERR_WORKSPACE;
     if (!device_error_ptr()) return MOE_ERR_CUDA;
-    return cuda_status(launch_decode(x, logits, w->w13, w->w2, T, H, F, E, k, block_n, b->topk_ids, b->topk_w,
-                                     b->counts, b->offsets, b->perm, b->inv_perm, b->block_map, b->num_blocks, b->h,
-                                     b->y, out, b->decode_ws, wait_limit_ns(), num_sms(),
-                                     reinterpret_cast<cudaStream_t>(stream)));
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (chosen && logits && (rc = cuda_status(launch_gate(logits, T, gate, E, k, b->topk_ids, b->topk_w, s)))) return rc;
+    rc = cuda_status(launch_decode(x, chosen ? nullptr : logits, w->w13, w->w2, T, H, F, E, k, block_n, b->topk_ids,
+                                   b->topk_w, b->counts, b->offsets, b->perm, b->inv_perm, b->block_map, b->num_blocks,
+                                   b->h, b->y, residual ? nullptr : out, b->decode_ws, wait_limit_ns(), num_sms(), s));
+    return rc || !residual ? rc : combine();
   }
-  int rc = moe_route(logits, T, E, k, block_n, b->topk_ids, b->topk_w, b->counts, b->offsets, b->perm, b->inv_perm,
-                     b->block_map, b->num_blocks, b->workspace, b->workspace_bytes, stream);
+  int rc = chosen ? moe_route_gated(logits, T, E, k, gate, block_n, b->topk_ids, b->topk_w, b->counts, b->offsets,
+                                    b->perm, b->inv_perm, b->block_map, b->num_blocks, b->workspace, b->workspace_bytes,
+                                    stream)
+                  : moe_route(logits, T, E, k, block_n, b->topk_ids, b->topk_w, b->counts, b->offsets, b->perm,
+                              b->inv_perm, b->block_map, b->num_blocks, b->workspace, b->workspace_bytes, stream);
   if (rc) return rc;
   const int resolved = impl == MOE_IMPL_AUTO ? (block_n <= gemv_max_rows() ? MOE_IMPL_GEMV : MOE_IMPL_TC) : impl;
-  if (resolved == MOE_IMPL_TC && !b->combine_ws && block_n <= 64 && H % 128 == 0 && F % 256 == 0) {
+  const bool in_epilogue = b->combine_ws && !residual;
+  if (resolved == MOE_IMPL_TC && !in_epilogue && block_n <= 64 && H % 128 == 0 && F % 256 == 0) {
     // tiles of at most 64 rows: both projections of a tile in one launch, h kept in shared memory
     // (the same bits of y; measured faster than the two GEMMs at these tile heights)
     rc = moe_expert_ffn_w4(x, T, H, F, E, k, w->w13, w->w2, b->perm, b->block_map, b->num_blocks, block_n, b->y,
                            stream);
-    if (rc) return rc;
-    return moe_combine(b->y, b->inv_perm, b->topk_w, out, T, H, k, stream);
+    return rc ? rc : combine();
   }
   rc = moe_expert_gemm_w4(MOE_GATE_UP_SWIGLU, impl, x, T, H, F, E, k, w->w13, b->perm, b->topk_w, b->block_map,
                           b->num_blocks, block_n, b->h, stream);
   if (rc) return rc;
-  if (resolved == MOE_IMPL_TC && b->combine_ws) {
+  if (resolved == MOE_IMPL_TC && in_epilogue) {
     // the down GEMM with the combine in its epilogue (one launch fewer, y read back from L2 at once)
     return moe_down_combine(b->h, T, H, F, E, k, w->w2, b->perm, b->inv_perm, b->topk_w, b->block_map,
                             b->num_blocks, block_n, b->y, out, b->combine_ws, b->combine_ws_bytes, stream);
   }
   rc = moe_expert_gemm_w4(MOE_DOWN, impl, b->h, T, H, F, E, k, w->w2, b->perm, b->topk_w, b->block_map,
                           b->num_blocks, block_n, b->y, stream);
-  if (rc) return rc;
-  return moe_combine(b->y, b->inv_perm, b->topk_w, out, T, H, k, stream);
+  return rc ? rc : combine();
+}
+
+int moe_layer_forward(const uint16_t* x, const float* logits, uint16_t* out, int T, int H, int F, int E, int k,
+                      int block_n, int impl, const moe_weights_t* w, const moe_buffers_t* b, moe_stream_t stream) {
+  if (!w || !b) return MOE_ERR_NULL;
+  return layer_forward(x, logits, false, nullptr, out, nullptr, T, H, F, E, k, block_n, impl, w, b, stream);
+}
+
+int moe_layer_forward_gated(const uint16_t* x, const float* logits, const moe_gate_t* gate, uint16_t* out,
+                            const moe_residual_t* residual, int T, int H, int F, int E, int k, int block_n, int impl,
+                            const moe_weights_t* w, const moe_buffers_t* b, moe_stream_t stream) {
+  if (!w || !b) return MOE_ERR_NULL;
+  // all of it is checked before anything is enqueued
+  int rc = check_shape(T, H, F, E, k, block_n);
+  if (rc || (logits && (rc = check_gate(gate, E, k)))) return rc;
+  if (!aligned16(logits)) return MOE_ERR_ALIGN;
+  if (residual) {
+    ResidualArgs a;
+    if ((rc = check_ptrs(b->y)) || (rc = residual_args(b->y, H, (k + 1ll) * T, true, T, H, residual, &a))) return rc;
+  } else if ((rc = check_ptrs(out))) {
+    return rc;
+  }
+  return layer_forward(x, logits, true, gate, out, residual, T, H, F, E, k, block_n, impl, w, b, stream);
 }
 
 int moe_kv_append(const uint16_t* k, int64_t k_token_stride, int64_t k_head_stride, const uint16_t* v,

@@ -15,6 +15,8 @@
 //   R  routing, recomputed by every CTA in shared memory from the logits with
 //      the same device code as moe_route (top-k and weights, counts, offsets,
 //      stable permutation, block map); CTA 0 also writes moe_route's outputs.
+//      Without logits the experts and weights are those that topk_ids and topk_w
+//      hold already.
 //   G  gate/up work items (tile, 16 features), exactly as the GEMV kernel
 //      (the first down item's weights are already streaming during the last).
 //   -  grid barrier: every h value is written.
@@ -22,7 +24,8 @@
 //   -  grid barrier: every y value is written.
 //   C  the gather-combine, one warp per (token, 32 channels):
 //      out = bf16(sum_j topk_w[t, j] * y[row(t, j)] + y[shared row]), FP32 in
-//      the same fixed order as moe_combine.
+//      the same fixed order as moe_combine.  Without `out` it is left to the
+//      caller (moe_combine_residual_norm), and the second barrier with it.
 //   The last CTA to finish resets the barrier counters for the next call.
 // The grid barriers are counters in global memory (one fence and one atomic
 // per CTA); they rely on every CTA being resident, which the cooperative
@@ -212,9 +215,18 @@ __global__ void __launch_bounds__(GV_THREADS, GV_CTAS_PER_SM) decode_kernel(cons
 
   // ---------------------------------------------------------------- R: routing
   if (warp < T) {
-    int id;
-    float w;
-    route_dev::warp_topk_any(p.logits + static_cast<size_t>(warp) * E, E, k, lane, &id, &w);
+    int id = 0;
+    float w = 0.f;
+    if (p.logits) {
+      route_dev::warp_topk_any(p.logits + static_cast<size_t>(warp) * E, E, k, lane, &id, &w);
+    } else if (lane < k) {  // chosen already
+      id = __ldg(p.topk_ids + warp * k + lane);
+      w = __ldg(p.topk_w + warp * k + lane);
+      if (id < 0 || id >= E) {
+        set_device_error(p.err, MOE_DEV_BAD_INDEX);
+        id = 0;
+      }
+    }
     if (lane < k) {
       s_ids[warp * k + lane] = id;
       s_w[warp * k + lane] = w;
@@ -246,8 +258,10 @@ __global__ void __launch_bounds__(GV_THREADS, GV_CTAS_PER_SM) decode_kernel(cons
   if (blockIdx.x == 0) {
     // the outputs of moe_route for the same logits
     for (int a = tid; a < A; a += GV_THREADS) {
-      p.topk_ids[a] = s_ids[a];
-      p.topk_w[a] = s_w[a];
+      if (p.logits) {
+        p.topk_ids[a] = s_ids[a];
+        p.topk_w[a] = s_w[a];
+      }
       p.inv_perm[a] = s_inv[a];
       p.perm[s_inv[a]] = a;
     }
@@ -369,10 +383,10 @@ __global__ void __launch_bounds__(GV_THREADS, GV_CTAS_PER_SM) decode_kernel(cons
   }
   if (myD == 0) grid_barrier(ws_bar);  // CTAs without down items still take part in the first barrier
   ptx::cp_async_wait_all();
-  grid_barrier(ws_bar + 1);  // all of y is written
+  if (p.out) grid_barrier(ws_bar + 1);  // all of y is written
 
   // ---------------------------------------------------------------- C: combine, one warp per (token, 32 channels)
-  for (int c = blockIdx.x * GV_WARPS + warp; c < T * IPT1; c += gridDim.x * GV_WARPS) {
+  for (int c = blockIdx.x * GV_WARPS + warp; p.out && c < T * IPT1; c += gridDim.x * GV_WARPS) {
     const int t = c / IPT1, jb = c - t * IPT1;
     // rows loaded eight at a time before they are summed (one L2 round trip per batch)
     const uint16_t ys = __ldcg(p.y + static_cast<size_t>(A + t) * H + 32 * jb + lane);

@@ -51,7 +51,9 @@ enum {
   MOE_ERR_WORKSPACE = -4, /* workspace smaller than moe_route_workspace_size() */
   MOE_ERR_CUDA = -5,      /* a CUDA launch or copy failed */
   MOE_ERR_DEVICE = -6,    /* moe_get_device_error found a kernel-side fault */
-  MOE_ERR_MODE = -7       /* unknown mode or variant */
+  MOE_ERR_MODE = -7,      /* unknown mode or variant */
+  MOE_ERR_OVERLAP = -8    /* an output shares memory with an input or another output in a way that the
+                             call cannot take (moe_residual_norm, moe_combine_residual_norm) */
 };
 
 /* Device error word values (written by kernels, read by moe_get_device_error). */
@@ -213,6 +215,118 @@ int moe_rms_norm(const uint16_t* x, uint16_t* out, int T, int H, float eps, moe_
  */
 int moe_norm_router(const uint16_t* x, const uint16_t* w_router, int T, int H, int E, float eps, uint16_t* x_norm,
                     float* logits, moe_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* Gates: other ways from router logits to experts                          */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * moe_route and moe_router choose by a softmax renormalised over the chosen
+ * ("Perplexity Open Sources Lily", Technical Details, Model bullet names no
+ * other).  A gate describes the other ways that mixture-of-experts models
+ * choose.  For a token's logits l:
+ *   s_e = sigmoid(l_e), or exp(l_e) / sum of all exp(l_i)
+ *   v_e = s_e + bias_e          (the bias, which balances the experts' load,
+ *                                takes part in the choice alone)
+ *   groups: the experts in order form `groups` groups of E / groups; a group's
+ *           score is its largest v_e or the sum of its two largest, and the
+ *           top_groups best groups stay (equal scores: lower index first)
+ *   chosen: the k largest v_e of the groups that stay, in descending order,
+ *           equal ones by index
+ *   w_j = scale * s_j / (sum of the chosen s_i, if renorm, else 1); 0 where
+ *         that sum is 0 (scores below 2^-126 count as 0)
+ * The choice is that of scores in 64 bits: a token whose choice a rounding in
+ * 32 bits could change is done again in 64.  Without a bias, and with groups
+ * (if any) scored by their largest, the logits themselves are compared.  An expert whose logit is -inf or NaN is not
+ * available: it is chosen only where fewer than k others are left (then by
+ * index), with weight 0; a group is scored by its available experts, one
+ * without any is behind all others.  A logit of +inf counts as the largest
+ * finite one.  bias has to be finite.
+ */
+enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 };
+enum { MOE_GROUP_MAX = 0, MOE_GROUP_TOP2 = 1 };
+
+typedef struct {
+  const float* bias;   /* [E], 4-byte aligned, or NULL */
+  int32_t score;       /* MOE_SCORE_* */
+  int32_t groups;      /* 1..32, divides E; 1: no groups */
+  int32_t top_groups;  /* 1..groups; the groups that stay have at least k experts */
+  int32_t group_score; /* MOE_GROUP_* */
+  int32_t renorm;
+  float scale;         /* finite */
+} moe_gate_t;
+
+/*
+ * moe_gate -- topk_ids int32 [T, k] and topk_w float32 [T, k] of router logits
+ * float32 [T, E].  T = 0 does nothing.  MOE_ERR_MODE for an unknown score,
+ * MOE_ERR_SHAPE for groups outside the limits.  One launch.
+ */
+int moe_gate(const float* logits, int T, int E, int k, const moe_gate_t* gate, int32_t* topk_ids, float* topk_w,
+             moe_stream_t stream);
+
+/*
+ * moe_route_gated -- moe_route with the experts chosen by a gate: the same
+ * outputs, workspace and limits.  With logits NULL the experts are those that
+ * topk_ids and topk_w hold (`gate` is not read; an id outside [0, E) sets
+ * MOE_DEV_BAD_INDEX where T * k > 1024 and is taken as one inside it).
+ */
+int moe_route_gated(const float* logits, int T, int E, int k, const moe_gate_t* gate, int block_n, int32_t* topk_ids,
+                    float* topk_w, int32_t* counts, int32_t* offsets, int32_t* perm, int32_t* inv_perm,
+                    int32_t* block_map, int32_t* num_blocks, void* workspace, size_t workspace_bytes,
+                    moe_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* Norms around a block, with its gate and its residual addition            */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * What follows a block (attention or experts) whose output is y, for the
+ * residual stream x, per token:
+ *   z = y / rms(y) * (w_post + offset)  if post, else y    rms(v) = sqrt(mean v^2 + eps)
+ *   r = scale x + gate z                the stream's next value
+ *   n = r / rms(r) * (w_pre + offset)   what the next block takes
+ * The sums run in FP32, n is taken of the unrounded r, r and n are rounded once.
+ * A tensor's rows are H consecutive elements and its strides count elements;
+ * pointers need only their elements' alignment (rows on 16 bytes are read
+ * faster).  r may take the place of x or y, n that of x or y or a gate per
+ * channel and token, if the pointer, the stride and the type are the same (in
+ * moe_combine_residual_norm not that of y); columns of one wider tensor may
+ * alternate.  Any other overlap of an output returns MOE_ERR_OVERLAP.
+ * Limits: 0 <= T <= 2^20 (T = 0 does nothing), 1 <= H <= 32768, strides below
+ * 2^40, those of inputs >= 0 (0: one row for all), those of outputs >= H.
+ */
+typedef struct {
+  const void* x;     /* [T, H] bf16, or float32 if stream_f32 */
+  int64_t x_stride;
+  void* r;           /* [T, H] of x's type, or NULL: not written */
+  int64_t r_stride;
+  uint16_t* n;       /* [T, H] bf16, or NULL: not written (r and n not both) */
+  int64_t n_stride;
+  const void* w_pre;  /* [H] bf16, or float32 if param_f32; NULL: n = r / rms(r) */
+  const void* w_post; /* as w_pre; NULL with post: z = y / rms(y) */
+  const void* gate;   /* bf16, or float32 if gate_f32; NULL: 1 */
+  int64_t gate_token_stride; /* 0: the same for all tokens */
+  int32_t gate_per_channel;  /* 0: one value per token, else H consecutive ones */
+  int32_t post;
+  int32_t stream_f32, param_f32, gate_f32;
+  float offset, scale, eps;  /* finite, eps >= 0 */
+} moe_residual_t;
+
+/*
+ * moe_residual_norm -- y bf16 [T, H] (row stride y_stride).  y NULL: r = scale
+ * x (the norm before the first block; post and gate are not read).  One launch.
+ */
+int moe_residual_norm(const uint16_t* y, int64_t y_stride, int T, int H, const moe_residual_t* p, moe_stream_t stream);
+
+/*
+ * moe_combine_residual_norm -- the same where token t's y is moe_combine's
+ * sum_j topk_w[t, j] * y[inv_perm[t*k + j]] + y[A + t] (FP32, in that order, not
+ * rounded in between); y bf16 [A+T, H], dense.  An inv_perm entry outside [0, A)
+ * sets MOE_DEV_BAD_INDEX and that term is skipped.  1 <= k <= 32; y, inv_perm and
+ * topk_w 16-byte aligned.  One launch.
+ */
+int moe_combine_residual_norm(const uint16_t* y, const int32_t* inv_perm, const float* topk_w, int T, int H, int k,
+                              const moe_residual_t* p, moe_stream_t stream);
 
 /* ------------------------------------------------------------------------ */
 /* Weights                                                                  */
@@ -425,7 +539,19 @@ int moe_layer_forward(const uint16_t* x, const float* logits, uint16_t* out,
                       moe_stream_t stream);
 
 /*
- * moe_layer_forward_host -- the same with x_host, logits_host and out_host in
+ * moe_layer_forward_gated -- moe_layer_forward with the experts chosen by
+ * `gate` (logits NULL: `gate` is not read, and buffers->topk_ids and topk_w hold
+ * the choice), and with `residual` (NULL: out is written) what follows the
+ * block fused with the combine, as moe_combine_residual_norm; out is then not
+ * read or written, nor combine_ws.  The same y as moe_layer_forward's for the
+ * same choice.
+ */
+int moe_layer_forward_gated(const uint16_t* x, const float* logits, const moe_gate_t* gate, uint16_t* out,
+                            const moe_residual_t* residual, int T, int H, int F, int E, int k, int block_n, int impl,
+                            const moe_weights_t* weights, const moe_buffers_t* buffers, moe_stream_t stream);
+
+/*
+ * moe_layer_forward_host -- moe_layer_forward with x_host, logits_host and out_host in
  * host memory, all on `stream`: x is copied to the device staging buffer x_dev
  * first (the grouped GEMM reads each row k + 1 times).  When logits_host and
  * out_host are pinned (or registered) host memory, the kernels read the

@@ -1,0 +1,216 @@
+"""moe_gate and moe_route_gated on the GPU against the float64 oracle: the same experts in the same order, always;
+weights within the error of their FP32 arithmetic."""
+import numpy as np
+import pytest
+
+from oracle import gate_ref
+
+pytestmark = pytest.mark.gpu
+
+
+def setup_module():
+    import gpu_util
+    gpu_util.ensure_built()
+
+
+def make(k, bias=None, **kw):
+    import torch
+
+    from bit_mixture_experts_gb300 import ExpertGate
+    return ExpertGate(k, bias=None if bias is None else torch.tensor(bias, dtype=torch.float32, device="cuda"), **kw)
+
+
+def weight_bound(ref, logits, ids, kw):
+    """u = 2^-24.  A score: exp 4 u, its argument's rounding u (top - l), sum and division 3 u.  The sum over the experts
+    (at most 64 per lane, then 5 steps): 69 u, its terms 4 u and as much as ln E u for their arguments; the sum over the
+    chosen 5 u and its terms' error; division and scale 2 u.  Below 2^-126 scores are flushed."""
+    l = np.take_along_axis(np.minimum(np.nan_to_num(logits, nan=-np.inf, posinf=3.4e38), 3.4e38), ids, 1)
+    top = np.nanmax(np.where(np.isfinite(logits), logits, np.nan), axis=1, initial=0, keepdims=True)
+    rel = 2 * 7 + 7.0
+    if kw.get("score", "softmax") == "softmax":
+        with np.errstate(invalid="ignore"):
+            rel = rel + np.where(np.isfinite(l), np.abs(top - l), 0) + 80
+    return np.abs(ref) * rel * 2.0 ** -24 + abs(kw.get("scale", 1.0)) * 2.0 ** -120
+
+
+def check(logits, k, bias=None, **kw):
+    import torch
+
+    from bit_mixture_experts_gb300 import _lib
+    gate = make(k, bias, **kw)
+    T, E = logits.shape
+    # guard rows behind the last token stay as they are
+    ids = torch.full((T + 1, k), -7, dtype=torch.int32, device="cuda")
+    w = torch.full((T + 1, k), -7.0, device="cuda")
+    gate.choose(torch.tensor(logits, dtype=torch.float32, device="cuda"), out=(ids[:T], w[:T]))
+    torch.cuda.synchronize()
+    assert _lib.moe_get_device_error() == 0
+    assert (ids[T] == -7).all() and (w[T] == -7).all()
+    want_ids, want_w = gate_ref.choose(logits.astype(np.float32), k, bias=None if bias is None else np.float32(bias), **kw)
+    np.testing.assert_array_equal(ids[:T].cpu().numpy(), want_ids)
+    got = w[:T].double().cpu().numpy()
+    off = np.abs(got - want_w) - weight_bound(want_w, logits.astype(np.float64), want_ids, kw)
+    assert (off <= 0).all(), (off.max(), np.abs(got - want_w).max())
+
+
+def draw(T, E, seed, coarse=False):
+    r = np.random.default_rng(seed)
+    l = (r.standard_normal((T, E)) * np.exp(0.3 * r.standard_normal((T, 1))) + 0.7 * r.standard_normal(E)).astype(np.float32)
+    if coarse:
+        l = np.round(l * 4) / 4
+    return l, (np.round(r.standard_normal(E) * 40) * 0.001).astype(np.float32)
+
+
+CASES = [  # T, E, k, groups, top_groups
+    (1, 1, 1, 1, 1), (3, 2, 2, 1, 1), (5, 7, 3, 1, 1), (33, 32, 32, 1, 1), (9, 37, 5, 1, 1), (17, 74, 8, 2, 1),
+    (64, 160, 6, 8, 3), (333, 256, 8, 8, 4), (100, 256, 8, 1, 1), (7, 96, 32, 3, 2), (8, 1020, 16, 17, 5),
+    (5, 1000, 4, 5, 2), (4, 1024, 32, 32, 9), (3, 1024, 32, 1, 1), (2, 64, 4, 32, 2), (6, 1023, 31, 31, 3),
+]
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("with_bias", [False, True])
+@pytest.mark.parametrize("T,E,k,groups,top", CASES)
+def test_choice_and_weights(T, E, k, groups, top, with_bias, score):
+    seed = T * 1000 + E + 7 * k + 13 * groups
+    for i, (group_score, renorm, coarse) in enumerate([("top2", True, False), ("max", False, True)]):
+        l, b = draw(T, E, seed + i, coarse)
+        check(l, k, b if with_bias else None, score=score, groups=groups, top_groups=top, group_score=group_score,
+              renorm=renorm, scale=2.5 if renorm else 1.0)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_equal_scores_go_to_the_lower_index(score):
+    E = 256
+    flat = np.zeros((4, E), np.float32)
+    check(flat, 8, score=score)
+    check(flat, 8, np.zeros(E), score=score, groups=8, top_groups=4)
+    b = np.zeros(E)
+    b[[3, 77, 78, 200, 255]] = 0.001
+    check(flat, 8, b, score=score, groups=8, top_groups=4)
+    check(np.where(np.arange(E) % 2, 0.0, -0.0)[None].astype(np.float32), 9, score=score)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("groups,top", [(1, 1), (8, 3)])
+def test_scores_that_differ_by_less_than_32_bits_hold(score, groups, top):
+    # biases that bring every expert's value to the same number, as far as 32 bits go: the order is that of what is left
+    E, r = 256, np.random.default_rng(5)
+    l = r.standard_normal((1, E)).astype(np.float32)
+    s, _ = gate_ref.scores(l[0], score)
+    b = (0.9 - s).astype(np.float32)
+    check(np.repeat(l, 3, 0), 8, b, score=score, groups=groups, top_groups=top)
+    check(np.repeat(l, 3, 0), 32, b, score=score, groups=groups, top_groups=max(top, 4) if groups > 1 else 1,
+          group_score="max")
+    # only the border of the choice is near: expert k is next to expert k + 1
+    l = np.linspace(3, -3, E).astype(np.float32)[None]
+    s, _ = gate_ref.scores(l[0], score)
+    b = np.zeros(E, np.float32)
+    b[200] = np.float32(s[7] - s[200])
+    check(l, 8, b, score=score)
+    check(l, 9, b, score=score)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("with_bias", [False, True])
+@pytest.mark.parametrize("group_score", ["max", "top2"])
+def test_experts_that_are_not_available(score, with_bias, group_score):
+    l, b = draw(12, 64, 3)
+    b = b if with_bias else None
+    l[0] = -np.inf
+    l[1, :] = np.nan
+    l[2, 10:] = -np.inf
+    l[3, ::2] = np.nan
+    l[4, 8:16] = -np.inf   # a group without any
+    l[5, np.arange(64) % 8 != 3] = -np.inf  # one in each group
+    l[6, 5] = np.inf
+    l[7, [5, 9]] = np.inf
+    l[8, :60] = -np.inf
+    l[9] = -200.0  # scores that 32 bits do not hold (sigmoid)
+    for groups, top in ((1, 1), (8, 2)):
+        check(l, 8, b, score=score, groups=groups, top_groups=top, group_score=group_score)
+
+
+def test_large_logits():
+    r = np.random.default_rng(1)
+    l = (r.standard_normal((16, 128)) * 60).astype(np.float32)
+    for score in ("softmax", "sigmoid"):
+        check(l, 4, None, score=score)
+        check(l, 4, np.zeros(128), score=score, groups=4, top_groups=2) if score == "softmax" else None
+
+
+def test_no_tokens():
+    import torch
+    ids, w = make(2).choose(torch.empty((0, 16), device="cuda"))
+    assert ids.shape == (0, 2) and w.shape == (0, 2)
+
+
+def test_softmax_gate_is_moe_route():
+    import torch
+
+    from bit_mixture_experts_gb300 import _lib
+    for T, E, k in ((5, 16, 2), (300, 256, 8)):
+        l = torch.tensor(draw(T, E, T)[0], device="cuda")
+        got = make(k).route(l, 32)
+        ref = [torch.empty_like(t) for t in got]
+        ws = torch.zeros(max(16, _lib.moe_route_workspace_size(T, E, k, 32)), dtype=torch.uint8, device="cuda")
+        _lib.moe_route(l, k, 32, *ref, ws)
+        n = int(ref[7])
+        for name, a, b in zip(got._fields, got, ref):
+            a, b = (a[:n], b[:n]) if name == "block_map" else (a, b)
+            assert torch.equal(a, b), name
+
+
+@pytest.mark.parametrize("T,E,k,block_n", [(1, 256, 8, 8), (100, 64, 4, 16), (129, 64, 8, 64), (3000, 256, 8, 64)])
+def test_route(T, E, k, block_n):
+    import torch
+
+    from bit_mixture_experts_gb300 import _lib
+    l, b = draw(T, E, T + E)
+    kw = dict(score="sigmoid", groups=8, top_groups=4, scale=2.5)
+    gate = make(k, b, **kw)
+    lt = torch.tensor(l, device="cuda")
+    got = [gate.route(lt, block_n) for _ in range(2)][1]  # the second call finds the scratch as the first left it
+    ids, w = gate.choose(lt)
+    torch.cuda.synchronize()
+    assert _lib.moe_get_device_error() == 0
+    assert torch.equal(got.topk_ids, ids) and torch.equal(got.topk_w, w)
+    want = gate_ref.sort_assignments(ids.cpu().numpy(), E)
+    for name, ref in zip(("counts", "offsets", "perm", "inv_perm"), want):
+        np.testing.assert_array_equal(getattr(got, name).cpu().numpy(), ref, err_msg=name)
+
+
+def test_streams_and_graphs():
+    import torch
+    gate = make(8, draw(1, 256, 9)[1], score="sigmoid", groups=8, top_groups=4)
+    a, b = (torch.tensor(draw(700, 256, s)[0], device="cuda") for s in (1, 2))
+    want = [gate.route(x, 64) for x in (a, b)]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for s in (side, side.cuda_stream):
+        got = gate.route(b, 64, stream=s)
+        side.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(got[:6], want[1][:6]))
+    # two graphs captured on one stream, replayed together with other calls in between
+    x = a.clone()
+    graphs, outs = [], []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            outs.append(gate.route(x, 64))
+        graphs.append(g)
+    x.copy_(b)
+    other = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graphs[0].replay()
+    with torch.cuda.stream(other):
+        graphs[1].replay()
+    gate.route(a, 64)
+    torch.cuda.synchronize()
+    for o in outs:
+        assert all(torch.equal(p, q) for p, q in zip(o[:6], want[1][:6]))
+    # the bias is read by every call
+    gate.bias.zero_()
+    ids, _ = gate.choose(b)
+    np.testing.assert_array_equal(
+        ids.cpu().numpy(), gate_ref.choose(b.cpu().numpy(), 8, score="sigmoid", bias=np.zeros(256), groups=8, top_groups=4)[0])
