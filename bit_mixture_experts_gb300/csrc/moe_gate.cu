@@ -1,35 +1,72 @@
 // Router logits to experts and weights (moe_gate; see moe_gate_dev.cuh for the
-// choice itself): one warp per token.
+// choice itself).
 #include "moe_gate_dev.cuh"
 
 namespace moe {
 
+int num_sms();
+
 namespace {
 
 using gate_dev::Gate;
+using gate_dev::Mode;
 
 constexpr int GATE_WARPS = 8;
 
-template <int EPL, bool VEC>
+template <int EPL, int IDX, Mode MODE, int BATCH, bool WHOLE>
 __global__ void __launch_bounds__(32 * GATE_WARPS) gate_kernel(const float* logits, int T,
                                                                const __grid_constant__ Gate g, int32_t* ids, float* w) {
+  constexpr int SEG = 32 / BATCH;
   const int lane = threadIdx.x & 31;
-  const int t = static_cast<int>(blockIdx.x) * GATE_WARPS + (threadIdx.x >> 5);
+  int t = (static_cast<int>(blockIdx.x) * GATE_WARPS + (threadIdx.x >> 5)) * BATCH;
+  const int step = static_cast<int>(gridDim.x) * GATE_WARPS * BATCH;
   if (t >= T) return;
-  int id;
-  float x;
-  gate_dev::warp_gate<EPL, VEC>(logits + static_cast<size_t>(t) * g.E, g, lane, &id, &x);
-  if (lane < g.k) {
-    ids[static_cast<size_t>(t) * g.k + lane] = id;
-    w[static_cast<size_t>(t) * g.k + lane] = x;
+  const gate_dev::Lane me(g, lane);
+  const gate_dev::Units<EPL, IDX, MODE> units(g, me);
+  for (; t < T; t += step) {
+    int id;
+    float x;
+    gate_dev::warp_gate<EPL, IDX, MODE, BATCH, WHOLE>(logits, t, T, units, g, me, lane, &id, &x);
+    if (t + lane / SEG < T && lane % SEG < g.k) {
+      const size_t at = static_cast<size_t>(t + lane / SEG) * g.k + lane % SEG;
+      ids[at] = id;
+      w[at] = x;
+    }
   }
 }
 
-template <int EPL, bool VEC>
+template <int EPL, int IDX, Mode MODE, int BATCH, bool WHOLE>
 cudaError_t launch(const float* logits, int T, const Gate& g, int32_t* ids, float* w, cudaStream_t s) {
-  gate_kernel<EPL, VEC><<<ceil_div(T, GATE_WARPS), 32 * GATE_WARPS, 0, s>>>(logits, T, g, ids, w);
+  const auto kernel = gate_kernel<EPL, IDX, MODE, BATCH, WHOLE>;
+  int per_sm = 0;
+  const cudaError_t e = cached_occupancy(reinterpret_cast<const void*>(kernel), 32 * GATE_WARPS, 0, &per_sm);
+  if (e != cudaSuccess) return e;
+  kernel<<<min(ceil_div(T, GATE_WARPS * BATCH), num_sms() * per_sm), 32 * GATE_WARPS, 0, s>>>(logits, T, g, ids, w);
   note_launches(1);
   return cudaGetLastError();
+}
+
+template <int EPL, int IDX, Mode MODE, bool WHOLE>
+cudaError_t launch_batch(const float* logits, int T, const Gate& g, int32_t* ids, float* w, cudaStream_t s) {
+  // with few tokens, one per warp: they are done sooner
+  const int batch = T <= GATE_WARPS * num_sms() ? 1 : gate_dev::batch_of(g, EPL);
+  if (EPL <= 8 && batch == 4) return launch<EPL, IDX, MODE, EPL <= 8 ? 4 : 1, WHOLE>(logits, T, g, ids, w, s);
+  if (EPL <= 16 && batch == 2) return launch<EPL, IDX, MODE, EPL <= 16 ? 2 : 1, WHOLE>(logits, T, g, ids, w, s);
+  return launch<EPL, IDX, MODE, 1, WHOLE>(logits, T, g, ids, w, s);
+}
+
+template <Mode MODE>
+cudaError_t launch_mode(const float* logits, int T, const Gate& g, int32_t* ids, float* w, cudaStream_t s) {
+  const bool whole = g.per_group % g.width == 0 && 32 >> g.lanes_log == g.groups;
+  if (g.E > 256) {  // keys of ten index bits
+    if (g.width <= 16) return launch_batch<16, 10, MODE, false>(logits, T, g, ids, w, s);
+    if (g.width > 32) return launch_batch<64, 10, MODE, false>(logits, T, g, ids, w, s);
+    return launch_batch<32, 10, MODE, false>(logits, T, g, ids, w, s);
+  }
+  if (g.width <= 4) return launch_batch<4, 8, MODE, false>(logits, T, g, ids, w, s);
+  if (g.width > 8) return launch_batch<16, 8, MODE, false>(logits, T, g, ids, w, s);
+  return whole && g.width == 8 ? launch_batch<8, 8, MODE, true>(logits, T, g, ids, w, s)
+                               : launch_batch<8, 8, MODE, false>(logits, T, g, ids, w, s);
 }
 
 }  // namespace
@@ -57,14 +94,9 @@ Gate make_gate(const moe_gate_t* p, int E, int k) {
 cudaError_t launch_gate(const float* logits, int T, const moe_gate_t* p, int E, int k, int32_t* ids, float* w,
                         cudaStream_t s) {
   const Gate g = make_gate(p, E, k);
-  const bool vec = g.width % 4 == 0 && g.per_group % g.width == 0;
-  if (g.width <= 1) return launch<1, false>(logits, T, g, ids, w, s);
-  if (g.width <= 2) return launch<2, false>(logits, T, g, ids, w, s);
-  if (g.width <= 4) return vec ? launch<4, true>(logits, T, g, ids, w, s) : launch<4, false>(logits, T, g, ids, w, s);
-  if (g.width <= 8) return vec ? launch<8, true>(logits, T, g, ids, w, s) : launch<8, false>(logits, T, g, ids, w, s);
-  if (g.width <= 16) return vec ? launch<16, true>(logits, T, g, ids, w, s) : launch<16, false>(logits, T, g, ids, w, s);
-  if (g.width <= 32) return vec ? launch<32, true>(logits, T, g, ids, w, s) : launch<32, false>(logits, T, g, ids, w, s);
-  return launch<64, false>(logits, T, g, ids, w, s);
+  if (g.by_logit) return launch_mode<gate_dev::BY_LOGIT>(logits, T, g, ids, w, s);
+  return g.softmax ? launch_mode<gate_dev::SOFTMAX>(logits, T, g, ids, w, s)
+                   : launch_mode<gate_dev::SIGMOID>(logits, T, g, ids, w, s);
 }
 
 }  // namespace moe

@@ -1,4 +1,4 @@
-// The choice of a token's experts by one warp, for routers with sigmoid or
+// The choice of tokens' experts by a warp, for routers with sigmoid or
 // softmax scores, a bias that takes part in the choice alone, groups of experts
 // of which the best stay, and weights that are renormalised and scaled:
 //
@@ -8,14 +8,22 @@
 //   w_j = scale s_j / (sum of the chosen s, or 1)
 //
 // The choice has to be what exact scores give, and FP32 scores can be off by
-// more than two experts differ.  So the FP32 choice comes with a bound on the
-// error of each v, and where two neighbours of the sorted choice, the last one
-// chosen and any other expert, or the last group that stays and the first that
-// does not are nearer to each other than their bounds, the token is done again
-// in 64 bits (about one token in a thousand at 256 experts).  Experts whose
-// logit and bias are the same bits tie in any precision and need no second
-// look.  Without a bias the scores are monotone in the logits, which are then
-// compared themselves, exactly.
+// more than two experts differ.  So values are compared as integers m, v in
+// units of 2^-23 (2^-21 above 256 experts) of the range that v can have, and
+// where two neighbours of the sorted choice, the last one chosen and any other
+// expert, or the last group that stays and the first that does not are not
+// further apart than their errors, the token is done again with scores of twice
+// the length, off by less than 2^-40 (256 experts, 8 chosen: about one token in
+// 700).  Experts whose logit and bias are
+// the same bits tie in any precision and need no second look.  Without a bias
+// the scores are monotone in the logits, which are then compared themselves: m
+// is the upper 23 (21) bits of the logit, and the second look is at all of it.
+//
+// m and the expert's index make one key (equal m: lower index first), 31 bits,
+// so that a round of the choice is one redux.sync over the lanes' largest keys
+// below the last one chosen.  A warp takes up to four tokens at a time: what
+// concerns a token's k choices or its groups needs fewer lanes than a warp has,
+// and is done for all of them at once.
 #pragma once
 #include <float.h>
 
@@ -42,273 +50,594 @@ struct Gate {
 // Experts a lane holds, at most (groups of any number up to 32, E <= 1024).
 constexpr int MAX_WIDTH = 64;
 
-// Bound on |s - exact| = rel s + abs.  Sigmoid: the fast exponential is off by (2 + 1.16 |l|) 2^-23, which
-// enters s times 1 - s (s (1 - s) <= 1/4, s (1 - s) |l| <= 0.224), the sum by 2^-24, the division by 2^-22.
-// Softmax: expf by 2^-22, its argument by 2^-24 (m - l), together at most 2^-24 0.37 / sum that enters
-// absolutely (x e^-x <= 0.37); the sum by as much on average (at most ln 1024 2^-24) and its additions.
-struct Bound {
-  float rel, abs;
-};
+enum Mode { BY_LOGIT, SIGMOID, SOFTMAX };  // what is compared; SOFTMAX also where weights need the sum over all
 
 __device__ __forceinline__ float available(float l) {  // NaN counts as -inf, +inf as the largest number
   return l > -INFINITY ? fminf(l, FLT_MAX) : -INFINITY;
 }
 
-__device__ __forceinline__ float fast_sigmoid(float l) { return __fdividef(1.0f, 1.0f + __expf(-l)); }
-
-// ---- the same in 64 bits; lane j < k gets the j-th choice
-__device__ __forceinline__ uint64_t double_key(double x) {
-  uint64_t u = static_cast<uint64_t>(__double_as_longlong(x));
-  if (u == 0x8000000000000000ull) u = 0;
-  return u >> 63 ? ~u : u | 0x8000000000000000ull;
+__device__ __forceinline__ float fast_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
+__device__ __forceinline__ float fast_rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// A lane's share of the experts.
+struct Lane {
+  int group, first, n;
+  __device__ __forceinline__ Lane(const Gate& g, int lane) {
+    const int sub = lane & ((1 << g.lanes_log) - 1);
+    group = lane >> g.lanes_log;
+    first = group * g.per_group + sub * g.width;
+    n = group < g.groups ? min(max(g.per_group - sub * g.width, 0), g.width) : 0;
+  }
+};
+
+// ---- The second look: scores as pairs of floats (high part, rest), about 45 bits, on the FP32 pipe.  (In
+// 64-bit floats, of which an SM does one a clock, a token's 256 exponentials took 9000 cycles, all of its
+// second look 29000.)
+struct Pair {
+  float h, l;
+};
+
+__device__ __forceinline__ Pair fast_sum(float a, float b) {  // |a| >= |b| or a = 0: exact
+  const float s = __fadd_rn(a, b);
+  return {s, __fsub_rn(b, __fsub_rn(s, a))};
+}
+
+__device__ __forceinline__ Pair sum(float a, float b) {  // exact
+  const float s = __fadd_rn(a, b), bb = __fsub_rn(s, a);
+  return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, bb)), __fsub_rn(b, bb))};
+}
+
+__device__ __forceinline__ Pair add(Pair a, Pair b) {
+  const Pair s = sum(a.h, b.h);
+  return fast_sum(s.h, __fadd_rn(s.l, __fadd_rn(a.l, b.l)));
+}
+
+__device__ __forceinline__ Pair mul(Pair a, Pair b) {
+  const float p = __fmul_rn(a.h, b.h);
+  return fast_sum(p, __fmaf_rn(a.h, b.l, __fmaf_rn(a.l, b.h, __fmaf_rn(a.h, b.h, -p))));
+}
+
+// e^x for x <= 0, 0 below about -87: x = n ln 2 + r with ln 2 in three parts (the first has ten bits, so that
+// its product with n is exact), e^r by its Taylor series, the terms from r^7 on as floats.
+__device__ __forceinline__ Pair exp_pair(Pair x) {
+  if (x.h < -150.f) x = {-150.f, 0.f};
+  const float n = rintf(x.h * 1.44269504f);
+  Pair r = sum(__fmaf_rn(n, -0.693359375f, x.h), x.l);
+  const float p = __fmul_rn(n, 0x1.bd01060000000p-13f);
+  r = add(r, {p, __fmaf_rn(n, -0x1.cf79ac0000000p-40f, __fmaf_rn(n, 0x1.bd01060000000p-13f, -p))});
+  float t = 1.0f / 479001600.0f;
+  t = fmaf(t, r.h, 1.0f / 39916800.0f);
+  t = fmaf(t, r.h, 1.0f / 3628800.0f);
+  t = fmaf(t, r.h, 1.0f / 362880.0f);
+  t = fmaf(t, r.h, 1.0f / 40320.0f);
+  t = fmaf(t, r.h, 1.0f / 5040.0f);
+  Pair q = add({0x1.6c16c20000000p-10f, -0x1.27d27e0000000p-35f}, mul(r, {t, 0.f}));
+  q = add({0x1.1111120000000p-7f, -0x1.ddddde0000000p-32f}, mul(r, q));
+  q = add({0x1.5555560000000p-5f, -0x1.5555560000000p-30f}, mul(r, q));
+  q = add({0x1.5555560000000p-3f, -0x1.5555560000000p-28f}, mul(r, q));
+  q = add({0.5f, 0.f}, mul(r, q));
+  q = add({1.0f, 0.f}, mul(r, q));
+  q = add({1.0f, 0.f}, mul(r, q));
+  const float f = n < -126.f ? 0.f : __uint_as_float(static_cast<uint32_t>(static_cast<int>(n) + 127) << 23);
+  return {q.h * f, q.l * f};
+}
+
+__device__ __forceinline__ Pair reciprocal(Pair d) {  // of 1 and more
+  const float q = __frcp_rn(d.h);
+  return fast_sum(q, __fmul_rn(q, __fmaf_rn(-q, d.l, __fmaf_rn(-q, d.h, 1.0f))));
+}
+
+__device__ __forceinline__ Pair sigmoid_pair(float l) {
+  const Pair e = exp_pair({-fabsf(l), 0.f});
+  const Pair d = fast_sum(1.0f, e.h), q = reciprocal(fast_sum(d.h, __fadd_rn(d.l, e.l)));
+  return l >= 0.f ? q : mul(e, q);
+}
+
+// Pairs in their order as integers: of -inf 0x007fffff80000000, of all others more.
+__device__ __forceinline__ uint64_t pair_key(Pair x) { return static_cast<uint64_t>(float_key(x.h)) << 32 | float_key(x.l); }
+__device__ __forceinline__ Pair key_pair(uint64_t k) {
+  return {key_float(static_cast<uint32_t>(k >> 32)), key_float(static_cast<uint32_t>(k))};
+}
+constexpr uint64_t NOT_AVAILABLE = 0x007fffff80000000ull;
+
+// The largest of the lanes' x, by two reductions of 32 bits.
 __device__ __forceinline__ uint64_t warp_max_u64(uint64_t x) {
-#pragma unroll
-  for (int m = 16; m >= 1; m >>= 1) {
-    const uint64_t o = __shfl_xor_sync(FULL, x, m);
-    x = o > x ? o : x;
-  }
-  return x;
+  const uint32_t hi = static_cast<uint32_t>(x >> 32), top = __reduce_max_sync(FULL, hi);
+  const uint32_t lo = __reduce_max_sync(FULL, hi == top ? static_cast<uint32_t>(x) : 0u);
+  return static_cast<uint64_t>(top) << 32 | lo;
 }
 
-static __device__ __noinline__ int choose_exact(const float* row, const Gate& g, int lane) {
-  const int L = 1 << g.lanes_log, group = lane >> g.lanes_log, sub = lane & (L - 1);
-  const int first = group * g.per_group + sub * g.width;
-  const int n = group < g.groups ? min(max(g.per_group - sub * g.width, 0), g.width) : 0;
-  const double none = -INFINITY;
-  double v[MAX_WIDTH];
+// What softmax's scores hang on, by the whole warp: the largest logit and 1 / sum.
+struct Scale {
+  float top;
+  Pair inv;
+};
+
+__device__ __forceinline__ Scale softmax_scale(const float* row, const Lane& me) {
   float top = -INFINITY;
-  for (int i = 0; i < n; ++i) top = fmaxf(top, available(__ldcg(row + first + i)));
+#pragma unroll 4
+  for (int i = 0; i < me.n; ++i) top = fmaxf(top, available(__ldcg(row + me.first + i)));
+  __syncwarp();
+  top = key_float(__reduce_max_sync(FULL, float_key(top)));
+  Pair total = {0.f, 0.f};
+#pragma unroll 2
+  for (int i = 0; i < me.n; ++i) {
+    const float l = available(__ldcg(row + me.first + i));
+    if (l != -INFINITY) total = add(total, exp_pair(sum(l, -top)));
+  }
+  __syncwarp();
 #pragma unroll
-  for (int m = 16; m >= 1; m >>= 1) top = fmaxf(top, __shfl_xor_sync(FULL, top, m));
-  double sum = 0.0;
-  for (int i = 0; i < n; ++i) {
-    const float l = available(__ldcg(row + first + i));
-    v[i] = l == -INFINITY ? none : g.softmax ? exp(static_cast<double>(l) - top) : 1.0 / (1.0 + exp(-static_cast<double>(l)));
-    if (v[i] != none) sum += v[i];
-  }
-  if (g.softmax) {
-#pragma unroll
-    for (int m = 16; m >= 1; m >>= 1) sum += __shfl_xor_sync(FULL, sum, m);
-  }
-  double c1 = none, c2 = none;
-  for (int i = 0; i < n; ++i) {
-    if (v[i] == none) continue;
-    if (g.softmax) v[i] /= sum;
-    if (g.bias) v[i] += static_cast<double>(__ldg(g.bias + first + i));
-    if (!(v[i] == v[i])) v[i] = none;
-    c2 = v[i] > c1 ? c1 : fmax(c2, v[i]);
-    c1 = fmax(c1, v[i]);
-  }
-  bool stays = group < g.groups;
-  if (g.top_groups < g.groups) {
-    for (int m = 1; m < L; m <<= 1) {
-      const double o1 = __shfl_xor_sync(FULL, c1, m), o2 = __shfl_xor_sync(FULL, c2, m);
-      c2 = fmax(fmin(c1, o1), fmax(c2, o2));
-      c1 = fmax(c1, o1);
+  for (int m = 16; m >= 1; m >>= 1)
+    total = add(total, {__shfl_xor_sync(FULL, total.h, m), __shfl_xor_sync(FULL, total.l, m)});
+  return {top, reciprocal(total)};
+}
+
+// The value of expert e, logit l.
+template <Mode MODE>
+__device__ __forceinline__ uint64_t value_of(float l, int e, const Gate& g, const Scale& s) {
+  if (l == -INFINITY) return NOT_AVAILABLE;
+  Pair v = {l, 0.f};
+  if (MODE != BY_LOGIT) {
+    v = MODE == SOFTMAX ? mul(exp_pair(sum(l, -s.top)), s.inv) : sigmoid_pair(l);
+    if (g.bias) v = add(v, {__ldg(g.bias + e), 0.f});
+    if (!(fabsf(v.h) < INFINITY)) {  // a bias that is not finite
+      if (!(v.h > 0.f)) return NOT_AVAILABLE;
+      v = {FLT_MAX, 0.f};
     }
-    const double mine = g.top2 && c2 != none ? c1 + c2 : c1;
-    int ahead = 0;
-    for (int o = 0; o < g.groups; ++o) {
-      const double other = __shfl_sync(FULL, mine, o << g.lanes_log);
-      ahead += other > mine || (other == mine && o < group);
-    }
-    stays &= ahead < g.top_groups;
   }
-  uint64_t taken = 0;
-  int id = 0;
+  return pair_key(v);
+}
+
+// Whether the lane's group stays, by the whole warp.
+template <Mode MODE>
+__device__ __forceinline__ bool group_stays(const float* row, const Lane& me, const Gate& g, const Scale& s) {
+  uint64_t c1 = 0, c2 = 0;
+#pragma unroll 2
+  for (int i = 0; i < me.n; ++i) {
+    const uint64_t x = value_of<MODE>(available(__ldcg(row + me.first + i)), me.first + i, g, s), lo = min(c1, x);
+    c1 = max(c1, x);
+    c2 = max(c2, lo);
+  }
+  __syncwarp();
+  for (int m = 1; m < 1 << g.lanes_log; m <<= 1) {
+    const uint64_t o1 = __shfl_xor_sync(FULL, c1, m), o2 = __shfl_xor_sync(FULL, c2, m);
+    c2 = max(min(c1, o1), max(c2, o2));
+    c1 = max(c1, o1);
+  }
+  const uint64_t mine = g.top2 && c2 > NOT_AVAILABLE ? pair_key(add(key_pair(c1), key_pair(c2))) : c1;
+  int ahead = 0;
+  for (int m = 1; m << g.lanes_log < 32; ++m) {
+    const uint64_t o = __shfl_xor_sync(FULL, mine, m << g.lanes_log);
+    ahead += o > mine || (o == mine && (me.group ^ m) < me.group);
+  }
+  return ahead < g.top_groups && me.group < g.groups;
+}
+
+// The choice among the groups that stay with every value worked out anew for each of the k: for tokens of
+// which more experts are close to the last one chosen than a warp has lanes.
+template <Mode MODE>
+__device__ __forceinline__ int choose_slowly(const float* row, const Lane& me, bool stays, const Gate& g, const Scale& s,
+                                             int lane) {
+  uint64_t last = ~0ull;
+  int last_e = -1, id = 0;
+#pragma unroll 1
   for (int j = 0; j < g.k; ++j) {
     uint64_t best = 0;
     int at = 0;
-    for (int i = 0; stays && i < n; ++i) {
-      const uint64_t key = double_key(v[i]);
-      if (!(taken >> i & 1) && key > best) {
-        best = key;
-        at = i;
+#pragma unroll 1
+    for (int i = 0; stays && i < me.n; ++i) {
+      const int e = me.first + i;
+      const uint64_t x = value_of<MODE>(available(__ldcg(row + e)), e, g, s);
+      if (x > best && (x < last || (x == last && e > last_e))) {
+        best = x;
+        at = e;
       }
     }
+    __syncwarp();
     const uint64_t most = warp_max_u64(best);
     const int win = __ffs(__ballot_sync(FULL, best == most)) - 1;
-    if (lane == win) taken |= 1ull << at;
-    const int e = __shfl_sync(FULL, first + at, win);
-    if (lane == j) id = e;
+    last = most;
+    last_e = __shfl_sync(FULL, at, win);
+    if (lane == j) id = last_e;
   }
-  return min(id, g.E - 1);
+  return id;
 }
 
-// Lane j < k ends with the token's j-th choice and its weight.  EPL >= g.width; VEC: the lane's experts
-// start on 16 bytes and are a multiple of four.  The row is read through L2 (it may have been written by
-// other CTAs of the same kernel).
-template <int EPL, bool VEC>
-__device__ __forceinline__ void warp_gate(const float* row, const Gate& g, int lane, int* id_out, float* w_out) {
-  const int L = 1 << g.lanes_log, group = lane >> g.lanes_log, sub = lane & (L - 1);
-  const int first = group * g.per_group + sub * g.width;
-  const int n = group < g.groups ? min(max(g.per_group - sub * g.width, 0), g.width) : 0;
-  float v[EPL];  // logits, then what is compared
+// What a warp keeps from token to token: its experts' biases in units, and what a unit is.
+//   m = s a + base_e,  base_e = (b_e - least bias) a + 2,  below 2^(31 - IDX)
+// computed as FP32 numbers of 2^23 and more, whose lower bits are the integer.
+template <int EPL, int IDX, Mode MODE>
+struct Units {
+  static constexpr bool KEEP = EPL <= 8;
+  float a, least;
+  float base[KEEP ? EPL : 1];
+
+  __device__ __forceinline__ float at(float b) const { return fmaf(b - least, a, 8388608.0f + 2.0f); }
+
+  __device__ __forceinline__ Units(const Gate& g, const Lane& me) : a(0.f), least(0.f) {
+    if (MODE == BY_LOGIT) return;
+    float most = 0.f;
+    if (g.bias) {
+      float lo = INFINITY, hi = -INFINITY;
+      bool nan = false;
+      for (int i = 0; i < me.n; ++i) {
+        const float b = __ldg(g.bias + me.first + i);
+        lo = fminf(lo, b);
+        hi = fmaxf(hi, b);
+        nan |= b != b;
+      }
+      least = key_float(__reduce_min_sync(FULL, float_key(lo)));
+      most = __any_sync(FULL, nan) ? INFINITY : key_float(__reduce_max_sync(FULL, float_key(hi)));
+    }
+    // (a range that is not finite leaves nothing to compare: every token is then done in 64 bits)
+    const float range = most - least + 1.0f;
+    if (range < 1e30f) {
+      a = (static_cast<float>(1 << (31 - IDX)) - 16.0f) / range;
+    } else {
+      least = 0.f;
+    }
+    if (KEEP) {
 #pragma unroll
-  for (int i = 0; i < EPL; ++i) v[i] = -INFINITY;
-  if (VEC) {
+      for (int i = 0; i < EPL; ++i) base[KEEP ? i : 0] = at(g.bias && a > 0.f && i < me.n ? __ldg(g.bias + me.first + i) : least);
+    }
+  }
+};
+
+// Loads a lane's logits; VEC: they start on 16 bytes and are a multiple of four.  Through L2: the row may
+// have been written by other CTAs of the same kernel.
+template <int EPL, bool VEC>
+__device__ __forceinline__ void load_logits(const float* row, const Lane& me, float (&l)[EPL]) {
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) l[i] = -INFINITY;
+  if constexpr (VEC) {
 #pragma unroll
     for (int i = 0; i < EPL; i += 4)
-      if (i < n) {
-        const float4 x = __ldcg(reinterpret_cast<const float4*>(row + first + i));
-        v[i] = x.x, v[i + 1] = x.y, v[i + 2] = x.z, v[i + 3] = x.w;
+      if (i < me.n) {
+        const float4 x = __ldcg(reinterpret_cast<const float4*>(row + me.first + i));
+        l[i] = x.x, l[i + 1] = x.y, l[i + 2] = x.z, l[i + 3] = x.w;
       }
   } else {
 #pragma unroll
     for (int i = 0; i < EPL; ++i)
-      if (i < n) v[i] = __ldcg(row + first + i);
+      if (i < me.n) l[i] = __ldcg(row + me.first + i);
   }
+}
+
+// The largest of the lane's keys below `under`, less `under` (modulo 2^32).  Keys are 31 bits: of a key below
+// the difference has its top bit set, of all others not.
+template <int EPL>
+__device__ __forceinline__ uint32_t below(const uint32_t (&key)[EPL], uint32_t under) {
+  uint32_t d = key[0] - under;
 #pragma unroll
-  for (int i = 0; i < EPL; ++i) v[i] = available(v[i]);
-  float top = 0.f, inv = 0.f;  // softmax over all experts: the largest logit, 1 / sum (which is the largest score)
-  if (g.softmax && !(g.by_logit && g.renorm)) {
-    top = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) top = fmaxf(top, v[i]);
-#pragma unroll
-    for (int m = 16; m >= 1; m >>= 1) top = fmaxf(top, __shfl_xor_sync(FULL, top, m));
-    if (top == -INFINITY) top = 0.f;
-    float sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-      const float e = expf(v[i] - top);
-      sum += e;
-      if (!g.by_logit && v[i] != -INFINITY) v[i] = e;
-    }
-#pragma unroll
-    for (int m = 16; m >= 1; m >>= 1) sum += __shfl_xor_sync(FULL, sum, m);
-    inv = sum > 0.f ? 1.0f / sum : 0.f;
+  for (int i = 1; i < EPL; ++i) d = __viaddmax_u32(key[i], 0u - under, d);
+  return d;
+}
+
+// How many tokens a warp does together: as many as have room for their k choices side by side in its lanes,
+// and for a group's score each in the group's lanes.
+__host__ __device__ inline int batch_of(const Gate& g, int width) {
+  int n = g.k <= 8 ? 4 : g.k <= 16 ? 2 : 1;
+  if (g.top_groups < g.groups && n > 1 << g.lanes_log) n = 1 << g.lanes_log;
+  while (n * width > 32 && n > 1) n >>= 1;
+  return n;
+}
+
+// The second look at a token whose groups are beyond doubt: those that may be among the k by their keys (the k
+// and all within `near` of the last), a lane each, sorted by scores of twice the length.  key: the lane's
+// keys, 0 where its group does not stay; blur: the relative error of 1 / sum (softmax).  Lane j < k gets the
+// j-th choice; false: more candidates than lanes, or two that the blur could exchange.
+template <int EPL, int IDX, Mode MODE>
+__device__ __forceinline__ bool choose_close(const float* row, const uint32_t (&key)[EPL], uint32_t near,
+                                             const Scale& scale, float blur, const Gate& g, int lane, int* choice) {
+  constexpr uint32_t MASK = (1u << IDX) - 1u, OUT = MODE == BY_LOGIT ? 0x007fffffu >> (IDX + 1) : 1u;
+  uint32_t last = 0x80000000u, kth = 0, mine = 0;
+  int n = 0;
+#pragma unroll 1
+  for (;; ++n) {
+    const uint32_t d = __reduce_max_sync(FULL, below(key, last));
+    const uint32_t next = d >> 31 ? last + d : 0u;
+    if (n >= g.k && (next >> IDX <= OUT || (kth >> IDX) - (next >> IDX) > near)) break;
+    if (n == 32) return false;
+    last = next;
+    if (n == g.k - 1) kth = last;
+    if (lane == n) mine = last;
   }
-  Bound err = {0.f, 0.f};
-  if (!g.by_logit) {
-    err = g.softmax ? Bound{1.5e-6f + 6e-8f * EPL, 3e-8f * inv + 1e-37f} : Bound{4e-7f, 1e-7f};
+  const int id = min(static_cast<int>(MASK - (mine & MASK)), g.E - 1);
+  const float x = lane < n ? available(__ldcg(row + id)) : -INFINITY;
+  const float bias = MODE != BY_LOGIT && g.bias && lane < n ? __ldg(g.bias + id) : 0.f;
+  if (!__all_sync(FULL, fabsf(bias) < INFINITY)) return false;
+  Pair v = {x, 0.f};
+  float off = 0.f;
+  if (MODE != BY_LOGIT && x != -INFINITY) {
+    v = MODE == SOFTMAX ? mul(exp_pair(sum(x, -scale.top)), scale.inv) : sigmoid_pair(x);
+    off = blur * v.h;
+    v = add(v, {bias, 0.f});
+  }
+  const uint64_t value = x == -INFINITY ? NOT_AVAILABLE : pair_key(v);
+  int ahead = 0;
+#pragma unroll 1
+  for (int o = 0; o < n; ++o) {
+    const uint64_t other = __shfl_sync(FULL, value, o);
+    const int e = __shfl_sync(FULL, id, o);
+    ahead += other > value || (other == value && e < id);
+  }
+  // in order: lane j takes over from the lane that has j ahead of it
+  int from = lane;
+#pragma unroll 1
+  for (int j = 0; j < n; ++j) {
+    const int o = __ffs(__ballot_sync(FULL, lane < n && ahead == j)) - 1;
+    if (lane == j) from = o;
+  }
+  *choice = __shfl_sync(FULL, id, from);
+  if (MODE != SOFTMAX || blur == 0.f) return true;
+  // neighbours (every lane takes part in every exchange)
+  const int after = __shfl_down_sync(FULL, from, 1);
+  const float h = __shfl_sync(FULL, v.h, from), h2 = __shfl_sync(FULL, v.h, after);
+  const float l = __shfl_sync(FULL, v.l, from), l2 = __shfl_sync(FULL, v.l, after);
+  const float o = __shfl_sync(FULL, off, from), o2 = __shfl_sync(FULL, off, after);
+  const float x1 = __shfl_sync(FULL, x, from), x2 = __shfl_sync(FULL, x, after);
+  const float b1 = __shfl_sync(FULL, bias, from), b2 = __shfl_sync(FULL, bias, after);
+  const bool alike = x1 == x2 && b1 == b2;
+  return !__any_sync(FULL, lane + 1 < n && x2 != -INFINITY && !alike && !((h - h2) + (l - l2) > o + o2));
+}
+
+// Tokens t .. t + BATCH - 1 (those below T) by one warp: lane i (32 / BATCH) + j ends with the j-th choice of
+// token t + i and its weight.  WHOLE: every lane has EPL experts, which start on 16 bytes.
+template <int EPL, int IDX, Mode MODE, int BATCH, bool WHOLE>
+__device__ __forceinline__ void warp_gate(const float* logits, int t, int T, const Units<EPL, IDX, MODE>& u, const Gate& g,
+                                          const Lane& me, int lane, int* id_out, float* w_out) {
+  constexpr uint32_t MASK = (1u << IDX) - 1u;
+  constexpr int SEG = 32 / BATCH;
+  // m of experts that are not available, and of none that is
+  constexpr uint32_t OUT = MODE == BY_LOGIT ? 0x007fffffu >> (IDX + 1) : 1u;
+  const int ti = lane / SEG, tj = lane % SEG;  // whose choice this lane ends with
+  uint32_t key[BATCH][EPL];
+  float top = 0.f, inv = 0.f;  // this lane's token's: softmax's largest logit, 1 / sum (the largest score)
+  uint32_t near[BATCH];
+  uint32_t c1 = 0, c2 = 0;  // the two largest keys of this lane's group, of token (lane modulo BATCH)
+  const bool drop = g.top_groups < g.groups;
+  {
+    float l[BATCH][EPL];
 #pragma unroll
-    for (int i = 0; i < EPL; ++i)
-      if (v[i] != -INFINITY) {
-        const float s = g.softmax ? v[i] * inv : fast_sigmoid(v[i]);
-        v[i] = g.bias ? fmaxf(s + __ldg(g.bias + first + i), -INFINITY) : s;
+    for (int b = 0; b < BATCH; ++b) load_logits<EPL, WHOLE>(logits + static_cast<size_t>(min(t + b, T - 1)) * g.E, me, l[b]);
+#pragma unroll
+    for (int b = 0; b < BATCH; ++b) {
+      float total = 0.f, e[MODE == SOFTMAX ? EPL : 1];
+      if (MODE == SOFTMAX || (MODE == BY_LOGIT && g.softmax && !g.renorm)) {
+        float most = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) most = fmaxf(most, available(l[b][i]));
+        most = key_float(__reduce_max_sync(FULL, float_key(most)));
+        if (most == -INFINITY) most = 0.f;
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) {
+          const float x = expf(available(l[b][i]) - most);
+          sum += x;
+          if (MODE == SOFTMAX) e[MODE == SOFTMAX ? i : 0] = x;
+        }
+#pragma unroll
+        for (int m = 16; m >= 1; m >>= 1) sum += __shfl_xor_sync(FULL, sum, m);
+        total = sum > 0.f ? 1.0f / sum : 0.f;
+        if (ti == b) {
+          top = most;
+          inv = total;
+        }
       }
-  }
-  bool sure = true;  // false: the choice may hang on a rounding
-  // ---- groups
-  bool stays = true;
-  if (g.top_groups < g.groups) {
-    float c1 = -INFINITY, c2 = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-      c2 = fmaxf(c2, fminf(c1, v[i]));
-      c1 = fmaxf(c1, v[i]);
-    }
-    for (int m = 1; m < L; m <<= 1) {
-      const float o1 = __shfl_xor_sync(FULL, c1, m), o2 = __shfl_xor_sync(FULL, c2, m);
-      c2 = fmaxf(fminf(c1, o1), fmaxf(c2, o2));
-      c1 = fmaxf(c1, o1);
-    }
-    const float mine = g.top2 && c2 != -INFINITY ? c1 + c2 : c1;
-    int ahead = 0;
-    for (int o = 0; o < g.groups; ++o) {
-      const float other = __shfl_sync(FULL, mine, o << g.lanes_log);
-      ahead += other > mine || (other == mine && o < group);
-    }
-    stays = ahead < g.top_groups && group < g.groups;
-    if (!g.by_logit) {
-      const uint32_t key = float_key(mine);
-      const float last = key_float(__reduce_min_sync(FULL, stays ? key : 0xffffffffu));
-      const float next = key_float(__reduce_max_sync(FULL, stays || group >= g.groups ? 0u : key));
-      const float most = g.softmax ? inv : 1.0f;
-      const float a1 = c1 == -INFINITY ? 0.f : fabsf(c1), a2 = c2 == -INFINITY ? 0.f : fabsf(c2);
-      const float d = 4.f * (err.rel * most + err.abs) + (fabsf(last) + fabsf(next) + 2.f * fmaxf(a1, a2)) * 2.4e-7f;
-      // (a group without an available expert is behind all others for sure)
-      if (next != -INFINITY && !(last - next > d)) sure = false;
-      sure = __all_sync(FULL, sure);
-    }
-  }
-  uint32_t key[EPL];
-#pragma unroll
-  for (int i = 0; i < EPL; ++i) key[i] = stays && i < n ? float_key(v[i]) : 0u;
-  // ---- the k largest: lower lanes have lower experts
-  uint32_t best = 0, my_key = 0;
-  int id = 0;
-#pragma unroll
-  for (int i = 0; i < EPL; ++i) best = max(best, key[i]);
-  for (int j = 0; j < g.k; ++j) {
-    const uint32_t most = __reduce_max_sync(FULL, best);
-    const int win = __ffs(__ballot_sync(FULL, best == most)) - 1;
-    int at = 0;
-    if (lane == win) {
-      bool done = false;
-      best = 0;
+      // Keys.  `near`: the largest difference of two m that errors may account for.  Each is off by its
+      // score's error and 1.5 (b - least, base, m).  Sigmoid: the fast exponential is off by
+      // (2 + 1.16 |l|) 2^-23, which enters s times 1 - s (s (1 - s) <= 1/4, s (1 - s) |l| <= 0.224), the sum by
+      // 2^-24, the reciprocal by 2^-23: below 5e-7.  Softmax: s times 1.5e-6 and 2^-24 per addition (expf
+      // 2^-22, its argument 2^-24 (top - l), on average at most ln 1024 2^-24, sum, reciprocal, product), and
+      // 2^-24 s (top - l) <= 2^-24 0.37 / sum.
+      near[b] = 0;
+      if (MODE == SIGMOID) near[b] = static_cast<uint32_t>(1e-6f * u.a) + 5u;
+      if (MODE == SOFTMAX) near[b] = static_cast<uint32_t>((3.1e-6f + 1.2e-7f * EPL) * total * u.a) + 5u;
 #pragma unroll
       for (int i = 0; i < EPL; ++i) {
-        if (!done && key[i] == most) {
-          done = true;
-          key[i] = 0;
-          at = i;
+        const uint32_t index = MASK - static_cast<uint32_t>(me.first + i);
+        uint32_t& x = key[b][i];
+        if (MODE == BY_LOGIT) {
+          x = (float_key(available(l[b][i])) >> (IDX + 1) << IDX) | index;
+        } else {
+          const float s = MODE == SOFTMAX ? e[MODE == SOFTMAX ? i : 0] * total
+                                          : fast_rcp(1.0f + fast_exp2(l[b][i] * -1.44269504f));
+          float base;
+          if (u.KEEP)
+            base = u.base[u.KEEP ? i : 0];
+          else
+            base = u.at(g.bias && u.a > 0.f && i < me.n ? __ldg(g.bias + me.first + i) : u.least);
+          x = (__float_as_uint(fmaf(s, u.a, base)) << IDX) + index;
+          if (!(l[b][i] > -INFINITY)) x = (OUT << IDX) + index;
         }
-        best = max(best, key[i]);
+        if (!WHOLE && i >= me.n) x = 0;
       }
-    }
-    const int e = __shfl_sync(FULL, first + at, win);
-    if (lane == j) {
-      id = e;
-      my_key = most;
+      if (drop) {
+        uint32_t a1 = 0, a2 = 0;
+#pragma unroll
+        for (int i = 0; i < EPL; i += 2) {
+          const uint32_t hi = EPL == 1 ? key[b][i] : max(key[b][i], key[b][(i + 1) % EPL]);
+          const uint32_t lo = EPL == 1 ? 0u : min(key[b][i], key[b][(i + 1) % EPL]);
+          a2 = __vimax3_u32(min(a1, hi), a2, lo);
+          a1 = max(a1, hi);
+        }
+        for (int m = 1; m < 1 << g.lanes_log; m <<= 1) {
+          const uint32_t o1 = __shfl_xor_sync(FULL, a1, m), o2 = __shfl_xor_sync(FULL, a2, m);
+          a2 = __vimax3_u32(min(a1, o1), a2, o2);
+          a1 = max(a1, o1);
+        }
+        if (BATCH == 1 || (lane & (BATCH - 1)) == b) {
+          c1 = a1 >> IDX;
+          c2 = a2 >> IDX;
+        }
+      }
     }
   }
-  id = min(id, g.E - 1);
-  // ---- is the choice beyond doubt?
-  if (!g.by_logit) {
-    float c = key_float(my_key);
-    const float l = available(__ldcg(row + id)), b = g.bias ? __ldg(g.bias + id) : 0.f;
-    const float s = l == -INFINITY ? 0.f : g.softmax ? expf(l - top) * inv : fast_sigmoid(l);
-    const float dc = err.rel * s + err.abs + fabsf(c) * 1.2e-7f;
-    const float c2 = __shfl_down_sync(FULL, c, 1), l2 = __shfl_down_sync(FULL, l, 1), b2 = __shfl_down_sync(FULL, b, 1),
-                dc2 = __shfl_down_sync(FULL, dc, 1);
-    if (lane + 1 < g.k && c2 != -INFINITY && !(c - c2 > dc + dc2) && !(l == l2 && b == b2)) sure = false;
-    // the last one chosen and the others
-    const float ck = __shfl_sync(FULL, c, g.k - 1), dk = __shfl_sync(FULL, dc, g.k - 1);
-    const float most = g.softmax ? inv : 1.0f;
-    const float cu = key_float(best);  // this lane's best other one
-    if (__any_sync(FULL, best > 0x007fffffu && !(ck - cu > dk + err.rel * most + err.abs + fabsf(cu) * 1.2e-7f))) {
-      const float lk = __shfl_sync(FULL, l, g.k - 1), bk = __shfl_sync(FULL, b, g.k - 1);
-#pragma unroll 1
-      for (int i = 0; i < n; ++i) {
-        const int e = first + i;
-        const float lu = available(__ldcg(row + e)), bu = g.bias ? __ldg(g.bias + e) : 0.f;
-        bool out = lu == -INFINITY || !stays;
-        const float su = g.softmax ? expf(lu - top) * inv : fast_sigmoid(lu);
-        const float vu = fmaxf(su + bu, -INFINITY);
-        // (chosen ones are past the last one, or the last one itself)
-        out |= vu == -INFINITY || (lu == lk && bu == bk) || vu > ck;
-        if (!out && !(ck - vu > dk + err.rel * su + err.abs + fabsf(vu) * 1.2e-7f)) sure = false;
+  // tokens whose choice may hang on a rounding, a bit each: that of the groups, or of the experts in them
+  uint32_t unsure = 0, close = 0;
+  if (MODE != BY_LOGIT && !(u.a > 0.f)) unsure = (1u << BATCH) - 1u;
+  // ---- groups: lane's own, of token (lane modulo BATCH)
+  uint32_t stays = ~0u;
+  if (drop) {
+    // The score in units, from 1 on (0: none available), and the group's index.  A sum of two counts from
+    // twice the least bias, a lone value from that once.
+    uint32_t worth = 0;
+    bool doubt = false;
+    if (c1 > OUT) {
+      worth = c1;
+      if (MODE != BY_LOGIT && g.top2) {
+        const float from = fminf(fmaxf(rintf(u.least * u.a), -33554432.f), 33554432.f);
+        const int up = max(static_cast<int>(from), 0);
+        worth = static_cast<uint32_t>(c2 > OUT ? static_cast<int>(c1 + c2) - 3 + up
+                                               : max(static_cast<int>(c1) - 1 + up - static_cast<int>(from), 1));
+        doubt = c2 <= OUT && fabsf(from) > 16777216.f;
       }
     }
-    if (!__all_sync(FULL, sure)) id = choose_exact(row, g, lane);
+    const uint32_t mine = me.group < g.groups ? (worth + 1u) << 5 | static_cast<uint32_t>(31 - me.group) : 0u;
+    // places of the groups, and the best score of those behind this one
+    int ahead = 0;
+    uint32_t behind = 0;
+    for (int m = 1; m << g.lanes_log < 32; ++m) {
+      const uint32_t o = __shfl_xor_sync(FULL, mine, m << g.lanes_log);
+      ahead += o > mine;
+      behind = max(behind, o < mine ? o : 0u);
+    }
+    // (a group without an available expert is behind all others for sure)
+    uint32_t slack = near[0];
+    if (MODE == SOFTMAX) {
+#pragma unroll
+      for (int b = 1; b < BATCH; ++b) slack = (lane & (BATCH - 1)) == b ? near[b] : slack;
+    }
+    if (ahead == g.top_groups - 1 && behind >> 5 > 1u && (mine >> 5) - (behind >> 5) <= (g.top2 ? 2u * slack + 4u : slack)) doubt = true;
+    const uint32_t in = __ballot_sync(FULL, ahead < g.top_groups && me.group < g.groups);
+    const uint32_t un = __ballot_sync(FULL, doubt);
+    stays = 0;
+#pragma unroll
+    for (int b = 0; b < BATCH; ++b) {
+      stays |= (in >> ((me.group << g.lanes_log) + b) & 1u) << b;
+      uint32_t of_b = 0;  // the lanes that speak for token b
+#pragma unroll
+      for (int i = b; i < 32; i += BATCH) of_b |= 1u << i;
+      if (un & of_b) unsure |= 1u << b;
+    }
+  }
+  // ---- the k largest of each token
+  uint32_t chosen = 0, others = 0;
+#pragma unroll
+  for (int b = 0; b < BATCH; ++b) {
+    const bool in = stays >> b & 1u;
+    uint32_t last = 0x80000000u;
+    for (int j = 0; j < g.k; ++j) {
+      const uint32_t d = below(key[b], last);
+      last += __reduce_max_sync(FULL, in ? d : 0u);
+      if (lane == b * SEG + j) chosen = last;
+    }
+    const uint32_t d = below(key[b], last), most = __reduce_max_sync(FULL, in ? d : 0u);
+    const uint32_t next = most >> 31 ? last + most : 0u;
+    // every other expert that may be ahead of the last one chosen has to tie with it in logit and bias
+    if (next >> IDX > OUT && (last >> IDX) - (next >> IDX) <= near[b]) {
+      const float* row = logits + static_cast<size_t>(min(t + b, T - 1)) * g.E;
+      const int idk = min(static_cast<int>(MASK - (last & MASK)), g.E - 1);
+      const float xk = available(__ldcg(row + idk)), bk = g.bias ? __ldg(g.bias + idk) : 0.f;
+      bool alike = true;
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) {
+        const uint32_t x = key[b][i];
+        if (!in || x >= last || x >> IDX <= OUT || (last >> IDX) - (x >> IDX) > near[b]) continue;
+        const float xi = available(__ldcg(row + me.first + i)), bi = g.bias ? __ldg(g.bias + me.first + i) : 0.f;
+        if (!(xi == xk && bi == bk)) alike = false;
+      }
+      if (!__all_sync(FULL, alike)) close |= 1u << b;
+    }
+    if (ti == b) others = near[b];
+  }
+  int id = min(static_cast<int>(MASK - (chosen & MASK)), g.E - 1);
+  const float* row = logits + static_cast<size_t>(min(t + ti, T - 1)) * g.E;
+  float x = tj < g.k ? available(__ldcg(row + id)) : -INFINITY;
+  // ---- neighbours in the choice
+  {
+    const uint32_t m = chosen >> IDX, m2 = __shfl_down_sync(FULL, m, 1);
+    const bool near_by = tj + 1 < g.k && m2 > OUT && m - m2 <= others;
+    if (__any_sync(FULL, near_by)) {
+      const float bias = g.bias && tj < g.k ? __ldg(g.bias + id) : 0.f;
+      const float x2 = __shfl_down_sync(FULL, x, 1), b2 = __shfl_down_sync(FULL, bias, 1);
+      const uint32_t un = __ballot_sync(FULL, near_by && !(x == x2 && bias == b2));
+#pragma unroll
+      for (int b = 0; b < BATCH; ++b)
+        if (un >> (b * SEG) & (SEG == 32 ? FULL : (1u << (SEG & 31)) - 1u)) close |= 1u << b;
+    }
+  }
+  const uint32_t here = T - t < BATCH ? (1u << (T - t)) - 1u : (1u << BATCH) - 1u;
+  unsure &= here;
+  close &= here & ~unsure;
+  if (unsure | close) {
+#pragma unroll 1
+    for (uint32_t left = unsure | close; left; left &= left - 1u) {
+      const int b = __ffs(left) - 1;
+      const float* at = logits + static_cast<size_t>(t + b) * g.E;
+      uint32_t own[EPL], slack = 0;
+      bool in = true;
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) own[i] = 0;
+#pragma unroll
+      for (int o = 0; o < BATCH; ++o)
+        if (o == b) {
+          slack = near[o];
+          in = stays >> o & 1u;
+#pragma unroll
+          for (int i = 0; i < EPL; ++i) own[i] = key[o][i];
+        }
+      // softmax: with 1 / sum as it is first, unless the groups need it exact anyway
+      Scale scale = {__shfl_sync(FULL, top, b * SEG), {__shfl_sync(FULL, inv, b * SEG), 0.f}};
+      float blur = MODE == SOFTMAX ? 1.5e-6f + 6e-8f * EPL : 0.f;
+      bool groups = unsure >> b & 1u, done = false;
+      int e = 0;
+#pragma unroll 1
+      for (int go = 0; go < 2 && !done; ++go) {
+        if (MODE == SOFTMAX && (groups || go == 1)) {
+          scale = softmax_scale(at, me);
+          blur = 0.f;
+        }
+        if (groups && drop) in = group_stays<MODE>(at, me, g, scale);
+        groups = false;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) own[i] = in ? own[i] : 0u;
+        done = choose_close<EPL, IDX, MODE>(at, own, slack, scale, blur, g, lane, &e);
+        if (blur == 0.f) break;
+      }
+      if (!done) e = choose_slowly<MODE>(at, me, in, g, scale, lane);
+      const int mine = __shfl_sync(FULL, e, tj);
+      if (ti == b) id = min(max(mine, 0), g.E - 1);
+    }
+    if (tj < g.k) x = available(__ldcg(row + id));
   }
   // ---- weights
-  const float l = available(__ldcg(row + id));
   float z = 0.f;
-  if (lane < g.k && l != -INFINITY) {
-    if (!g.softmax)
-      z = 1.0f / (1.0f + expf(-l));
-    else if (!g.renorm)
-      z = expf(l - top) * inv;
-  }
   if (g.softmax && g.renorm) {
-    // exp(l - the chosen ones' largest): the difference carried exactly (two-sum)
-    float most = lane < g.k ? l : -INFINITY;
+    // exp(x - the chosen ones' largest): the difference carried exactly (two-sum)
+    float most = x;
 #pragma unroll
-    for (int m = 16; m >= 1; m >>= 1) most = fmaxf(most, __shfl_xor_sync(FULL, most, m));
-    if (lane < g.k && l != -INFINITY) {
-      const float hi = l - most, bb = hi - l, lo = (l - (hi - bb)) + (-most - bb);
+    for (int m = SEG / 2; m >= 1; m >>= 1) most = fmaxf(most, __shfl_xor_sync(FULL, most, m));
+    if (x != -INFINITY) {
+      const float hi = x - most, bb = hi - x, lo = (x - (hi - bb)) + (-most - bb);
       z = expf(hi) * (1.0f + lo);
     }
+  } else if (x != -INFINITY) {
+    z = g.softmax ? expf(x - top) * inv : 1.0f / (1.0f + expf(-x));
   }
   if (g.renorm) {
     float sum = z;
 #pragma unroll
-    for (int m = 16; m >= 1; m >>= 1) sum += __shfl_xor_sync(FULL, sum, m);
+    for (int m = SEG / 2; m >= 1; m >>= 1) sum += __shfl_xor_sync(FULL, sum, m);
     z = sum > 0.f ? z / sum : 0.f;
   }
   *id_out = id;

@@ -225,7 +225,7 @@ int moe_norm_router(const uint16_t* x, const uint16_t* w_router, int T, int H, i
  * ("Perplexity Open Sources Lily", Technical Details, Model bullet names no
  * other).  A gate describes the other ways that mixture-of-experts models
  * choose.  For a token's logits l:
- *   s_e = sigmoid(l_e), or exp(l_e) / sum of all exp(l_i)
+ *   s_e = sigmoid(l_e), or exp(l_e) / sum of all exp(l_i); below 2^-126 it is 0
  *   v_e = s_e + bias_e          (the bias, which balances the experts' load,
  *                                takes part in the choice alone)
  *   groups: the experts in order form `groups` groups of E / groups; a group's
@@ -234,9 +234,10 @@ int moe_norm_router(const uint16_t* x, const uint16_t* w_router, int T, int H, i
  *   chosen: the k largest v_e of the groups that stay, in descending order,
  *           equal ones by index
  *   w_j = scale * s_j / (sum of the chosen s_i, if renorm, else 1); 0 where
- *         that sum is 0 (scores below 2^-126 count as 0)
- * The choice is that of scores in 64 bits: a token whose choice a rounding in
- * 32 bits could change is done again in 64.  Without a bias, and with groups
+ *         that sum is 0
+ * The choice is that of scores that are off by less than 2^-40: a token whose
+ * choice a rounding in 32 bits could change is done again with scores of twice
+ * the length.  Without a bias, and with groups
  * (if any) scored by their largest, the logits themselves are compared.  An expert whose logit is -inf or NaN is not
  * available: it is chosen only where fewer than k others are left (then by
  * index), with weight 0; a group is scored by its available experts, one

@@ -6,7 +6,7 @@ import numpy as np
 
 
 def scores(logits, score):
-    """logits float [E] -> (scores float64 [E], which are available)."""
+    """logits float [E] -> (scores float64 [E], those below 2^-126 as 0, which are available)."""
     l = np.asarray(logits, np.float64)
     here = l > -np.inf  # not NaN either
     l = np.where(here, np.minimum(l, np.finfo(np.float32).max), -np.inf)
@@ -15,8 +15,10 @@ def scores(logits, score):
     with np.errstate(over="ignore"):
         if score == "softmax":
             e = np.exp(l - l.max())
-            return e / e.sum(), here
-        return 1.0 / (1.0 + np.exp(-l)), here
+            s = e / e.sum()
+        else:
+            s = 1.0 / (1.0 + np.exp(-l))
+    return np.where(s < 2.0 ** -126, 0.0, s), here
 
 
 def choose_token(logits, k, score="softmax", bias=None, groups=1, top_groups=None, group_score="top2", renorm=True,
@@ -39,7 +41,7 @@ def choose_token(logits, k, score="softmax", bias=None, groups=1, top_groups=Non
         allowed = np.isin(np.arange(E) // per, stay)
     order = sorted((e for e in range(E) if allowed[e]), key=lambda e: (not here[e], -v[e] if here[e] else 0.0, e))
     ids = np.array(order[:k])
-    w = np.where(here[ids] & (s[ids] >= 2.0 ** -126), s[ids], 0.0)
+    w = np.where(here[ids], s[ids], 0.0)
     if renorm:
         w = w / w.sum() if w.sum() > 0 else np.zeros(k)
     return ids, w * scale
