@@ -12,9 +12,10 @@ using gate_dev::Gate;
 using gate_dev::Mode;
 
 constexpr int GATE_WARPS = 8;
+constexpr int GATE_BATCH_ROWS = 12;  // per token of a warp, this many tokens an SM
 
 template <int EPL, int IDX, Mode MODE, int BATCH, bool WHOLE>
-__global__ void __launch_bounds__(32 * GATE_WARPS) gate_kernel(const float* logits, int T,
+__global__ void __launch_bounds__(32 * GATE_WARPS, BATCH == 4 ? 3 : 1) gate_kernel(const float* logits, int T,
                                                                const __grid_constant__ Gate g, int32_t* ids, float* w) {
   constexpr int SEG = 32 / BATCH;
   const int lane = threadIdx.x & 31;
@@ -48,8 +49,8 @@ cudaError_t launch(const float* logits, int T, const Gate& g, int32_t* ids, floa
 
 template <int EPL, int IDX, Mode MODE, bool WHOLE>
 cudaError_t launch_batch(const float* logits, int T, const Gate& g, int32_t* ids, float* w, cudaStream_t s) {
-  // with few tokens, one per warp: they are done sooner
-  const int batch = T <= GATE_WARPS * num_sms() ? 1 : gate_dev::batch_of(g, EPL);
+  int batch = gate_dev::batch_of(g, EPL);
+  while (batch > 1 && T < batch * GATE_BATCH_ROWS * num_sms()) batch >>= 1;
   if (EPL <= 8 && batch == 4) return launch<EPL, IDX, MODE, EPL <= 8 ? 4 : 1, WHOLE>(logits, T, g, ids, w, s);
   if (EPL <= 16 && batch == 2) return launch<EPL, IDX, MODE, EPL <= 16 ? 2 : 1, WHOLE>(logits, T, g, ids, w, s);
   return launch<EPL, IDX, MODE, 1, WHOLE>(logits, T, g, ids, w, s);

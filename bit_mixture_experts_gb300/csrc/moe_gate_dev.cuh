@@ -312,13 +312,13 @@ __device__ __forceinline__ void load_logits(const float* row, const Lane& me, fl
   }
 }
 
-// The largest of the lane's keys below `under`, less `under` (modulo 2^32).  Keys are 31 bits: of a key below
-// the difference has its top bit set, of all others not.
+// The largest of the lane's keys below `under`, less `under` (modulo 2^32); minus: 0 - under.  Keys are 31 bits:
+// of a key below the difference has its top bit set, of all others not.
 template <int EPL>
-__device__ __forceinline__ uint32_t below(const uint32_t (&key)[EPL], uint32_t under) {
-  uint32_t d = key[0] - under;
+__device__ __forceinline__ uint32_t below(const uint32_t (&key)[EPL], uint32_t minus) {
+  uint32_t d = key[0] + minus;
 #pragma unroll
-  for (int i = 1; i < EPL; ++i) d = __viaddmax_u32(key[i], 0u - under, d);
+  for (int i = 1; i < EPL; ++i) d = __viaddmax_u32(key[i], minus, d);
   return d;
 }
 
@@ -343,7 +343,7 @@ __device__ __forceinline__ bool choose_close(const float* row, const uint32_t (&
   int n = 0;
 #pragma unroll 1
   for (;; ++n) {
-    const uint32_t d = __reduce_max_sync(FULL, below(key, last));
+    const uint32_t d = __reduce_max_sync(FULL, below(key, 0u - last));
     const uint32_t next = d >> 31 ? last + d : 0u;
     if (n >= g.k && (next >> IDX <= OUT || (kth >> IDX) - (next >> IDX) > near)) break;
     if (n == 32) return false;
@@ -405,6 +405,9 @@ __device__ __forceinline__ void warp_gate(const float* logits, int t, int T, con
   uint32_t near[BATCH];
   uint32_t c1 = 0, c2 = 0;  // the two largest keys of this lane's group, of token (lane modulo BATCH)
   const bool drop = g.top_groups < g.groups;
+  uint32_t places[(EPL + 3) / 4];  // 255 less the experts' indices, a byte each
+#pragma unroll
+  for (int i = 0; i < (EPL + 3) / 4; ++i) places[i] = (MASK - static_cast<uint32_t>(me.first + 4 * i)) * 0x01010101u - 0x03020100u;
   {
     float l[BATCH][EPL];
 #pragma unroll
@@ -442,6 +445,14 @@ __device__ __forceinline__ void warp_gate(const float* logits, int t, int T, con
       near[b] = 0;
       if (MODE == SIGMOID) near[b] = static_cast<uint32_t>(1e-6f * u.a) + 5u;
       if (MODE == SOFTMAX) near[b] = static_cast<uint32_t>((3.1e-6f + 1.2e-7f * EPL) * total * u.a) + 5u;
+      // (0 x: NaN of what is not finite; a comparison per expert would cost twice as much)
+      bool odd = true;
+      if (WHOLE && MODE != BY_LOGIT) {
+        float zero = 0.f;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) zero = fmaf(l[b][i], 0.f, zero);
+        odd = __any_sync(FULL, zero != 0.f);
+      }
 #pragma unroll
       for (int i = 0; i < EPL; ++i) {
         const uint32_t index = MASK - static_cast<uint32_t>(me.first + i);
@@ -456,10 +467,18 @@ __device__ __forceinline__ void warp_gate(const float* logits, int t, int T, con
             base = u.base[u.KEEP ? i : 0];
           else
             base = u.at(g.bias && u.a > 0.f && i < me.n ? __ldg(g.bias + me.first + i) : u.least);
-          x = (__float_as_uint(fmaf(s, u.a, base)) << IDX) + index;
-          if (!(l[b][i] > -INFINITY)) x = (OUT << IDX) + index;
+          const uint32_t m = __float_as_uint(fmaf(s, u.a, base));
+          if (IDX == 8)  // the integer's three bytes and the index's
+            x = __byte_perm(m, places[i / 4], 0x2104 + i % 4);
+          else
+            x = (m << IDX) + index;
         }
         if (!WHOLE && i >= me.n) x = 0;
+      }
+      if (MODE != BY_LOGIT && odd) {
+#pragma unroll
+        for (int i = 0; i < EPL; ++i)
+          if (!(l[b][i] > -INFINITY) && (WHOLE || i < me.n)) key[b][i] = (OUT << IDX) + MASK - static_cast<uint32_t>(me.first + i);
       }
       if (drop) {
         uint32_t a1 = 0, a2 = 0;
@@ -530,18 +549,30 @@ __device__ __forceinline__ void warp_gate(const float* logits, int t, int T, con
       if (un & of_b) unsure |= 1u << b;
     }
   }
-  // ---- the k largest of each token
+  // ---- the k largest of each token (side by side: a round is a chain of latencies)
   uint32_t chosen = 0, others = 0;
+  uint32_t minus[BATCH], own_minus[BATCH];  // 0 less the last one chosen; for a group that does not stay 0: no key is below
+#pragma unroll
+  for (int b = 0; b < BATCH; ++b) {
+    minus[b] = 0x80000000u;
+    own_minus[b] = stays >> b & 1u ? 0x80000000u : 0u;
+  }
+#pragma unroll 1
+  for (int j = 0; j < g.k; ++j) {
+    uint32_t mine = 0;
+#pragma unroll
+    for (int b = 0; b < BATCH; ++b) {
+      const uint32_t r = __reduce_max_sync(FULL, below(key[b], own_minus[b]));
+      minus[b] -= r;
+      own_minus[b] -= r * (stays >> b & 1u);
+      if (ti == b) mine = minus[b];
+    }
+    if (tj == j) chosen = 0u - mine;
+  }
 #pragma unroll
   for (int b = 0; b < BATCH; ++b) {
     const bool in = stays >> b & 1u;
-    uint32_t last = 0x80000000u;
-    for (int j = 0; j < g.k; ++j) {
-      const uint32_t d = below(key[b], last);
-      last += __reduce_max_sync(FULL, in ? d : 0u);
-      if (lane == b * SEG + j) chosen = last;
-    }
-    const uint32_t d = below(key[b], last), most = __reduce_max_sync(FULL, in ? d : 0u);
+    const uint32_t most = __reduce_max_sync(FULL, below(key[b], own_minus[b])), last = 0u - minus[b];
     const uint32_t next = most >> 31 ? last + most : 0u;
     // every other expert that may be ahead of the last one chosen has to tie with it in logit and bias
     if (next >> IDX > OUT && (last >> IDX) - (next >> IDX) <= near[b]) {
