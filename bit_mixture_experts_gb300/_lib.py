@@ -318,12 +318,13 @@ def moe_route_gated(logits, T, E, k, gate: Gate, block_n, topk_ids, topk_w, coun
 
 def moe_residual_norm(y, y_stride, T, H, residual: Residual, stream=None):
     """A block's residual addition between the norm of its output and the next block's norm."""
-    _call("moe_residual_norm", _ptr(y), y_stride, T, H, residual, _stream(stream))
+    _call("moe_residual_norm", None if y is None else y.data_ptr(), y_stride, T, H, residual, _stream(stream))
 
 
 def moe_combine_residual_norm(y, inv_perm, topk_w, T, H, k, residual: Residual, stream=None):
     """The same where y is the weighted sum of each token's expert rows (bf16 [T k + T, H])."""
-    _call("moe_combine_residual_norm", _ptr(y), _ptr(inv_perm), _ptr(topk_w), T, H, k, residual, _stream(stream))
+    _call("moe_combine_residual_norm", y.data_ptr(), inv_perm.data_ptr(), topk_w.data_ptr(), T, H, k, residual,
+          _stream(stream))
 
 
 def moe_layer_forward_gated(x, logits, gate, out, residual, T, H, F, E, k, block_n, impl, weights: Weights,

@@ -1,20 +1,24 @@
 """A decoder block over the paged key/value cache: attention, then the W4 mixture-of-experts layer.
 
-    python -m bit_mixture_experts_gb300.block [--fmt e4m3] [--prompts 300,45] [--chunk 128] [--steps 8]
+    python -m bit_mixture_experts_gb300.block [--fmt e4m3] [--prompts 300,45] [--chunk 128] [--steps 8] [--gated]
 
 The command serves a ragged batch as a server would: the prompts go through the block in chunks, all
 sequences' chunks of a step packed into one batch; then one token per sequence and step.  It needs a GPU and
 is run from the repository root (the synthetic weights come from `workloads`).  PyTorch does the block's two
-dense bf16 projections and the residual additions; norms, cache, attention, router and experts are
-libmoe_w4.so's kernels.  There is no positional encoding.
+dense bf16 projections and, in a block without `norms`, the residual additions; norms, cache, attention,
+router and experts are libmoe_w4.so's kernels.  There is no positional encoding.  With --gated the experts are
+chosen by sigmoid scores with a bias in groups, and the block has norms with gains before and after its
+attention and its experts, a gate per channel and a residual stream in 32 bits.
 """
 from __future__ import annotations
 
 import argparse
 
 from . import _lib
+from .gate import ExpertGate
 from .kv import PagedKVCache
 from .layer import MoELayerW4, _dev
+from .residual import ResidualNorm
 
 
 class DecoderBlockW4:
@@ -22,9 +26,13 @@ class DecoderBlockW4:
 
     w_qkv is bf16 [(q_heads + 2 * cache.heads) * d, H] (all query heads, then keys, then values), w_o bf16
     [H, q_heads * d], w_router bf16 [E, H], `moe` a MoELayerW4 and `cache` a PagedKVCache.
+
+    `norms`: three ResidualNorm for a block with gains, post-norms, gates and scales of its own: of the block's input,
+    around the addition of the attention's output (its n is what router and experts take), and around that of the
+    experts' (its n is what the next block's attention takes).  `gates`: their gates' values per channel, or None.
     """
 
-    def __init__(self, w_qkv, w_o, w_router, moe: MoELayerW4, cache: PagedKVCache):
+    def __init__(self, w_qkv, w_o, w_router, moe: MoELayerW4, cache: PagedKVCache, norms=None, gates=(None, None)):
         self.q_heads = w_o.shape[1] // cache.d
         want = ((self.q_heads + 2 * cache.heads) * cache.d, moe.H)
         if tuple(w_qkv.shape) != want or w_o.shape[0] != moe.H or tuple(w_router.shape) != (moe.E, moe.H):
@@ -34,20 +42,24 @@ class DecoderBlockW4:
         if w_o.shape[1] % cache.d or self.q_heads % cache.heads:
             raise ValueError(f"w_o's {w_o.shape[1]} columns must be q_heads * {cache.d}, q_heads a multiple of the cache's "
                              f"{cache.heads} heads")
+        if norms is not None and len(norms) != 3:
+            raise ValueError(f"three norms are needed, got {len(norms)}")
+        self.norms, self.gates = norms, gates
         self.w_qkv, self.w_o, self.w_router, self.moe, self.cache = w_qkv, w_o, w_router, moe, cache
 
-    def project(self, x):
-        """Queries, keys and values of the normed x: slices of one [T, q_heads + 2 heads, d] tensor, which the
-        cache and the attention read where they are."""
+    def project(self, x, xn=None):
+        """Queries, keys and values of the normed x (xn, if it is known): slices of one [T, q_heads + 2 heads, d]
+        tensor, which the cache and the attention read where they are."""
         import torch
-        xn = torch.empty_like(x)
-        _lib.moe_rms_norm(x, xn)
+        if xn is None:
+            xn = torch.empty_like(x)
+            _lib.moe_rms_norm(x, xn)
         hq, hkv = self.q_heads, self.cache.heads
         return (xn @ self.w_qkv.T).view(x.shape[0], hq + 2 * hkv, self.cache.d).split((hq, hkv, hkv), dim=1)
 
-    def attend(self, x, batch):
+    def attend(self, x, batch, xn=None):
         """The new tokens' attention output, bf16 [T, q_heads, d]; their keys and values enter the cache."""
-        q, k, v = self.project(x)
+        q, k, v = self.project(x, xn)
         self.cache.append(k, v, batch)
         return self.cache.attention(q, batch)
 
@@ -67,13 +79,31 @@ class DecoderBlockW4:
         return self.moe.forward(xn, logits)
 
     def forward(self, x, batch):
-        """x bf16 [T, H], the new tokens of `batch`'s sequences (cache.batch) -> bf16 [T, H]."""
+        """x bf16 [T, H], the new tokens of `batch`'s sequences (cache.batch) -> bf16 [T, H].  With `norms` the residual
+        stream may also be float32; the result then is too."""
+        if self.norms is not None:
+            return self.forward_stream(x, self.norms[0].norm(x), batch)[0]
         x = x + self.attend(x, batch).view(x.shape[0], -1) @ self.w_o.T
         return x + self.experts(x)
 
+    def forward_stream(self, x, xn, batch):
+        """One block of a stack with `norms`: the residual stream x (bf16 or float32 [T, H]) and its norm xn (bf16) ->
+        both after the block; the next block's forward_stream takes them."""
+        import torch
+        T, E, k = x.shape[0], self.moe.E, self.moe.k
+        _, around_attention, around_experts = self.norms
+        y = self.attend(x, batch, xn).view(T, -1) @ self.w_o.T
+        x, xn = around_attention.add(x, y, self.gates[0])
+        logits = torch.empty((T, E), dtype=torch.float32, device=x.device)
+        ids = torch.empty((T, k), dtype=torch.int32, device=x.device)
+        _lib.moe_router(xn, self.w_router, k, logits, ids, torch.empty((T, k), dtype=torch.float32, device=x.device))
+        return self.moe.forward_residual(xn, logits, x, around_experts, self.gates[1])
 
-def synthetic(shape, q_heads=16, kv_heads=2, d=128, fmt="bf16", num_pages=256, page_size=64, seed=0, device="cuda"):
-    """A block of random weights: experts and router from `workloads`, projections of unit-variance outputs."""
+
+def synthetic(shape, q_heads=16, kv_heads=2, d=128, fmt="bf16", num_pages=256, page_size=64, seed=0, device="cuda",
+              gated=False):
+    """A block of random weights: experts and router from `workloads`, projections of unit-variance outputs; `gated`:
+    with a gate of sigmoid scores, a bias and groups, and with norms."""
     import torch
 
     import workloads
@@ -82,10 +112,22 @@ def synthetic(shape, q_heads=16, kv_heads=2, d=128, fmt="bf16", num_pages=256, p
     def dense(rows, cols):
         return (torch.randn((rows, cols), generator=gen) * cols ** -0.5).bfloat16().to(device)
 
-    moe = MoELayerW4(shape.H, shape.E, shape.k, shape.F, workloads.make_weights(shape, seed), device=device)
+    gate = norms = None
+    gates = (None, None)
+    if gated:
+        def gains():
+            return (1 + 0.2 * torch.randn(shape.H, generator=gen)).to(device)
+
+        bias = (torch.randn(shape.E, generator=gen) * 20).round().mul(0.001).to(device)
+        groups = 4 if shape.E % 4 == 0 else 1
+        gate = ExpertGate(shape.k, "sigmoid", bias, groups, max(1, groups // 2), scale=2.5)
+        norms = ResidualNorm(gains()), ResidualNorm(gains(), gains()), ResidualNorm(gains(), gains(), scale=0.9)
+        gates = 0.5 * gains(), 0.5 * gains()
+    moe = MoELayerW4(shape.H, shape.E, shape.k, shape.F, workloads.make_weights(shape, seed), device=device, gate=gate)
     router = _dev(workloads.router_weight_bits(shape, seed), device).view(torch.bfloat16)
     cache = PagedKVCache(num_pages, page_size, kv_heads, d, fmt, device)
-    return DecoderBlockW4(dense((q_heads + 2 * kv_heads) * d, shape.H), dense(shape.H, q_heads * d), router, moe, cache)
+    return DecoderBlockW4(dense((q_heads + 2 * kv_heads) * d, shape.H), dense(shape.H, q_heads * d), router, moe, cache,
+                          norms, gates)
 
 
 def serve(block, prompts, chunk, steps):
@@ -134,14 +176,15 @@ def main(argv=None):
     ap.add_argument("--prompts", default="300,45", help="prompt lengths, comma-separated")
     ap.add_argument("--chunk", type=int, default=128)
     ap.add_argument("--steps", type=int, default=8)
+    ap.add_argument("--gated", action="store_true", help="a gate and norms with gains (see above)")
     args = ap.parse_args(argv)
     import torch
 
     import workloads
-    block = synthetic(workloads.FULL, fmt=args.fmt)
+    block = synthetic(workloads.FULL, fmt=args.fmt, gated=args.gated)
     gen = torch.Generator().manual_seed(1)
-    prompts = [torch.randn((int(n), workloads.FULL.H), generator=gen).bfloat16().cuda()
-               for n in args.prompts.split(",")]
+    stream = torch.float32 if args.gated else torch.bfloat16
+    prompts = [torch.randn((int(n), workloads.FULL.H), generator=gen).to(stream).cuda() for n in args.prompts.split(",")]
     for i, (x, new, lens, _, out) in enumerate(serve(block, prompts, args.chunk, args.steps)):
         torch.cuda.synchronize()
         err = _lib.moe_get_device_error()

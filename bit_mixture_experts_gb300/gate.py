@@ -15,10 +15,18 @@ Routing = collections.namedtuple("Routing", "topk_ids topk_w counts offsets perm
 
 
 def _on(stream, device):
-    """A `with` block in which `stream`, a torch stream, a raw handle or None, is the current one."""
+    """A `with` block in which `stream`, a torch stream or a raw handle, is the current one."""
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream, device=device)
     return torch.cuda.stream(stream)
+
+
+def _empty(shape, dtype, device, stream):
+    """An output for a call on `stream` (None: the current one): memory of that stream."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with _on(stream, device):
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
 class ExpertGate:
@@ -50,7 +58,7 @@ class ExpertGate:
         self.k, self.score, self.bias, self.groups = k, score, bias, groups
         self.top_groups = groups if top_groups is None else top_groups
         self.group_score, self.renorm, self.scale = group_score, renorm, scale
-        self._workspaces = {}
+        self._workspaces, self._plans = {}, {}
         self.struct = _lib.Gate(_lib._ptr(bias), _lib.SCORES[score], groups, self.top_groups,
                                 _lib.GROUP_SCORES[group_score], int(renorm), scale)
 
@@ -73,9 +81,7 @@ class ExpertGate:
         self._logits(logits)
         shape, dev = (logits.shape[0], self.k), logits.device
         if out is None:
-            with _on(stream, dev):
-                out = (torch.empty(shape, dtype=torch.int32, device=dev),
-                       torch.empty(shape, dtype=torch.float32, device=dev))
+            out = _empty(shape, torch.int32, dev, stream), _empty(shape, torch.float32, dev, stream)
         else:
             for t, dtype in zip(out, (torch.int32, torch.float32)):
                 if t.dtype != dtype or t.shape != shape or t.device != dev or not t.is_contiguous():
@@ -89,22 +95,33 @@ class ExpertGate:
         block_n rows (include/moe_w4.h).  Scratch is kept per stream, in a graph capture it is the graph's."""
         self._logits(logits)
         (T, E), k, dev = logits.shape, self.k, logits.device
-        cap = _lib.moe_block_map_capacity(T, E, k, block_n)
-        need = _lib.moe_route_workspace_size(T, E, k, block_n)
-        with _on(stream, dev):
-            def new(*shape, dtype=torch.int32):
-                return torch.empty(shape, dtype=dtype, device=dev)
-            r = Routing(new(T, k), new(T, k, dtype=torch.float32), new(E), new(E + 1), new(T * k), new(T * k),
-                        new(cap, 3), new(1))
-            ws = self._workspace(need, stream, dev) if need else None
+        shapes, need = self._plan(T, E, block_n)
+        r = Routing(*(_empty(shape, dtype, dev, stream) for shape, dtype in shapes))
+        ws = self._workspace(need, stream, dev) if need else None
         _lib.moe_route_gated(logits, T, E, k, self.struct, block_n, *r, ws, stream)
         return r
 
+    def _plan(self, T, E, block_n):
+        """Shapes and types of a Routing's tensors, bytes of scratch."""
+        have = self._plans.get((T, E, block_n))
+        if have is None:
+            A, cap, i32 = T * self.k, _lib.moe_block_map_capacity(T, E, self.k, block_n), torch.int32
+            shapes = (((T, self.k), i32), ((T, self.k), torch.float32), ((E,), i32), ((E + 1,), i32), ((A,), i32),
+                      ((A,), i32), ((cap, 3), i32), ((1,), i32))
+            have = self._plans[T, E, block_n] = shapes, _lib.moe_route_workspace_size(T, E, self.k, block_n)
+        return have
+
     def _workspace(self, need, stream, dev):
         """Zeros, which every call leaves behind as it found them."""
+        if stream is not None:
+            with _on(stream, dev):
+                return self._workspace_here(need, dev)
+        return self._workspace_here(need, dev)
+
+    def _workspace_here(self, need, dev):
         if torch.cuda.is_current_stream_capturing():
             return torch.zeros(need, dtype=torch.uint8, device=dev)
-        key = (dev, _lib._stream(stream))
+        key = (dev, _lib._stream())
         have = self._workspaces.get(key)
         if have is None or have.numel() < need:
             have = self._workspaces[key] = torch.zeros(need, dtype=torch.uint8, device=dev)

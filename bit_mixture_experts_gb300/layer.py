@@ -44,16 +44,23 @@ class MoELayerW4:
 
     `weights` holds the canonical arrays of the workloads module (w13_packed,
     w13_scale, w13_bias, w2_packed, w2_scale, w2_bias) as numpy arrays or torch
-    tensors already on the device.
+    tensors already on the device.  `gate` (an ExpertGate of the same k) is how
+    the experts are chosen; None: softmax renormalised over the chosen.
     """
 
-    def __init__(self, H, E, k, F, weights: dict, device="cuda", impl="auto", block_n=None, fuse_combine=False):
+    def __init__(self, H, E, k, F, weights: dict, device="cuda", impl="auto", block_n=None, fuse_combine=False,
+                 gate=None):
         import torch
         self.H, self.E, self.k, self.F = H, E, k, F
         self.device = torch.device(device)
         self.impl = _lib.IMPLS[impl] if isinstance(impl, str) else int(impl)
         if H % 128 or F % 128:
             raise ValueError(f"H={H} and F={F} must be multiples of 128 (the kernels' K and M steps)")
+        if gate is not None:
+            if gate.k != k:
+                raise ValueError(f"the gate chooses {gate.k} experts a token, the layer takes {k}")
+            gate.check(E, gate.bias.device if gate.bias is not None else self.device)
+        self.gate = gate
         self.block_n = block_n  # None: chosen per token count by default_block_n
         # tensor-core path: the combine in the down GEMM's epilogue (moe_down_combine) instead of its own
         # launch; off by default, as it measures slower: the epilogue's counts, fences and gathers lengthen
@@ -155,12 +162,49 @@ class MoELayerW4:
         b = self.buffers(T)
         if out is None:
             out = torch.empty((T, self.H), dtype=torch.bfloat16, device=self.device)
-        _lib.moe_layer_forward(x, logits, out, T, self.H, self.F, self.E, self.k, self.block_n_for(T),
-                               self.impl_for(T), self.weights, b["struct"], stream)
+        sizes = T, self.H, self.F, self.E, self.k, self.block_n_for(T), self.impl_for(T), self.weights, b["struct"], stream
+        if self.gate is None:
+            _lib.moe_layer_forward(x, logits, out, *sizes)
+        else:
+            _lib.moe_layer_forward_gated(x, logits, self.gate.struct, out, None, *sizes)
+        return out
+
+    def forward_residual(self, x, logits, residual, norm, gate=None, out=None, choice=None, stream=None):
+        """The layer and what follows it: x bf16 [T, H] (the normed input), logits fp32 [T, E] -> (r, n) of
+        ``norm`` (a ResidualNorm) for the residual stream `residual` [T, H] and the experts' combined output, which is
+        not written.  `gate`, `out`: as ResidualNorm.add's.  `choice`: (ids int32 [T, k], weights float32 [T, k]) chosen
+        already, with logits None."""
+        import torch
+        T = x.shape[0]
+        if x.dtype != torch.bfloat16 or x.shape != (T, self.H) or not x.is_contiguous() or x.device != residual.device:
+            raise ValueError(f"x must be contiguous bfloat16 [T, {self.H}] on {residual.device}: got {x.dtype} "
+                             f"{tuple(x.shape)} on {x.device}")
+        if (logits is None) == (choice is None):
+            raise ValueError("either logits or a choice is needed")
+        if residual.shape != x.shape:
+            raise ValueError(f"residual is {tuple(residual.shape)}, x {tuple(x.shape)}")
+        b = self.buffers(T)
+        struct = b["struct"]
+        for t, name, shape, dtype in ([(logits, "logits", (T, self.E), torch.float32)] if choice is None else
+                                      [(choice[0], "choice[0]", (T, self.k), torch.int32),
+                                       (choice[1], "choice[1]", (T, self.k), torch.float32)]):
+            if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.device != x.device:
+                raise ValueError(f"{name} must be contiguous {dtype} {shape} on {x.device}: got {t.dtype} {tuple(t.shape)} "
+                                 f"on {t.device}")
+        if choice is not None:
+            struct = _lib.Buffers.from_buffer_copy(struct)
+            struct.topk_ids, struct.topk_w = choice[0].data_ptr(), choice[1].data_ptr()
+        s, out = norm.describe(residual, gate, out, stream)
+        how = self.gate.struct if self.gate is not None else _lib.Gate(None, 0, 1, 1, 0, 1, 1.0)
+        _lib.moe_layer_forward_gated(x, logits, how, None, s, T, self.H, self.F, self.E, self.k, self.block_n_for(T),
+                                     self.impl_for(T), self.weights, struct, stream)
         return out
 
     def forward_host(self, x_host, logits_host, out_host, stage, stream=None):
-        """Host (pinned) x, logits, out; `stage` holds device x, logits, out of the same shapes."""
+        """Host (pinned) x, logits, out; `stage` holds device x, logits, out of the same shapes.  Not for a layer
+        with a gate."""
+        if self.gate is not None:
+            raise ValueError("a layer with a gate takes its inputs on the device (forward)")
         T = x_host.shape[0]
         b = self.buffers(T)
         _lib.moe_layer_forward_host(x_host, logits_host, out_host, stage["x"], stage["logits"], stage["out"], T,

@@ -12,9 +12,18 @@ from __future__ import annotations
 import torch
 
 from . import _lib
-from .gate import _on
+from .gate import _empty
 
 _F32 = {torch.bfloat16: 0, torch.float32: 1}
+_current_device = torch.cuda.current_device
+
+
+def _row_stride(t, name, dtype, shape, device):
+    """The distance of t's rows, which must be contiguous and as the others'."""
+    if t.shape != shape or t.dtype != dtype or t.device != device or (t.stride(1) != 1 and shape[1] > 1):
+        raise ValueError(f"{name} must be {dtype} {tuple(shape)} on {device} with contiguous rows: got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}, strides {t.stride()}")
+    return t.stride(0)
 
 
 class ResidualNorm:
@@ -33,61 +42,56 @@ class ResidualNorm:
         self.w_pre, self.w_post, self.scale, self.eps, self.offset = w_pre, w_post, scale, eps, offset
         self.H = given[0].shape[0] if given else None
         self.device = given[0].device if given else None
-        self.param_f32 = _F32[given[0].dtype] if given else 0
-
-    def _rows(self, t, name, dtypes, shape, device):
-        if t.dtype not in dtypes or t.shape != shape or t.device != device or (t.stride(1) != 1 and shape[1] > 1):
-            raise ValueError(f"{name} must be {' or '.join(str(d) for d in dtypes)} {tuple(shape)} on {device} with "
-                             f"contiguous rows: got {t.dtype} {tuple(t.shape)} on {t.device}, strides {t.stride()}")
+        self._constants = _lib.Residual(w_pre=_lib._ptr(w_pre), w_post=_lib._ptr(w_post), post=int(w_post is not None),
+                                        param_f32=_F32[given[0].dtype] if given else 0, offset=offset, scale=scale, eps=eps)
 
     def describe(self, x, gate, out, stream=None, post=True):
         """The call's description for the library, and its outputs (r, n): `out`, or new ones of `stream`."""
-        if x.dim() != 2 or x.device.type != "cuda":
-            raise ValueError(f"x must be [T, H] on a CUDA device: got {tuple(x.shape)} on {x.device}")
-        shape, dev = x.shape, x.device
-        self._rows(x, "x", tuple(_F32), shape, dev)
+        shape, dev, dtype = x.shape, x.device, x.dtype
+        if len(shape) != 2 or not x.is_cuda or dtype not in _F32:
+            raise ValueError(f"x must be bfloat16 or float32 [T, H] on a CUDA device: got {dtype} {tuple(shape)} on {dev}")
         if self.H is not None and (self.H != shape[1] or self.device != dev):
             raise ValueError(f"x is {tuple(shape)} on {dev}, the gains [{self.H}] on {self.device}")
-        if torch.cuda.current_device() != dev.index:
-            raise ValueError(f"x is on {dev}, but device {torch.cuda.current_device()} is the current one")
+        if _current_device() != dev.index:
+            raise ValueError(f"x is on {dev}, but device {_current_device()} is the current one")
+        s = _lib.Residual.from_buffer_copy(self._constants)
+        s.x, s.x_stride, s.stream_f32 = x.data_ptr(), _row_stride(x, "x", dtype, shape, dev), _F32[dtype]
         if out is None:
-            with _on(stream, dev):
-                r, n = torch.empty(shape, dtype=x.dtype, device=dev), torch.empty(shape, dtype=torch.bfloat16, device=dev)
+            r, n = _empty(shape, dtype, dev, stream), _empty(shape, torch.bfloat16, dev, stream)
         else:
             r, n = out
-            if r is not None:
-                self._rows(r, "out[0]", (x.dtype,), shape, dev)
-            if n is not None:
-                self._rows(n, "out[1]", (torch.bfloat16,), shape, dev)
-        g_ptr, g_token, g_channel, g_f32 = None, 0, 0, 0
+        if r is not None:
+            s.r, s.r_stride = r.data_ptr(), _row_stride(r, "out[0]", dtype, shape, dev)
+        if n is not None:
+            s.n, s.n_stride = n.data_ptr(), _row_stride(n, "out[1]", torch.bfloat16, shape, dev)
+        if not post:
+            s.post = 0
         if gate is not None:
             # [H], [1], [T, 1], [1, H] or [T, H], as broadcast against [T, H]
-            g = gate if gate.dim() == 2 else gate[None]
-            if (gate.dim() not in (1, 2) or g.dtype not in _F32 or g.device != dev
-                    or g.shape[0] not in (1, shape[0]) or g.shape[1] not in (1, shape[1])
-                    or (g.shape[1] > 1 and g.stride(1) != 1)):
+            dims, strides, g_type = gate.shape, gate.stride(), gate.dtype
+            if len(dims) == 1:
+                dims, strides = (1, dims[0]), (0, strides[0])
+            if (len(dims) != 2 or g_type not in _F32 or gate.device != dev or dims[0] not in (1, shape[0])
+                    or dims[1] not in (1, shape[1]) or (dims[1] > 1 and strides[1] != 1)):
                 raise ValueError(f"gate must be bfloat16 or float32 on {dev}, with contiguous rows, and fit {tuple(shape)}: "
-                                 f"got {gate.dtype} {tuple(gate.shape)} on {gate.device}, strides {gate.stride()}")
-            g_ptr, g_f32 = g.data_ptr(), _F32[g.dtype]
-            g_token, g_channel = g.stride(0) if g.shape[0] > 1 else 0, int(g.shape[1] > 1)
-        s = _lib.Residual(x.data_ptr(), x.stride(0), _lib._ptr(r), 0 if r is None else r.stride(0), _lib._ptr(n),
-                          0 if n is None else n.stride(0), _lib._ptr(self.w_pre), _lib._ptr(self.w_post), g_ptr, g_token,
-                          g_channel, int(post and self.w_post is not None), _F32[x.dtype], self.param_f32, g_f32,
-                          self.offset, self.scale, self.eps)
+                                 f"got {g_type} {tuple(gate.shape)} on {gate.device}, strides {gate.stride()}")
+            s.gate, s.gate_f32 = gate.data_ptr(), _F32[g_type]
+            s.gate_token_stride, s.gate_per_channel = strides[0] if dims[0] > 1 else 0, int(dims[1] > 1)
         return s, (r, n)
 
     def add(self, x, y, gate=None, out=None, stream=None):
         """(r, n) of the stream x [T, H] and the block's output y (bf16 [T, H]).  `gate`: bf16 or float32 that broadcasts
         against [T, H].  `out`: the pair to write, either of which may be None."""
         s, out = self.describe(x, gate, out, stream)
-        self._rows(y, "y", (torch.bfloat16,), x.shape, x.device)
-        _lib.moe_residual_norm(y, y.stride(0), x.shape[0], x.shape[1], s, stream)
+        T, H = shape = x.shape
+        _lib.moe_residual_norm(y, _row_stride(y, "y", torch.bfloat16, shape, x.device), T, H, s, stream)
         return out
 
     def norm(self, x, out=None, stream=None):
         """n of r = scale x: the norm before a first block, bf16 [T, H] (`out` None: a new tensor)."""
-        with _on(stream, x.device):
-            n = torch.empty(x.shape, dtype=torch.bfloat16, device=x.device) if out is None else out
+        if out is None and x.is_cuda:
+            out = _empty(x.shape, torch.bfloat16, x.device, stream)
+        n = out
         s, _ = self.describe(x, None, (None, n), stream, post=False)
         _lib.moe_residual_norm(None, 0, x.shape[0], x.shape[1], s, stream)
         return n
@@ -105,7 +109,7 @@ class ResidualNorm:
                 or not inv_perm.is_contiguous():
             raise ValueError(f"inv_perm must be contiguous int32 [{T * k}] on {x.device}: got {inv_perm.dtype} "
                              f"{tuple(inv_perm.shape)} on {inv_perm.device}")
-        self._rows(y, "y", (torch.bfloat16,), (T * k + T, H), x.device)
+        _row_stride(y, "y", torch.bfloat16, (T * k + T, H), x.device)
         if not y.is_contiguous():
             raise ValueError(f"y must be contiguous: strides {y.stride()}")
         _lib.moe_combine_residual_norm(y, inv_perm, topk_w, T, H, k, s, stream)

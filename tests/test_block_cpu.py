@@ -39,3 +39,12 @@ def test_block_refuses_projections_that_are_no_heads(q_heads, kv_heads, extra):
         block.DecoderBlockW4(*w, moe, cache)
     ok = [torch.zeros(s) for s in ((8 * d, H), (H, 4 * d), (E, H))]
     assert block.DecoderBlockW4(*ok, moe, types.SimpleNamespace(d=d, heads=2)).q_heads == 4
+
+
+def test_block_takes_three_norms():
+    from bit_mixture_experts_gb300 import block
+    d, E = 64, 4
+    moe, cache = types.SimpleNamespace(H=H, E=E), types.SimpleNamespace(d=d, heads=2)
+    w = [torch.zeros(s) for s in ((8 * d, H), (H, 4 * d), (E, H))]
+    with pytest.raises(ValueError, match="three norms"):
+        block.DecoderBlockW4(*w, moe, cache, norms=(None, None))
