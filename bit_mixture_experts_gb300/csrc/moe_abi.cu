@@ -382,6 +382,11 @@ int moe_combine_residual_norm(const uint16_t* y, const int32_t* inv_perm, const 
   if (rc || T == 0) return rc;
   rc = check_ptrs(y, inv_perm, topk_w);
   if (rc) return rc;
+  const Rows r = rows_of(p->r, p->r_stride, H, p->stream_f32 ? 4 : 2, T), n = rows_of(p->n, p->n_stride, H, 2, T);
+  for (const void* i : {static_cast<const void*>(inv_perm), static_cast<const void*>(topk_w)}) {
+    const Rows in = rows_of(i, 0, static_cast<long long>(T) * k, 4, 1);
+    if (overlap(in, r) || overlap(in, n)) return MOE_ERR_OVERLAP;
+  }
   a.inv_perm = inv_perm;
   a.topk_w = topk_w;
   a.k = k;

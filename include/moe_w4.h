@@ -235,14 +235,15 @@ int moe_norm_router(const uint16_t* x, const uint16_t* w_router, int T, int H, i
  *           equal ones by index
  *   w_j = scale * s_j / (sum of the chosen s_i, if renorm, else 1); 0 where
  *         that sum is 0
- * The choice is that of scores that are off by less than 2^-40: a token whose
- * choice a rounding in 32 bits could change is done again with scores of twice
- * the length.  Without a bias, and with groups
- * (if any) scored by their largest, the logits themselves are compared.  An expert whose logit is -inf or NaN is not
- * available: it is chosen only where fewer than k others are left (then by
- * index), with weight 0; a group is scored by its available experts, one
- * without any is behind all others.  A logit of +inf counts as the largest
- * finite one.  bias has to be finite.
+ * The choice is that of values that are off by less than 2^-40 (times the
+ * largest bias, where that is above 1): a token whose choice a rounding in 32
+ * bits could change is done again with scores of twice the length.  Without a
+ * bias, and with groups (if any) scored by their largest, the logits themselves
+ * are compared.  An expert whose logit is -inf or NaN is not available: it is
+ * chosen only where fewer than k others are left (then by index), with weight 0;
+ * a group is scored by its available experts, one without any is behind all
+ * others.  A logit of +inf counts as the largest finite one.  bias has to be
+ * finite.
  */
 enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 };
 enum { MOE_GROUP_MAX = 0, MOE_GROUP_TOP2 = 1 };
@@ -268,8 +269,8 @@ int moe_gate(const float* logits, int T, int E, int k, const moe_gate_t* gate, i
 /*
  * moe_route_gated -- moe_route with the experts chosen by a gate: the same
  * outputs, workspace and limits.  With logits NULL the experts are those that
- * topk_ids and topk_w hold (`gate` is not read; an id outside [0, E) sets
- * MOE_DEV_BAD_INDEX where T * k > 1024 and is taken as one inside it).
+ * topk_ids and topk_w hold (`gate` is not read; an id outside [0, E) is taken
+ * as one inside it, and sets MOE_DEV_BAD_INDEX where T * k > 1024).
  */
 int moe_route_gated(const float* logits, int T, int E, int k, const moe_gate_t* gate, int block_n, int32_t* topk_ids,
                     float* topk_w, int32_t* counts, int32_t* offsets, int32_t* perm, int32_t* inv_perm,
@@ -289,10 +290,11 @@ int moe_route_gated(const float* logits, int T, int E, int k, const moe_gate_t* 
  * The sums run in FP32, n is taken of the unrounded r, r and n are rounded once.
  * A tensor's rows are H consecutive elements and its strides count elements;
  * pointers need only their elements' alignment (rows on 16 bytes are read
- * faster).  r may take the place of x or y, n that of x or y or a gate per
- * channel and token, if the pointer, the stride and the type are the same (in
- * moe_combine_residual_norm not that of y); columns of one wider tensor may
- * alternate.  Any other overlap of an output returns MOE_ERR_OVERLAP.
+ * faster; others are read with what lies around them in the same 16 bytes).  An
+ * output may take the place of x, y or a gate per token and channel, if the
+ * pointer, the stride and the type are the same (in moe_combine_residual_norm
+ * not that of y); columns of one wider tensor may alternate.  Any other overlap
+ * of an output with an input or the other output returns MOE_ERR_OVERLAP.
  * Limits: 0 <= T <= 2^20 (T = 0 does nothing), 1 <= H <= 32768, strides below
  * 2^40, those of inputs >= 0 (0: one row for all), those of outputs >= H.
  */

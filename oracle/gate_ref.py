@@ -55,6 +55,30 @@ def choose(logits, k, **kw):
     return np.stack([b[0] for b in both]).astype(np.int32), np.stack([b[1] for b in both])
 
 
+def choose_many(logits, k, score="softmax", bias=None, groups=1, top_groups=None, group_score="top2", renorm=True,
+                scale=1.0):
+    """choose for many tokens at a time, all of whose logits are finite."""
+    l = np.asarray(logits, np.float64)
+    T, E = l.shape
+    if score == "softmax":
+        s = np.exp(l - l.max(1, keepdims=True))
+        s /= s.sum(1, keepdims=True)
+    else:
+        s = 1.0 / (1.0 + np.exp(-l))
+    dropping = top_groups is not None and top_groups < groups
+    v = s + np.asarray(bias, np.float64) if bias is not None else s if dropping and group_score == "top2" else l
+    if dropping:
+        best = -np.sort(-v.reshape(T, groups, -1), axis=2)
+        worth = best[:, :, 0] if group_score == "max" else best[:, :, :2].sum(2)
+        stay = np.argsort(-worth, axis=1, kind="stable")[:, :top_groups]
+        allowed = np.zeros((T, groups), bool)
+        np.put_along_axis(allowed, stay, True, 1)
+        v = np.where(np.repeat(allowed, E // groups, 1), v, -np.inf)
+    ids = np.argsort(-v, axis=1, kind="stable")[:, :k]
+    w = np.take_along_axis(s, ids, 1)
+    return ids.astype(np.int32), (w / w.sum(1, keepdims=True) if renorm else w) * scale
+
+
 def sort_assignments(ids, E):
     """ids [T, k] -> (counts, offsets, perm, inv_perm) of moe_route."""
     flat = np.asarray(ids).reshape(-1)

@@ -60,6 +60,19 @@ def test_experts_that_are_not_available_by_hand():
     assert ids.tolist() == [1, 2]
 
 
+def test_many_tokens_at_a_time_are_the_same():
+    r = np.random.default_rng(2)
+    l, b = r.standard_normal((30, 48)), r.standard_normal(48) * 0.05
+    l[:10] = np.round(l[:10] * 2) / 2
+    for score in ("softmax", "sigmoid"):
+        for bias in (None, b):
+            for groups, top, how in ((1, None, "max"), (6, 2, "max"), (6, 2, "top2"), (6, 6, "top2")):
+                kw = dict(score=score, bias=bias, groups=groups, top_groups=top, group_score=how, scale=1.5)
+                one, many = gate_ref.choose(l, 7, **kw), gate_ref.choose_many(l, 7, **kw)
+                np.testing.assert_array_equal(one[0], many[0])
+                np.testing.assert_allclose(one[1], many[1], rtol=1e-14)
+
+
 def _residual_fractions(x, y, w_pre, w_post, gate, scale, eps, offset):
     """The definition with exact sums of squares."""
     def rms(v):
@@ -178,6 +191,7 @@ def test_residual_argument_errors(lib, k):
     if k:
         assert call(r=BASE) == -8 and call(n=BASE + 11 * row) == -8  # rows that other tokens read
         assert call(y=None) == -1 and call(y=BASE + 2) == -2
+        assert call(r=7 * BASE - 2 * row) == -8 and call(n=8 * BASE) == -8  # over the rows' places and weights
         assert lib.moe_combine_residual_norm(BASE, BASE, BASE, 4, 64, 33, None, None) == -3
     else:
         assert call(y_stride=-1) == -3

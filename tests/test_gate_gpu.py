@@ -214,3 +214,62 @@ def test_streams_and_graphs():
     ids, _ = gate.choose(b)
     np.testing.assert_array_equal(
         ids.cpu().numpy(), gate_ref.choose(b.cpu().numpy(), 8, score="sigmoid", bias=np.zeros(256), groups=8, top_groups=4)[0])
+
+
+MANY = [  # T, E, k, groups, top_groups: tokens enough that a warp takes two or four together, in every width of a lane
+    (4001, 256, 8, 8, 4), (9001, 256, 8, 8, 4), (9002, 256, 8, 1, 1), (8003, 160, 6, 8, 3), (8001, 64, 8, 4, 2),
+    (7500, 256, 16, 8, 4), (7501, 256, 20, 8, 4), (9003, 128, 4, 16, 5), (8002, 252, 8, 9, 4), (8000, 255, 6, 17, 5),
+    (7777, 96, 8, 32, 7), (4100, 512, 16, 16, 4), (8004, 512, 8, 1, 1), (4000, 1000, 8, 5, 2), (20000, 37, 2, 1, 1),
+]
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("T,E,k,groups,top", MANY)
+def test_many_tokens(T, E, k, groups, top, score):
+    import torch
+
+    from bit_mixture_experts_gb300 import _lib
+    for i, (with_bias, how, coarse) in enumerate(((True, "top2", False), (False, "top2", True), (True, "max", True),
+                                                  (False, "max", False))):
+        l, b = draw(T, E, T + 10 * i, coarse)
+        if i == 2:  # many values that 32 bits do not tell apart
+            s, _ = gate_ref.scores(l[0], score)
+            b = (0.5 - s).astype(np.float32)
+            l[::7] = l[0]
+        b = b if with_bias else None
+        kw = dict(score=score, groups=groups, top_groups=top, group_score=how, renorm=i % 2 == 0, scale=2.0)
+        gate = make(k, b, **kw)
+        ids, w = gate.choose(torch.tensor(l, device="cuda"))
+        torch.cuda.synchronize()
+        assert _lib.moe_get_device_error() == 0
+        want_ids, want_w = gate_ref.choose_many(l, k, bias=b, **kw)
+        np.testing.assert_array_equal(ids.cpu().numpy(), want_ids)
+        off = np.abs(w.double().cpu().numpy() - want_w) - weight_bound(want_w, l.astype(np.float64), want_ids, kw)
+        assert (off <= 0).all(), off.max()
+
+
+def test_unavailable_experts_among_many_tokens():
+    """Tokens of one warp with and without experts that are not available."""
+    import torch
+    l, b = draw(8100, 256, 1)
+    r = np.random.default_rng(0)
+    l[::3, r.permutation(256)[:40]] = -np.inf
+    l[5::97] = np.nan
+    l[8::101, :250] = -np.inf
+    kw = dict(score="sigmoid", groups=8, top_groups=4, scale=2.5)
+    ids, w = make(8, b, **kw).choose(torch.tensor(l, device="cuda"))
+    few, few_w = make(8, b, **kw).choose(torch.tensor(l[:700], device="cuda"))  # a token a warp
+    assert torch.equal(ids[:700], few) and torch.equal(w[:700], few_w)
+    at = np.r_[0:60, 8000:8100, 5:8100:97][:200]
+    want_ids, want_w = gate_ref.choose(l[at], 8, bias=b, **kw)
+    np.testing.assert_array_equal(ids.cpu().numpy()[at], want_ids)
+    np.testing.assert_allclose(w.double().cpu().numpy()[at], want_w, rtol=2e-6)
+
+
+def test_a_bias_out_of_proportion():
+    """Biases that switch experts on and off: the range of values is no longer that of the scores."""
+    l, b = draw(60, 256, 4)
+    b[[3, 50, 51, 200]] = [1000.0, -1000.0, 1e6, -1e6]
+    for kw in (dict(), dict(groups=8, top_groups=4), dict(groups=8, top_groups=3, group_score="max")):
+        for score in ("sigmoid", "softmax"):
+            check(l, 8, b, score=score, **kw)
