@@ -252,6 +252,12 @@ __device__ __forceinline__ int choose_slowly(const float* row, const Lane& me, b
   return id;
 }
 
+// m of experts that are not available, and of none that is.
+template <int IDX, Mode MODE>
+__host__ __device__ constexpr uint32_t not_available_m() {
+  return MODE == BY_LOGIT ? 0x007fffffu >> (IDX + 1) : 1u;
+}
+
 // What a warp keeps from token to token: its experts' biases in units, and what a unit is.
 //   m = s a + base_e,  base_e = (b_e - least bias) a + 2,  below 2^(31 - IDX)
 // computed as FP32 numbers of 2^23 and more, whose lower bits are the integer.
@@ -338,7 +344,7 @@ __host__ __device__ inline int batch_of(const Gate& g, int width) {
 template <int EPL, int IDX, Mode MODE>
 __device__ __forceinline__ bool choose_close(const float* row, const uint32_t (&key)[EPL], uint32_t near,
                                              const Scale& scale, float blur, const Gate& g, int lane, int* choice) {
-  constexpr uint32_t MASK = (1u << IDX) - 1u, OUT = MODE == BY_LOGIT ? 0x007fffffu >> (IDX + 1) : 1u;
+  constexpr uint32_t MASK = (1u << IDX) - 1u, OUT = not_available_m<IDX, MODE>();
   uint32_t last = 0x80000000u, kth = 0, mine = 0;
   int n = 0;
 #pragma unroll 1
@@ -390,95 +396,103 @@ __device__ __forceinline__ bool choose_close(const float* row, const uint32_t (&
   return !__any_sync(FULL, lane + 1 < n && x2 != -INFINITY && !alike && !((h - h2) + (l - l2) > o + o2));
 }
 
+// What a warp makes of a token's logits.
+struct Made {
+  float top, inv;  // softmax: the largest logit, 1 / sum (the largest score)
+  uint32_t near;   // the largest difference of two m that errors may account for
+};
+
+// Keys of a lane's logits.  `near`: each m is off by its score's error and 1.5 (b - least, base, m).  Sigmoid: the
+// fast exponential is off by (2 + 1.16 |l|) 2^-23, which enters s times 1 - s (s (1 - s) <= 1/4, s (1 - s) |l| <=
+// 0.224), the sum by 2^-24, the reciprocal by 2^-23: below 5e-7.  Softmax: s times 1.5e-6 and 2^-24 per addition
+// (expf 2^-22, its argument 2^-24 (top - l), on average at most ln 1024 2^-24, sum, reciprocal, product), and
+// 2^-24 s (top - l) <= 2^-24 0.37 / sum.
+template <int EPL, int IDX, Mode MODE, bool WHOLE>
+__device__ __forceinline__ Made make_keys(const float (&l)[EPL], const Units<EPL, IDX, MODE>& u, const Gate& g,
+                                          const Lane& me, uint32_t (&key)[EPL]) {
+  constexpr uint32_t MASK = (1u << IDX) - 1u, OUT = not_available_m<IDX, MODE>();
+  Made made = {0.f, 0.f, 0};
+  float e[MODE == SOFTMAX ? EPL : 1];
+  if (MODE == SOFTMAX || (MODE == BY_LOGIT && g.softmax && !g.renorm)) {
+    float most = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) most = fmaxf(most, available(l[i]));
+    most = key_float(__reduce_max_sync(FULL, float_key(most)));
+    made.top = most == -INFINITY ? 0.f : most;
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      const float x = expf(available(l[i]) - made.top);
+      sum += x;
+      if (MODE == SOFTMAX) e[MODE == SOFTMAX ? i : 0] = x;
+    }
+#pragma unroll
+    for (int m = 16; m >= 1; m >>= 1) sum += __shfl_xor_sync(FULL, sum, m);
+    made.inv = sum > 0.f ? 1.0f / sum : 0.f;
+  }
+  if (MODE == SIGMOID) made.near = static_cast<uint32_t>(1e-6f * u.a) + 5u;
+  if (MODE == SOFTMAX) made.near = static_cast<uint32_t>((3.1e-6f + 1.2e-7f * EPL) * made.inv * u.a) + 5u;
+  // (0 x: NaN of what is not finite; a comparison per expert would cost twice as much)
+  bool odd = true;
+  if (WHOLE && MODE != BY_LOGIT) {
+    float zero = 0.f;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) zero = fmaf(l[i], 0.f, zero);
+    odd = __any_sync(FULL, zero != 0.f);
+  }
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) {
+    const uint32_t index = MASK - static_cast<uint32_t>(me.first + i);
+    if (MODE == BY_LOGIT) {
+      key[i] = (float_key(available(l[i])) >> (IDX + 1) << IDX) | index;
+    } else {
+      const float s = MODE == SOFTMAX ? e[MODE == SOFTMAX ? i : 0] * made.inv
+                                      : fast_rcp(1.0f + fast_exp2(l[i] * -1.44269504f));
+      float base;
+      if (u.KEEP)
+        base = u.base[u.KEEP ? i : 0];
+      else
+        base = u.at(g.bias && u.a > 0.f && i < me.n ? __ldg(g.bias + me.first + i) : u.least);
+      const uint32_t m = __float_as_uint(fmaf(s, u.a, base));
+      if (IDX == 8)  // the integer's three bytes and the index's, of which a word holds four
+        key[i] = __byte_perm(m, (index + i % 4) * 0x01010101u - 0x03020100u, 0x2104 + i % 4);
+      else
+        key[i] = (m << IDX) + index;
+    }
+    if (!WHOLE && i >= me.n) key[i] = 0;
+  }
+  if (MODE != BY_LOGIT && odd) {
+#pragma unroll
+    for (int i = 0; i < EPL; ++i)
+      if (!(l[i] > -INFINITY) && (WHOLE || i < me.n)) key[i] = (OUT << IDX) + MASK - static_cast<uint32_t>(me.first + i);
+  }
+  return made;
+}
+
 // Tokens t .. t + BATCH - 1 (those below T) by one warp: lane i (32 / BATCH) + j ends with the j-th choice of
 // token t + i and its weight.  WHOLE: every lane has EPL experts, which start on 16 bytes.
 template <int EPL, int IDX, Mode MODE, int BATCH, bool WHOLE>
 __device__ __forceinline__ void warp_gate(const float* logits, int t, int T, const Units<EPL, IDX, MODE>& u, const Gate& g,
                                           const Lane& me, int lane, int* id_out, float* w_out) {
-  constexpr uint32_t MASK = (1u << IDX) - 1u;
+  constexpr uint32_t MASK = (1u << IDX) - 1u, OUT = not_available_m<IDX, MODE>();
   constexpr int SEG = 32 / BATCH;
-  // m of experts that are not available, and of none that is
-  constexpr uint32_t OUT = MODE == BY_LOGIT ? 0x007fffffu >> (IDX + 1) : 1u;
   const int ti = lane / SEG, tj = lane % SEG;  // whose choice this lane ends with
   uint32_t key[BATCH][EPL];
-  float top = 0.f, inv = 0.f;  // this lane's token's: softmax's largest logit, 1 / sum (the largest score)
+  float top = 0.f, inv = 0.f;  // this lane's token's
   uint32_t near[BATCH];
   uint32_t c1 = 0, c2 = 0;  // the two largest keys of this lane's group, of token (lane modulo BATCH)
   const bool drop = g.top_groups < g.groups;
-  uint32_t places[(EPL + 3) / 4];  // 255 less the experts' indices, a byte each
-#pragma unroll
-  for (int i = 0; i < (EPL + 3) / 4; ++i) places[i] = (MASK - static_cast<uint32_t>(me.first + 4 * i)) * 0x01010101u - 0x03020100u;
   {
     float l[BATCH][EPL];
 #pragma unroll
     for (int b = 0; b < BATCH; ++b) load_logits<EPL, WHOLE>(logits + static_cast<size_t>(min(t + b, T - 1)) * g.E, me, l[b]);
 #pragma unroll
     for (int b = 0; b < BATCH; ++b) {
-      float total = 0.f, e[MODE == SOFTMAX ? EPL : 1];
-      if (MODE == SOFTMAX || (MODE == BY_LOGIT && g.softmax && !g.renorm)) {
-        float most = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) most = fmaxf(most, available(l[b][i]));
-        most = key_float(__reduce_max_sync(FULL, float_key(most)));
-        if (most == -INFINITY) most = 0.f;
-        float sum = 0.f;
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) {
-          const float x = expf(available(l[b][i]) - most);
-          sum += x;
-          if (MODE == SOFTMAX) e[MODE == SOFTMAX ? i : 0] = x;
-        }
-#pragma unroll
-        for (int m = 16; m >= 1; m >>= 1) sum += __shfl_xor_sync(FULL, sum, m);
-        total = sum > 0.f ? 1.0f / sum : 0.f;
-        if (ti == b) {
-          top = most;
-          inv = total;
-        }
-      }
-      // Keys.  `near`: the largest difference of two m that errors may account for.  Each is off by its
-      // score's error and 1.5 (b - least, base, m).  Sigmoid: the fast exponential is off by
-      // (2 + 1.16 |l|) 2^-23, which enters s times 1 - s (s (1 - s) <= 1/4, s (1 - s) |l| <= 0.224), the sum by
-      // 2^-24, the reciprocal by 2^-23: below 5e-7.  Softmax: s times 1.5e-6 and 2^-24 per addition (expf
-      // 2^-22, its argument 2^-24 (top - l), on average at most ln 1024 2^-24, sum, reciprocal, product), and
-      // 2^-24 s (top - l) <= 2^-24 0.37 / sum.
-      near[b] = 0;
-      if (MODE == SIGMOID) near[b] = static_cast<uint32_t>(1e-6f * u.a) + 5u;
-      if (MODE == SOFTMAX) near[b] = static_cast<uint32_t>((3.1e-6f + 1.2e-7f * EPL) * total * u.a) + 5u;
-      // (0 x: NaN of what is not finite; a comparison per expert would cost twice as much)
-      bool odd = true;
-      if (WHOLE && MODE != BY_LOGIT) {
-        float zero = 0.f;
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) zero = fmaf(l[b][i], 0.f, zero);
-        odd = __any_sync(FULL, zero != 0.f);
-      }
-#pragma unroll
-      for (int i = 0; i < EPL; ++i) {
-        const uint32_t index = MASK - static_cast<uint32_t>(me.first + i);
-        uint32_t& x = key[b][i];
-        if (MODE == BY_LOGIT) {
-          x = (float_key(available(l[b][i])) >> (IDX + 1) << IDX) | index;
-        } else {
-          const float s = MODE == SOFTMAX ? e[MODE == SOFTMAX ? i : 0] * total
-                                          : fast_rcp(1.0f + fast_exp2(l[b][i] * -1.44269504f));
-          float base;
-          if (u.KEEP)
-            base = u.base[u.KEEP ? i : 0];
-          else
-            base = u.at(g.bias && u.a > 0.f && i < me.n ? __ldg(g.bias + me.first + i) : u.least);
-          const uint32_t m = __float_as_uint(fmaf(s, u.a, base));
-          if (IDX == 8)  // the integer's three bytes and the index's
-            x = __byte_perm(m, places[i / 4], 0x2104 + i % 4);
-          else
-            x = (m << IDX) + index;
-        }
-        if (!WHOLE && i >= me.n) x = 0;
-      }
-      if (MODE != BY_LOGIT && odd) {
-#pragma unroll
-        for (int i = 0; i < EPL; ++i)
-          if (!(l[b][i] > -INFINITY) && (WHOLE || i < me.n)) key[b][i] = (OUT << IDX) + MASK - static_cast<uint32_t>(me.first + i);
+      const Made made = make_keys<EPL, IDX, MODE, WHOLE>(l[b], u, g, me, key[b]);
+      near[b] = made.near;
+      if (ti == b) {
+        top = made.top;
+        inv = made.inv;
       }
       if (drop) {
         uint32_t a1 = 0, a2 = 0;
@@ -550,29 +564,29 @@ __device__ __forceinline__ void warp_gate(const float* logits, int t, int T, con
     }
   }
   // ---- the k largest of each token (side by side: a round is a chain of latencies)
-  uint32_t chosen = 0, others = 0;
-  uint32_t minus[BATCH], own_minus[BATCH];  // 0 less the last one chosen; for a group that does not stay 0: no key is below
+  uint32_t chosen = 0, others = 0, minus[BATCH];  // minus: 0 less the last one chosen
+  constexpr uint32_t NO_KEY = 0x7fffffffu;        // above all keys, and so never below one chosen
 #pragma unroll
   for (int b = 0; b < BATCH; ++b) {
-    minus[b] = 0x80000000u;
-    own_minus[b] = stays >> b & 1u ? 0x80000000u : 0u;
+    minus[b] = 0u - NO_KEY;
+    if (drop) {
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) key[b][i] = stays >> b & 1u ? key[b][i] : NO_KEY;
+    }
   }
 #pragma unroll 1
   for (int j = 0; j < g.k; ++j) {
     uint32_t mine = 0;
 #pragma unroll
     for (int b = 0; b < BATCH; ++b) {
-      const uint32_t r = __reduce_max_sync(FULL, below(key[b], own_minus[b]));
-      minus[b] -= r;
-      own_minus[b] -= r * (stays >> b & 1u);
+      minus[b] -= __reduce_max_sync(FULL, below(key[b], minus[b]));
       if (ti == b) mine = minus[b];
     }
     if (tj == j) chosen = 0u - mine;
   }
 #pragma unroll
   for (int b = 0; b < BATCH; ++b) {
-    const bool in = stays >> b & 1u;
-    const uint32_t most = __reduce_max_sync(FULL, below(key[b], own_minus[b])), last = 0u - minus[b];
+    const uint32_t most = __reduce_max_sync(FULL, below(key[b], minus[b])), last = 0u - minus[b];
     const uint32_t next = most >> 31 ? last + most : 0u;
     // every other expert that may be ahead of the last one chosen has to tie with it in logit and bias
     if (next >> IDX > OUT && (last >> IDX) - (next >> IDX) <= near[b]) {
@@ -583,7 +597,7 @@ __device__ __forceinline__ void warp_gate(const float* logits, int t, int T, con
 #pragma unroll
       for (int i = 0; i < EPL; ++i) {
         const uint32_t x = key[b][i];
-        if (!in || x >= last || x >> IDX <= OUT || (last >> IDX) - (x >> IDX) > near[b]) continue;
+        if (x >= last || x >> IDX <= OUT || (last >> IDX) - (x >> IDX) > near[b]) continue;
         const float xi = available(__ldcg(row + me.first + i)), bi = g.bias ? __ldg(g.bias + me.first + i) : 0.f;
         if (!(xi == xk && bi == bk)) alike = false;
       }
@@ -615,20 +629,14 @@ __device__ __forceinline__ void warp_gate(const float* logits, int t, int T, con
     for (uint32_t left = unsure | close; left; left &= left - 1u) {
       const int b = __ffs(left) - 1;
       const float* at = logits + static_cast<size_t>(t + b) * g.E;
-      uint32_t own[EPL], slack = 0;
-      bool in = true;
-#pragma unroll
-      for (int i = 0; i < EPL; ++i) own[i] = 0;
-#pragma unroll
-      for (int o = 0; o < BATCH; ++o)
-        if (o == b) {
-          slack = near[o];
-          in = stays >> o & 1u;
-#pragma unroll
-          for (int i = 0; i < EPL; ++i) own[i] = key[o][i];
-        }
+      // (its keys anew: those of groups that do not stay are gone)
+      float l[EPL];
+      uint32_t own[EPL];
+      load_logits<EPL, WHOLE>(at, me, l);
+      const Made made = make_keys<EPL, IDX, MODE, WHOLE>(l, u, g, me, own);
+      bool in = stays >> b & 1u;
       // softmax: with 1 / sum as it is first, unless the groups need it exact anyway
-      Scale scale = {__shfl_sync(FULL, top, b * SEG), {__shfl_sync(FULL, inv, b * SEG), 0.f}};
+      Scale scale = {made.top, {made.inv, 0.f}};
       float blur = MODE == SOFTMAX ? 1.5e-6f + 6e-8f * EPL : 0.f;
       bool groups = unsure >> b & 1u, done = false;
       int e = 0;
@@ -642,7 +650,7 @@ __device__ __forceinline__ void warp_gate(const float* logits, int t, int T, con
         groups = false;
 #pragma unroll
         for (int i = 0; i < EPL; ++i) own[i] = in ? own[i] : 0u;
-        done = choose_close<EPL, IDX, MODE>(at, own, slack, scale, blur, g, lane, &e);
+        done = choose_close<EPL, IDX, MODE>(at, own, made.near, scale, blur, g, lane, &e);
         if (blur == 0.f) break;
       }
       if (!done) e = choose_slowly<MODE>(at, me, in, g, scale, lane);
