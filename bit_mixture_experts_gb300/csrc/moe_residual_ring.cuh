@@ -5,13 +5,16 @@
 // registers from row to row.  A stage is all that a token needs (its row of x,
 // its row or rows of y, its row of the gate); where two such stages do not fit, a
 // stage is one row (ROWS).  Rows that do not start on 16 bytes are copied with
-// what is around them in the same 16 bytes, and written by way of shared memory,
-// so that global memory sees whole pieces of 16 bytes either way.
+// what is around them in the same 16 bytes, and read from there and written
+// element by element.
 //
 // What bounds it: memory.  16384 rows of 8192 channels, float32 stream, a gate
-// per element: 300 us, 0.92 of the copy rate; the combine of 16384 tokens, nine
-// rows of 2048 each: 139 us, 1.0 of it; 4096 rows of 2048: 12.2 us where the copy
-// rate allows 9.9 (ramp and tail of a short call).
+// per element: 279 us, 0.99 of the copy rate; the combine of 16384 tokens, nine
+// rows of 2048 each: 139 us, 1.0 of it; 4096 rows of 2048: 16 us where the copy
+// rate allows 9.9 (ramp and tail of a short call).  Rows that are not aligned:
+// the elements' loads and stores, 50000 rows of 1999 205 us, 0.57 of the rate (by
+// way of shared memory, in whole pieces, the outputs took two barriers more:
+// 253 us).
 #pragma once
 #include "moe_ptx.cuh"
 #include "moe_residual_dev.cuh"
@@ -32,6 +35,10 @@ struct Ring {
 
 constexpr int RING_MAX_STAGES = 8, RING_MAX_ROWS = 16;  // stages of a token, of a row
 constexpr int RING_BYTES = 216 * 1024;  // of an SM's shared memory
+// Bytes per SM on their way ahead of use where as much is written as read: enough to cover the latency, and no more,
+// or reads and writes come in bursts of their own (4096 rows of 2048 channels 15.4 us with two stages per block,
+// 17.6 with six; 8192 rows of 16384 199 and 261).
+constexpr int RING_AHEAD = 64 * 1024;
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
@@ -62,26 +69,6 @@ __device__ __forceinline__ float ring_sum(float v, float* s, int warps) {
     v += (x.x + x.y) + (x.z + x.w);
   }
   return v;
-}
-
-// A row of `len` bytes in shared memory, `skip_of(dst)` bytes into `s`, to global memory: whole pieces of 16
-// bytes, elements of SIZE bytes at its ends.
-template <int SIZE>
-__device__ __forceinline__ void flush_row(uint8_t* dst, const uint8_t* s, int len, int tid, int threads) {
-  const int skip = static_cast<int>(skip_of(dst));
-  uint8_t* base = dst - skip;
-  for (int at = 16 * tid; at < skip + len; at += 16 * threads) {
-    if (at >= skip && at + 16 <= skip + len) {
-      *reinterpret_cast<uint4*>(base + at) = *reinterpret_cast<const uint4*>(s + at);
-    } else {
-      for (int o = max(at, skip); o < min(at + 16, skip + len); o += SIZE) {
-        if (SIZE == 4)
-          *reinterpret_cast<uint32_t*>(base + o) = *reinterpret_cast<const uint32_t*>(s + o);
-        else
-          *reinterpret_cast<uint16_t*>(base + o) = *reinterpret_cast<const uint16_t*>(s + o);
-      }
-    }
-  }
 }
 
 // Blocks per SM that registers have to leave room for.
@@ -257,9 +244,6 @@ __global__ void __launch_bounds__(NT, ring_blocks(CH, NT))
   }
   const bool add = COMBINE || p.y;
   const float inv_h = 1.0f / static_cast<float>(H);
-  // outputs on their way, where rows do not start on 16 bytes
-  uint8_t* out_r = ring_smem + g.stages * g.stage_bytes;
-  uint8_t* out_n = out_r + g.x_bytes;
   bool dead = false;
   auto take = [&]() -> const uint8_t* {
     // A warp whose wait gave up goes on without waiting or writing, so that none is left at a barrier; and without
@@ -373,26 +357,18 @@ __global__ void __launch_bounds__(NT, ring_blocks(CH, NT))
     uint8_t* n_at = p.n ? row_of<2>(p.n, t, p.n_stride) : nullptr;
     if (p.r && !dead) {
 #pragma unroll
-      for (int c = 0; c < CH; ++c) store8<VEC, X32>(VEC ? r_at : out_r + skip_of(r_at), c, tid, threads, H, x[c]);
+      for (int c = 0; c < CH; ++c) store8<VEC, X32>(r_at, c, tid, threads, H, x[c]);
     }
     if (p.n) {
       f = rsqrtf(fmaf(ring_sum(sum8(sq), s_sum[i & 1][1], warps), inv_h, p.eps));
-      if (!VEC && p.r && !dead) flush_row<XS>(r_at, out_r, H * XS, tid, threads);  // (every thread has written its part)
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
         float b[8];
         if (!KEEP) gains<VEC>(p.w_pre, p, c, tid, threads, b);
         mul8(x[c], f, x[c]);
         mul8(x[c], KEEP ? gb[KEEP ? c : 0] : b, x[c]);
-        if (!dead) store8<VEC, false>(VEC ? n_at : out_n + skip_of(n_at), c, tid, threads, H, x[c]);
+        if (!dead) store8<VEC, false>(n_at, c, tid, threads, H, x[c]);
       }
-    }
-    if (!VEC) {
-      ptx::named_bar_sync(1, threads);
-      if (!p.n && !dead) flush_row<XS>(r_at, out_r, H * XS, tid, threads);
-      if (p.n && !dead) flush_row<2>(n_at, out_n, H * 2, tid, threads);
-      // the next row's r is written behind its first sum's barrier, if it has one, and n behind its second's
-      if (!p.post || !p.n) ptx::named_bar_sync(1, threads);
     }
   }
 }
@@ -400,11 +376,11 @@ __global__ void __launch_bounds__(NT, ring_blocks(CH, NT))
 template <bool VEC, bool X32, bool COMBINE, int CH, int NT, bool ROWS>
 cudaError_t launch_ring(const ResidualArgs& p, Ring g, int threads, cudaStream_t s) {
   const auto kernel = ring_kernel<VEC, X32, COMBINE, CH, NT, ROWS>;
-  const int out = VEC ? 0 : g.x_bytes + g.row_bytes;
   // as many blocks per SM as registers allow and leave two stages to each
-  const int blocks = max(1, min(ring_blocks(CH, NT), RING_BYTES / (2 * g.stage_bytes + out)));
-  g.stages = min(ROWS ? RING_MAX_ROWS : RING_MAX_STAGES, (RING_BYTES / blocks - out) / g.stage_bytes);
-  const size_t smem = static_cast<size_t>(g.stages) * g.stage_bytes + out;
+  const int blocks = max(1, min(ring_blocks(CH, NT), RING_BYTES / (2 * g.stage_bytes)));
+  g.stages = min(ROWS ? RING_MAX_ROWS : RING_MAX_STAGES, RING_BYTES / blocks / g.stage_bytes);
+  if (!COMBINE) g.stages = min(g.stages, max(2, RING_AHEAD / blocks / g.stage_bytes));
+  const size_t smem = static_cast<size_t>(g.stages) * g.stage_bytes;
   cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void*>(kernel), smem);
   int per_sm = 0;
   if (e == cudaSuccess) e = cached_occupancy(reinterpret_cast<const void*>(kernel), threads + 32, smem, &per_sm);
@@ -424,11 +400,10 @@ cudaError_t try_ring(const ResidualArgs& p, cudaStream_t s, bool* ran) {
   const int gate_bytes = gate_rows ? room(p.H * (p.gate_f32 ? 4 : 2)) : 0;
   g.x_bytes = room(p.H * (X32 ? 4 : 2));
   g.row_bytes = room(p.H * 2);
-  const int out = VEC ? 0 : g.x_bytes + g.row_bytes;
   g.stage_bytes = (g.x_bytes + gate_bytes + (COMBINE ? p.k + 1 : p.y ? 1 : 0) * g.row_bytes + 127) / 128 * 128;
-  const bool rows = 2 * g.stage_bytes + out > RING_BYTES;
+  const bool rows = 2 * g.stage_bytes > RING_BYTES;
   if (rows) g.stage_bytes = (max(max(g.x_bytes, gate_bytes), g.row_bytes) + 127) / 128 * 128;
-  *ran = 2 * g.stage_bytes + out <= RING_BYTES;
+  *ran = 2 * g.stage_bytes <= RING_BYTES;
   if (!*ran) return cudaSuccess;
   const unsigned long long ns = wait_limit_ns();
   g.wait_cycles = ns > (~0ull) / 3 ? ~0ull : ns * 21 / 10;
