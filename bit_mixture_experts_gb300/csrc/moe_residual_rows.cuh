@@ -179,9 +179,11 @@ cudaError_t launch_short(const ResidualArgs& p, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-// Rows of up to 512 channels: lanes of a warp.  More: from two rows per SM on the ring, else a block per row (305
-// rows of 2048 channels 4.3 us in the ring, 304 in blocks 3.7; at 777 rows of 1999 6.3 and 6.7).
-constexpr int SHORT_CHUNKS = 64, RING_MAX_CHUNKS = 2048, RING_MIN_ROWS = 4;
+// Rows of up to 512 channels: lanes of a warp (131072 rows of 384 88 us, in the ring 108).  More: the ring from four
+// rows per SM on (608 rows of 2048 channels 4.0 us in blocks, 4.6 in the ring; 912 5.8 and 5.4; 1216 combined 12.3
+// and 11.5), with rows of over 4096 channels from one on, as an SM holds two blocks of those (200 rows of 8192 7.6 us
+// in blocks, 6.3 in the ring; 912 20 and 13).
+constexpr int SHORT_CHUNKS = 64, WIDE_CHUNKS = 512, RING_MAX_CHUNKS = 2048;
 
 template <bool VEC, bool X32, bool COMBINE>
 cudaError_t launch(const ResidualArgs& p, cudaStream_t s) {
@@ -193,7 +195,7 @@ cudaError_t launch(const ResidualArgs& p, cudaStream_t s) {
     if (chunks <= 32) return launch_short<VEC, X32, COMBINE, 32, 1>(p, s);
     return launch_short<VEC, X32, COMBINE, 32, 2>(p, s);
   }
-  if (chunks <= RING_MAX_CHUNKS && p.T > RING_MIN_ROWS * num_sms()) {
+  if (chunks <= RING_MAX_CHUNKS && p.T > (chunks > WIDE_CHUNKS ? 1 : 4) * num_sms()) {
     bool ran;
     const cudaError_t e = try_ring<VEC, X32, COMBINE>(p, s, &ran);
     if (e != cudaSuccess || ran) return e;
