@@ -310,10 +310,10 @@ def moe_gate(logits, k, gate: Gate, topk_ids, topk_w, stream=None):
 def moe_route_gated(logits, T, E, k, gate: Gate, block_n, topk_ids, topk_w, counts, offsets, perm, inv_perm, block_map,
                     num_blocks, workspace, stream=None):
     """moe_route with the experts chosen by a gate (logits None: topk_ids and topk_w hold the choice)."""
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _call("moe_route_gated", _ptr(logits), T, E, k, gate, block_n, _ptr(topk_ids), _ptr(topk_w), _ptr(counts),
-          _ptr(offsets), _ptr(perm), _ptr(inv_perm), _ptr(block_map), _ptr(num_blocks), _ptr(workspace), ws_bytes,
-          _stream(stream))
+    ws, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.nbytes)
+    _call("moe_route_gated", _ptr(logits), T, E, k, gate, block_n, topk_ids.data_ptr(), topk_w.data_ptr(),
+          counts.data_ptr(), offsets.data_ptr(), perm.data_ptr(), inv_perm.data_ptr(), block_map.data_ptr(),
+          num_blocks.data_ptr(), ws, ws_bytes, _stream(stream))
 
 
 def moe_residual_norm(y, y_stride, T, H, residual: Residual, stream=None):

@@ -170,13 +170,13 @@ struct Scale {
 __device__ __forceinline__ Scale softmax_scale(const float* row, const Lane& me) {
   float top = -INFINITY;
 #pragma unroll 4
-  for (int i = 0; i < me.n; ++i) top = fmaxf(top, available(__ldcg(row + me.first + i)));
+  for (int i = 0; i < me.n; ++i) top = fmaxf(top, available(__ldg(row + me.first + i)));
   __syncwarp();
   top = key_float(__reduce_max_sync(FULL, float_key(top)));
   Pair total = {0.f, 0.f};
 #pragma unroll 2
   for (int i = 0; i < me.n; ++i) {
-    const float l = available(__ldcg(row + me.first + i));
+    const float l = available(__ldg(row + me.first + i));
     if (l != -INFINITY) total = add(total, exp_pair(sum(l, -top)));
   }
   __syncwarp();
@@ -208,7 +208,7 @@ __device__ __forceinline__ bool group_stays(const float* row, const Lane& me, co
   uint64_t c1 = 0, c2 = 0;
 #pragma unroll 2
   for (int i = 0; i < me.n; ++i) {
-    const uint64_t x = value_of<MODE>(available(__ldcg(row + me.first + i)), me.first + i, g, s), lo = min(c1, x);
+    const uint64_t x = value_of<MODE>(available(__ldg(row + me.first + i)), me.first + i, g, s), lo = min(c1, x);
     c1 = max(c1, x);
     c2 = max(c2, lo);
   }
@@ -241,7 +241,7 @@ __device__ __forceinline__ int choose_slowly(const float* row, const Lane& me, b
 #pragma unroll 1
     for (int i = 0; stays && i < me.n; ++i) {
       const int e = me.first + i;
-      const uint64_t x = value_of<MODE>(available(__ldcg(row + e)), e, g, s);
+      const uint64_t x = value_of<MODE>(available(__ldg(row + e)), e, g, s);
       if (x > best && (x < last || (x == last && e > last_e))) {
         best = x;
         at = e;
@@ -303,8 +303,8 @@ struct Units {
   }
 };
 
-// Loads a lane's logits; VEC: they start on 16 bytes and are a multiple of four.  Through L2: the row may
-// have been written by other CTAs of the same kernel.
+// Loads a lane's logits; VEC: they start on 16 bytes and are a multiple of four.  (By way of L1, which has them
+// still when the chosen ones are read again.)
 template <int EPL, bool VEC>
 __device__ __forceinline__ void load_logits(const float* row, const Lane& me, float (&l)[EPL]) {
 #pragma unroll
@@ -313,13 +313,13 @@ __device__ __forceinline__ void load_logits(const float* row, const Lane& me, fl
 #pragma unroll
     for (int i = 0; i < EPL; i += 4)
       if (i < me.n) {
-        const float4 x = __ldcg(reinterpret_cast<const float4*>(row + me.first + i));
+        const float4 x = __ldg(reinterpret_cast<const float4*>(row + me.first + i));
         l[i] = x.x, l[i + 1] = x.y, l[i + 2] = x.z, l[i + 3] = x.w;
       }
   } else {
 #pragma unroll
     for (int i = 0; i < EPL; ++i)
-      if (i < me.n) l[i] = __ldcg(row + me.first + i);
+      if (i < me.n) l[i] = __ldg(row + me.first + i);
   }
 }
 
@@ -363,7 +363,7 @@ __device__ __forceinline__ bool choose_close(const float* row, const uint32_t (&
     if (lane == n) mine = last;
   }
   const int id = min(static_cast<int>(MASK - (mine & MASK)), g.E - 1);
-  const float x = lane < n ? available(__ldcg(row + id)) : -INFINITY;
+  const float x = lane < n ? available(__ldg(row + id)) : -INFINITY;
   const float bias = MODE != BY_LOGIT && g.bias && lane < n ? __ldg(g.bias + id) : 0.f;
   if (!__all_sync(FULL, fabsf(bias) < INFINITY)) return false;
   Pair v = {x, 0.f};
@@ -474,11 +474,20 @@ __device__ __forceinline__ Made make_keys(const float (&l)[EPL], const Units<EPL
   return made;
 }
 
+// The logits of tokens t .. t + BATCH - 1 (the last one again for those from T on).
+template <int EPL, int BATCH, bool WHOLE>
+__device__ __forceinline__ void load_tokens(const float* logits, int t, int T, const Gate& g, const Lane& me,
+                                            float (&l)[BATCH][EPL]) {
+#pragma unroll
+  for (int b = 0; b < BATCH; ++b) load_logits<EPL, WHOLE>(logits + static_cast<size_t>(min(t + b, T - 1)) * g.E, me, l[b]);
+}
+
 // Tokens t .. t + BATCH - 1 (those below T) by one warp: lane i (32 / BATCH) + j ends with the j-th choice of
-// token t + i and its weight.  WHOLE: every lane has EPL experts, which start on 16 bytes.
+// token t + i and its weight.  l: load_tokens'.  WHOLE: every lane has EPL experts, which start on 16 bytes.
 template <int EPL, int IDX, Mode MODE, int BATCH, bool WHOLE>
-__device__ __forceinline__ void warp_gate(const float* logits, int t, int T, const Units<EPL, IDX, MODE>& u, const Gate& g,
-                                          const Lane& me, int lane, int* id_out, float* w_out) {
+__device__ __forceinline__ void warp_gate(const float* logits, int t, int T, const float (&l)[BATCH][EPL],
+                                          const Units<EPL, IDX, MODE>& u, const Gate& g, const Lane& me, int lane,
+                                          int* id_out, float* w_out) {
   constexpr uint32_t MASK = (1u << IDX) - 1u, OUT = not_available_m<IDX, MODE>();
   constexpr int SEG = 32 / BATCH;
   const int ti = lane / SEG, tj = lane % SEG;  // whose choice this lane ends with
@@ -488,9 +497,6 @@ __device__ __forceinline__ void warp_gate(const float* logits, int t, int T, con
   uint32_t c1 = 0, c2 = 0;  // the two largest keys of this lane's group, of token (lane modulo BATCH)
   const bool drop = g.top_groups < g.groups;
   {
-    float l[BATCH][EPL];
-#pragma unroll
-    for (int b = 0; b < BATCH; ++b) load_logits<EPL, WHOLE>(logits + static_cast<size_t>(min(t + b, T - 1)) * g.E, me, l[b]);
 #pragma unroll
     for (int b = 0; b < BATCH; ++b) {
       const Made made = make_keys<EPL, IDX, MODE, WHOLE>(l[b], u, g, me, key[b]);
@@ -597,13 +603,13 @@ __device__ __forceinline__ void warp_gate(const float* logits, int t, int T, con
     if (next >> IDX > OUT && (last >> IDX) - (next >> IDX) <= near[b]) {
       const float* row = logits + static_cast<size_t>(min(t + b, T - 1)) * g.E;
       const int idk = min(static_cast<int>(MASK - (last & MASK)), g.E - 1);
-      const float xk = available(__ldcg(row + idk)), bk = g.bias ? __ldg(g.bias + idk) : 0.f;
+      const float xk = available(__ldg(row + idk)), bk = g.bias ? __ldg(g.bias + idk) : 0.f;
       bool alike = true;
 #pragma unroll
       for (int i = 0; i < EPL; ++i) {
         const uint32_t x = key[b][i];
         if (x >= last || x >> IDX <= OUT || (last >> IDX) - (x >> IDX) > near[b]) continue;
-        const float xi = available(__ldcg(row + me.first + i)), bi = g.bias ? __ldg(g.bias + me.first + i) : 0.f;
+        const float xi = available(__ldg(row + me.first + i)), bi = g.bias ? __ldg(g.bias + me.first + i) : 0.f;
         if (!(xi == xk && bi == bk)) alike = false;
       }
       if (!__all_sync(FULL, alike)) close |= 1u << b;
@@ -612,7 +618,7 @@ __device__ __forceinline__ void warp_gate(const float* logits, int t, int T, con
   }
   int id = min(static_cast<int>(MASK - (chosen & MASK)), g.E - 1);
   const float* row = logits + static_cast<size_t>(min(t + ti, T - 1)) * g.E;
-  float x = tj < g.k ? available(__ldcg(row + id)) : -INFINITY;
+  float x = tj < g.k ? available(__ldg(row + id)) : -INFINITY;
   // ---- neighbours in the choice
   {
     const uint32_t m = chosen >> IDX, m2 = __shfl_down_sync(FULL, m, 1);
@@ -635,10 +641,10 @@ __device__ __forceinline__ void warp_gate(const float* logits, int t, int T, con
       const int b = __ffs(left) - 1;
       const float* at = logits + static_cast<size_t>(t + b) * g.E;
       // (its keys anew: those of groups that do not stay are gone)
-      float l[EPL];
+      float again[EPL];
       uint32_t own[EPL];
-      load_logits<EPL, WHOLE>(at, me, l);
-      const Made made = make_keys<EPL, IDX, MODE, WHOLE>(l, u, g, me, own);
+      load_logits<EPL, WHOLE>(at, me, again);
+      const Made made = make_keys<EPL, IDX, MODE, WHOLE>(again, u, g, me, own);
       bool in = stays >> b & 1u;
       // softmax: with 1 / sum as it is first, unless the groups need it exact anyway
       Scale scale = {made.top, {made.inv, 0.f}};
@@ -662,7 +668,7 @@ __device__ __forceinline__ void warp_gate(const float* logits, int t, int T, con
       const int mine = __shfl_sync(FULL, e, tj);
       if (ti == b) id = min(max(mine, 0), g.E - 1);
     }
-    if (tj < g.k) x = available(__ldcg(row + id));
+    if (tj < g.k) x = available(__ldg(row + id));
   }
   // ---- weights
   float z = 0.f;

@@ -14,6 +14,11 @@ from . import _lib
 Routing = collections.namedtuple("Routing", "topk_ids topk_w counts offsets perm inv_perm block_map num_blocks")
 
 
+def _current_device():
+    """torch.cuda.current_device(), whose check that CUDA is initialised the tensors at hand make needless."""
+    return torch._C._cuda_getDevice()
+
+
 def _on(stream, device):
     """A `with` block in which `stream`, a torch stream or a raw handle, is the current one."""
     if isinstance(stream, int):
@@ -73,8 +78,8 @@ class ExpertGate:
             raise ValueError(f"logits must be contiguous float32 [T, E] on a CUDA device: got {logits.dtype} "
                              f"{tuple(logits.shape)}, strides {logits.stride()}, on {logits.device}")
         self.check(logits.shape[1], logits.device)
-        if torch.cuda.current_device() != logits.device.index:
-            raise ValueError(f"the logits are on {logits.device}, but device {torch.cuda.current_device()} is the current one")
+        if _current_device() != logits.get_device():
+            raise ValueError(f"the logits are on {logits.device}, but device {_current_device()} is the current one")
 
     def choose(self, logits, out=None, stream=None):
         """logits float32 [T, E] -> (int32 [T, k], float32 [T, k]), or into `out`, a pair of such tensors."""
@@ -83,7 +88,8 @@ class ExpertGate:
         if out is None:
             out = _empty(shape, torch.int32, dev, stream), _empty(shape, torch.float32, dev, stream)
         else:
-            for t, dtype in zip(out, (torch.int32, torch.float32)):
+            ids, w = out
+            for t, dtype in (ids, torch.int32), (w, torch.float32):
                 if t.dtype != dtype or t.shape != shape or t.device != dev or not t.is_contiguous():
                     raise ValueError(f"out must be contiguous int32 and float32 {shape} on {dev}: got {t.dtype} "
                                      f"{tuple(t.shape)} on {t.device}, strides {t.stride()}")

@@ -12,18 +12,18 @@ from __future__ import annotations
 import torch
 
 from . import _lib
-from .gate import _empty
+from .gate import _current_device, _empty
 
 _F32 = {torch.bfloat16: 0, torch.float32: 1}
-_current_device = torch.cuda.current_device
 
 
 def _row_stride(t, name, dtype, shape, device):
     """The distance of t's rows, which must be contiguous and as the others'."""
-    if t.shape != shape or t.dtype != dtype or t.device != device or (t.stride(1) != 1 and shape[1] > 1):
+    strides = t.stride()
+    if t.shape != shape or t.dtype != dtype or t.device != device or (strides[1] != 1 and shape[1] > 1):
         raise ValueError(f"{name} must be {dtype} {tuple(shape)} on {device} with contiguous rows: got {t.dtype} "
-                         f"{tuple(t.shape)} on {t.device}, strides {t.stride()}")
-    return t.stride(0)
+                         f"{tuple(t.shape)} on {t.device}, strides {strides}")
+    return strides[0]
 
 
 class ResidualNorm:
