@@ -83,9 +83,10 @@ __device__ __forceinline__ int ld_acquire(const int* p) {
 // then in assignment order, as moe_route's stable scatter -- and a tile
 // starts wherever the expert changes along the sorted rows (found by warp 0);
 // the shared expert's T rows follow as one tile.  s_ok receives the number
-// of routed tiles.
+// of routed tiles.  bn: the longest run that is one tile; a longer one, which only
+// a choice that names an expert twice for a token can have, is cut every bn rows.
 __device__ __noinline__ void route_small_batch(const int* s_ids, int* s_inv, int* s_tok, int* s_sorted,
-                                               int (*s_tile)[3], int* s_ok, int A, int T, int E, int k) {
+                                               int (*s_tile)[3], int* s_ok, int A, int T, int E, int k, int bn) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int a = 32 * warp + lane;
   if (a < A) {
@@ -106,6 +107,17 @@ __device__ __noinline__ void route_small_batch(const int* s_ids, int* s_inv, int
     const int r = lane + 32 * q;
     const bool st = r < A && (r == 0 || s_sorted[r] != s_sorted[r - 1]);
     starts |= static_cast<unsigned long long>(__ballot_sync(0xffffffffu, st)) << (32 * q);
+  }
+  if (bn < A) {
+    unsigned long long cuts = 0;
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const int r = lane + 32 * q;
+      const int first = 63 - __clzll(static_cast<long long>(starts & (~0ull >> (63 - r))));  // of r's run (row 0 is one)
+      const bool st = r < A && (r - first) % bn == 0;
+      cuts |= static_cast<unsigned long long>(__ballot_sync(0xffffffffu, st)) << (32 * q);
+    }
+    starts = cuts;
   }
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
@@ -232,12 +244,12 @@ __global__ void __launch_bounds__(GV_THREADS, GV_CTAS_PER_SM) decode_kernel(cons
       s_w[warp * k + lane] = w;
     }
   }
-  // Small batches (at most 64 assignments, every expert's rows in one tile):
+  // Small batches (at most 64 assignments, a token's rows of distinct experts in one tile each):
   // two warps rank the assignments and read the tiles off the sorted rows,
   // with no pass over all E experts (the same result as the general path).
   if (A <= 64 && T <= bn) {
     __syncthreads();  // s_ids
-    if (warp < 2) route_small_batch(s_ids, s_inv, s_tok, s_sorted, s_tile, &s_ok, A, T, E, k);
+    if (warp < 2) route_small_batch(s_ids, s_inv, s_tok, s_sorted, s_tile, &s_ok, A, T, E, k, p.logits ? A : bn);
     if (blockIdx.x == 0) {  // counts and offsets of every expert, for moe_route's outputs
       for (int e = tid; e < E; e += GV_THREADS) {
         int c = 0, o = 0;

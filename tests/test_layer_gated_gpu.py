@@ -118,6 +118,44 @@ def test_a_layer_without_a_gate_takes_what_follows_too():
         check_rows(n, want[1], want[3], STEP["bf16"], "n")
 
 
+@pytest.mark.parametrize("T,k,impl", [(1, 4, "auto"), (2, 8, "auto"), (3, 5, "gemv"), (8, 4, "auto"), (8, 8, "auto"), (8, 10, "auto"),
+                                      (12, 4, "gemv"), (100, 4, "auto"), (700, 4, "tc")])
+def test_a_choice_that_names_an_expert_twice(T, k, impl):
+    """Rows of their own, each with the values that the expert's row has where the others differ: an expert may then
+    have more rows than there are tokens."""
+    import torch
+
+    from bit_mixture_experts_gb300 import ResidualNorm
+    from oracle import moe_ref
+    _, layer, x, _ = make(T, impl, k=k)
+    b = layer.buffers(T)
+    w = torch.rand((T, k), generator=torch.Generator().manual_seed(T)).cuda()
+    norm = ResidualNorm()
+
+    def run(ids):
+        ids = ids.int().cuda()
+        b["y"].fill_(float("nan"))
+        r, n = layer.forward_residual(x, None, x, norm, choice=(ids, w))
+        no_error()
+        for name, want in zip(("counts", "offsets", "perm", "inv_perm"), gate_ref.sort_assignments(ids.cpu().numpy(), 64)):
+            np.testing.assert_array_equal(b[name].cpu().numpy().ravel(), want, err_msg=name)
+        tiles = moe_ref.block_map(b["counts"].cpu().numpy(), b["offsets"].cpu().numpy(), T, layer.block_n_for(T))
+        assert int(b["num_blocks"]) == len(tiles)
+        np.testing.assert_array_equal(b["block_map"][:len(tiles)].cpu().numpy(), tiles)
+        y, size = gate_ref.combined(f64(b["y"]), b["inv_perm"].cpu().numpy(), f64(w))
+        want = gate_ref.residual(f64(x), y, None, None, None, norm.scale, norm.eps, norm.offset, y_size=size, terms=k + 1)
+        check_rows(r, want[0], want[2], STEP["bf16"], "r")
+        check_rows(n, want[1], want[3], STEP["bf16"], "n")
+        return b["y"][b["inv_perm"].long()].view(T, k, -1)
+
+    first = run((torch.arange(k) + 3).expand(T, k))
+    for ids, same_as_first in ((torch.full((T, k), 3), range(k)), ((torch.arange(k) // 2 * 2 + 3).expand(T, k), range(0, k, 2)),
+                               (torch.where(torch.arange(k) < 2, 3, torch.arange(k) + 20).expand(T, k), (0, 1))):
+        y = run(ids)
+        for j in same_as_first:
+            assert torch.equal(y[:, j], first[:, ids[0, j] - 3]), j
+
+
 def test_choices_out_of_range_are_reported():
     """Decode and prefill: an expert that does not exist is an error, not an access out of range."""
     import torch
