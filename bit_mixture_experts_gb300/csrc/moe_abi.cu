@@ -153,6 +153,17 @@ bool overlap(const Rows& a, const Rows& b) {
   return d < a.len || d + b.len > a.stride;
 }
 
+// A gate's choice must lie apart from what it is made of: other tokens' logits are read while it is written.
+int check_gate_overlap(const float* logits, int T, int E, int k, const moe_gate_t* g, const int32_t* ids, const float* w) {
+  const Rows out[2] = {rows_of(ids, 0, static_cast<long long>(T) * k, 4, 1), rows_of(w, 0, static_cast<long long>(T) * k, 4, 1)};
+  const Rows in[2] = {rows_of(logits, 0, static_cast<long long>(T) * E, 4, 1), rows_of(g->bias, 0, E, 4, 1)};
+  if (overlap(out[0], out[1])) return MOE_ERR_OVERLAP;
+  for (const Rows& o : out)
+    for (const Rows& i : in)
+      if (overlap(o, i)) return MOE_ERR_OVERLAP;
+  return MOE_OK;
+}
+
 bool same(const Rows& a, const Rows& b) { return a.at == b.at && a.stride == b.stride && a.len == b.len && a.n == b.n; }
 
 bool aligned(const void* p, int size) { return reinterpret_cast<uintptr_t>(p) % size == 0; }
@@ -210,6 +221,16 @@ int residual_args(const uint16_t* y, long long y_stride, long long y_rows, bool 
   a->post = y && p->post;
   a->param_f32 = p->param_f32 != 0;
   a->gate_f32 = p->gate_f32 != 0;
+  return MOE_OK;
+}
+
+// The outputs lie apart from the combine's places and weights.
+int check_places_overlap(const int32_t* inv_perm, const float* topk_w, int T, int H, int k, const moe_residual_t* p) {
+  const Rows r = rows_of(p->r, p->r_stride, H, p->stream_f32 ? 4 : 2, T), n = rows_of(p->n, p->n_stride, H, 2, T);
+  for (const void* i : {static_cast<const void*>(inv_perm), static_cast<const void*>(topk_w)}) {
+    const Rows in = rows_of(i, 0, static_cast<long long>(T) * k, 4, 1);
+    if (overlap(in, r) || overlap(in, n)) return MOE_ERR_OVERLAP;
+  }
   return MOE_OK;
 }
 
@@ -340,7 +361,7 @@ int moe_gate(const float* logits, int T, int E, int k, const moe_gate_t* gate, i
   if (rc || (rc = check_gate(gate, E, k))) return rc;
   if (T == 0) return MOE_OK;
   rc = check_ptrs(logits, topk_ids, topk_w);
-  if (rc) return rc;
+  if (rc || (rc = check_gate_overlap(logits, T, E, k, gate, topk_ids, topk_w))) return rc;
   return cuda_status(launch_gate(logits, T, gate, E, k, topk_ids, topk_w, reinterpret_cast<cudaStream_t>(stream)));
 }
 
@@ -359,6 +380,7 @@ int moe_route_gated(const float* logits, int T, int E, int k, const moe_gate_t* 
     rc = check_ptrs(workspace);
     if (rc) return rc;
   }
+  if (logits && (rc = check_gate_overlap(logits, T, E, k, gate, topk_ids, topk_w))) return rc;
   if (!device_error_ptr()) return MOE_ERR_CUDA;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (logits && (rc = cuda_status(launch_gate(logits, T, gate, E, k, topk_ids, topk_w, s)))) return rc;
@@ -382,11 +404,7 @@ int moe_combine_residual_norm(const uint16_t* y, const int32_t* inv_perm, const 
   if (rc || T == 0) return rc;
   rc = check_ptrs(y, inv_perm, topk_w);
   if (rc) return rc;
-  const Rows r = rows_of(p->r, p->r_stride, H, p->stream_f32 ? 4 : 2, T), n = rows_of(p->n, p->n_stride, H, 2, T);
-  for (const void* i : {static_cast<const void*>(inv_perm), static_cast<const void*>(topk_w)}) {
-    const Rows in = rows_of(i, 0, static_cast<long long>(T) * k, 4, 1);
-    if (overlap(in, r) || overlap(in, n)) return MOE_ERR_OVERLAP;
-  }
+  if ((rc = check_places_overlap(inv_perm, topk_w, T, H, k, p))) return rc;
   a.inv_perm = inv_perm;
   a.topk_w = topk_w;
   a.k = k;
@@ -585,9 +603,11 @@ int moe_layer_forward_gated(const uint16_t* x, const float* logits, const moe_ga
   if (residual) {
     ResidualArgs a;
     if ((rc = check_ptrs(b->y)) || (rc = residual_args(b->y, H, (k + 1ll) * T, true, T, H, residual, &a))) return rc;
+    if ((rc = check_places_overlap(b->inv_perm, b->topk_w, T, H, k, residual))) return rc;
   } else if ((rc = check_ptrs(out))) {
     return rc;
   }
+  if (logits && (rc = check_gate_overlap(logits, T, E, k, gate, b->topk_ids, b->topk_w))) return rc;
   return layer_forward(x, logits, true, gate, out, residual, T, H, F, E, k, block_n, impl, w, b, stream);
 }
 

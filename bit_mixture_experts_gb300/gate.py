@@ -34,7 +34,18 @@ def _empty(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-class ExpertGate:
+class Fixed:
+    """An object whose description the library has been given: its public attributes keep their values.  (The memory
+    of a tensor put in another's place would not be what the calls read.)"""
+
+    def __setattr__(self, name, value):
+        if name[0] != "_" and name in self.__dict__:
+            raise AttributeError(f"{type(self).__name__}.{name} is fixed: make another {type(self).__name__}, or change a "
+                                 "tensor's values in place")
+        super().__setattr__(name, value)
+
+
+class ExpertGate(Fixed):
     """Chooses k experts of a token by score plus bias, of the groups that stay, and weighs them by score.
 
     score    "softmax" (over all experts) or "sigmoid" of the logits

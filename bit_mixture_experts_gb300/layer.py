@@ -59,7 +59,10 @@ class MoELayerW4:
         if gate is not None:
             if gate.k != k:
                 raise ValueError(f"the gate chooses {gate.k} experts a token, the layer takes {k}")
-            gate.check(E, gate.bias.device if gate.bias is not None else self.device)
+            here = self.device
+            if gate.bias is not None and here == torch.device("cuda"):
+                here = torch.device("cuda", torch.cuda.current_device())
+            gate.check(E, here)
         self.gate = gate
         self.block_n = block_n  # None: chosen per token count by default_block_n
         # tensor-core path: the combine in the down GEMM's epilogue (moe_down_combine) instead of its own

@@ -12,7 +12,7 @@ from __future__ import annotations
 import torch
 
 from . import _lib
-from .gate import _current_device, _empty
+from .gate import Fixed, _current_device, _empty
 
 _F32 = {torch.bfloat16: 0, torch.float32: 1}
 
@@ -26,7 +26,7 @@ def _row_stride(t, name, dtype, shape, device):
     return strides[0]
 
 
-class ResidualNorm:
+class ResidualNorm(Fixed):
     """w_pre, w_post: bf16 or float32 [H] (both of one type); w_post None: the block's output is not normed, w_pre None:
     gains of 1.  The stream x is bf16 or float32, r has its type; y and n are bf16.  Tensors are [T, H] with rows of any
     stride; r may be x's or y's memory and n x's or y's, where type and strides are the same."""

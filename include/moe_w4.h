@@ -53,7 +53,7 @@ enum {
   MOE_ERR_DEVICE = -6,    /* moe_get_device_error found a kernel-side fault */
   MOE_ERR_MODE = -7,      /* unknown mode or variant */
   MOE_ERR_OVERLAP = -8    /* an output shares memory with an input or another output in a way that the
-                             call cannot take (moe_residual_norm, moe_combine_residual_norm) */
+                             call cannot take (gates, moe_residual_norm, moe_combine_residual_norm) */
 };
 
 /* Device error word values (written by kernels, read by moe_get_device_error). */
@@ -261,7 +261,8 @@ typedef struct {
 /*
  * moe_gate -- topk_ids int32 [T, k] and topk_w float32 [T, k] of router logits
  * float32 [T, E].  T = 0 does nothing.  MOE_ERR_MODE for an unknown score,
- * MOE_ERR_SHAPE for groups outside the limits.  One launch.
+ * MOE_ERR_SHAPE for groups outside the limits, MOE_ERR_OVERLAP where topk_ids
+ * or topk_w share memory with each other, the logits or the bias.  One launch.
  */
 int moe_gate(const float* logits, int T, int E, int k, const moe_gate_t* gate, int32_t* topk_ids, float* topk_w,
              moe_stream_t stream);
@@ -269,8 +270,9 @@ int moe_gate(const float* logits, int T, int E, int k, const moe_gate_t* gate, i
 /*
  * moe_route_gated -- moe_route with the experts chosen by a gate: the same
  * outputs, workspace and limits.  With logits NULL the experts are those that
- * topk_ids and topk_w hold (`gate` is not read; an id outside [0, E) is taken
- * as one inside it, and sets MOE_DEV_BAD_INDEX where T * k > 1024).
+ * topk_ids and topk_w hold (`gate` is not read; a token may name an expert more
+ * than once, which are then rows of their own; an id outside [0, E) is taken as
+ * one inside it, and sets MOE_DEV_BAD_INDEX where T * k > 1024).
  */
 int moe_route_gated(const float* logits, int T, int E, int k, const moe_gate_t* gate, int block_n, int32_t* topk_ids,
                     float* topk_w, int32_t* counts, int32_t* offsets, int32_t* perm, int32_t* inv_perm,
@@ -287,7 +289,9 @@ int moe_route_gated(const float* logits, int T, int E, int k, const moe_gate_t* 
  *   z = y / rms(y) * (w_post + offset)  if post, else y    rms(v) = sqrt(mean v^2 + eps)
  *   r = scale x + gate z                the stream's next value
  *   n = r / rms(r) * (w_pre + offset)   what the next block takes
- * The sums run in FP32, n is taken of the unrounded r, r and n are rounded once.
+ * The sums run in FP32 (values beyond about 1e19 / sqrt(H) have squares that it
+ * does not hold: rms is then infinite), n is taken of the unrounded r, r and n
+ * are rounded once.
  * A tensor's rows are H consecutive elements and its strides count elements;
  * pointers need only their elements' alignment (rows on 16 bytes are read
  * faster; others are read with what lies around them in the same 16 bytes).  An

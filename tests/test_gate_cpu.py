@@ -147,6 +147,21 @@ def test_gate_argument_errors(lib, route):
         assert call(T=0, ptr=None) == 0  # does nothing
 
 
+@pytest.mark.parametrize("route", [False, True])
+def test_a_gates_outputs_lie_apart(lib, route):
+    """T 8, E 16, k 2: logits 512 bytes, ids and weights 64, bias 64."""
+    from bit_mixture_experts_gb300 import _lib
+
+    def call(logits=BASE, ids=2 * BASE, w=3 * BASE, bias=4 * BASE, **kw):
+        g = _lib.Gate(bias, 1, 1, 1, 1, 1, 1.0)
+        if not route:
+            return lib.moe_gate(logits, 8, 16, 2, g, ids, w, None)
+        return lib.moe_route_gated(logits, 8, 16, 2, g, 64, ids, w, *([9 * BASE] * 6), 9 * BASE, 1 << 20, None)
+    assert call(ids=BASE) == -8 and call(w=BASE + 512 - 16) == -8 and call(ids=BASE - 48) == -8
+    assert call(ids=3 * BASE) == -8 and call(w=2 * BASE + 48) == -8
+    assert call(w=4 * BASE) == -8 and call(ids=4 * BASE + 48) == -8 and call(bias=3 * BASE - 60) == -8
+
+
 BASE = 1 << 20  # addresses that no call gets to follow
 
 
@@ -257,3 +272,16 @@ def test_python_checks():
         ResidualNorm().norm(torch.zeros((2, 8)))
     with pytest.raises(ValueError, match="x must be"):
         ResidualNorm().add(torch.zeros(8), torch.zeros(8))
+
+
+def test_what_the_library_was_told_is_fixed():
+    """A tensor put in a gain's or a bias's place would not be read: the calls would go on with the old one's memory."""
+    import torch
+
+    from bit_mixture_experts_gb300 import ExpertGate, ResidualNorm
+    gate, norm = ExpertGate(2), ResidualNorm(scale=0.5)
+    for obj, name in [(gate, n) for n in ("bias", "k", "scale", "renorm", "score", "groups", "top_groups", "group_score")] + [
+            (norm, n) for n in ("w_pre", "w_post", "scale", "eps", "offset")]:
+        with pytest.raises(AttributeError, match="fixed"):
+            setattr(obj, name, torch.zeros(8))
+    assert gate.bias is None and norm.scale == 0.5
