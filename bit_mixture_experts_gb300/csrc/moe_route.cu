@@ -14,6 +14,7 @@
 //   route_fused_kernel   one CTA per chunk of tokens, one cooperative launch:
 //                        top-k and chunk counts | grid barrier | totals, scan,
 //                        block map | stable scatter (ranks with warp match)
+//   route_given_kernel   (moe_route_given.cu) the same for experts chosen already
 #include "moe_common.cuh"
 #include "moe_route_dev.cuh"
 
@@ -125,7 +126,7 @@ __global__ void __launch_bounds__(256) route_fused_kernel(const float* __restric
                                                           int32_t* cc, int* ctr, int32_t* counts, int32_t* offsets,
                                                           int32_t* perm, int32_t* inv_perm, int32_t* block_map,
                                                           int32_t* num_blocks, int cap, int* err,
-                                                          unsigned long long wait_cycles, int ids_given) {
+                                                          unsigned long long wait_cycles) {
   extern __shared__ int smem_i[];
   int* s_hist = smem_i;        // [E] chunk counts, then the chunk's next free row per expert
   int* s_wc = smem_i + E;      // [8][E] per-warp group sizes
@@ -142,15 +143,6 @@ __global__ void __launch_bounds__(256) route_fused_kernel(const float* __restric
   for (int t = t0 + warp; t < t1; t += 8) {
     int id;
     float w;
-    if (ids_given) {  // top-k already chosen (moe_route_x): take the ids
-      id = lane < k ? __ldg(topk_ids + static_cast<size_t>(t) * k + lane) : 0;
-      if (id < 0 || id >= E) {
-        set_device_error(err, MOE_DEV_BAD_INDEX);
-        id = 0;
-      }
-      if (lane < k) atomicAdd(&s_hist[id], 1);
-      continue;
-    }
     warp_topk_any(logits + static_cast<size_t>(t) * E, E, k, lane, &id, &w);
     if (lane < k) {
       topk_ids[static_cast<size_t>(t) * k + lane] = id;
@@ -308,7 +300,11 @@ size_t route_workspace_bytes(int T, int E, int k) {
 }
 
 unsigned long long wait_limit_ns();
+cudaError_t launch_route_given(const int32_t* ids, int T, int E, int k, int least, int bn, int32_t* counts,
+                               int32_t* offsets, int32_t* perm, int32_t* inv_perm, int32_t* bm, int32_t* nb, void* ws,
+                               size_t ws_bytes, cudaStream_t s);
 
+// ids_given: the experts are those of ids, which is not written (nor are logits and w read).
 cudaError_t launch_route(const float* logits, int T, int E, int k, int bn, int32_t* ids, float* w,
                          int32_t* counts, int32_t* offsets, int32_t* perm, int32_t* inv_perm, int32_t* bm,
                          int32_t* nb, void* ws, size_t ws_bytes, cudaStream_t s, int ids_given) {
@@ -325,6 +321,7 @@ cudaError_t launch_route(const float* logits, int T, int E, int k, int bn, int32
     return cudaGetLastError();
   }
   const int tc = route_chunk_tokens(T);
+  if (ids_given) return launch_route_given(ids, T, E, k, tc * k, bn, counts, offsets, perm, inv_perm, bm, nb, ws, ws_bytes, s);
   const int nch = ceil_div(T, tc);
   int32_t* cc = static_cast<int32_t*>(ws);
   int* ctr = reinterpret_cast<int*>(static_cast<char*>(ws) + ((ws_bytes - 16) & ~static_cast<size_t>(3)));
@@ -348,7 +345,7 @@ cudaError_t launch_route(const float* logits, int T, int E, int k, int bn, int32
   cfg.numAttrs = 1;
   const int cap = moe_block_map_capacity(T, E, k, bn);
   cudaError_t e = cudaLaunchKernelEx(&cfg, route_fused_kernel, logits, T, E, k, tc, bn, ids, w, cc, ctr, counts,
-                                     offsets, perm, inv_perm, bm, nb, cap, err, wait_cycles, ids_given);
+                                     offsets, perm, inv_perm, bm, nb, cap, err, wait_cycles);
   note_launches(1);
   return e != cudaSuccess ? e : cudaGetLastError();
 }

@@ -3,7 +3,7 @@ weights within the error of their FP32 arithmetic."""
 import numpy as np
 import pytest
 
-from oracle import gate_ref
+from oracle import gate_ref, moe_ref
 
 pytestmark = pytest.mark.gpu
 
@@ -159,6 +159,44 @@ def test_softmax_gate_is_moe_route():
         for name, a, b in zip(got._fields, got, ref):
             a, b = (a[:n], b[:n]) if name == "block_map" else (a, b)
             assert torch.equal(a, b), name
+
+
+@pytest.mark.parametrize("T,E,k,block_n,how", [
+    (33, 40, 32, 8, "any"), (1023, 256, 8, 64, "any"), (1024, 256, 8, 64, "one"), (2047, 7, 4, 16, "twice"),
+    (4096, 600, 2, 32, "any"), (9000, 1024, 1, 128, "any"), (16383, 256, 8, 64, "few"), (16384, 256, 8, 64, "any"),
+    (70001, 33, 5, 8, "few"), (140000, 64, 1, 64, "one")])
+def test_route_of_experts_chosen_already(T, E, k, block_n, how):
+    """Around the sizes where the rounds of a chunk begin and its CTAs change; experts without any and with all tokens."""
+    import torch
+
+    from bit_mixture_experts_gb300 import _lib
+    rng = np.random.default_rng(T)
+    ids = rng.integers(0, E, (T, k))
+    if how == "one":
+        ids[:] = E - 1
+    if how == "twice":
+        ids[:, 1:] = ids[:, :1]
+    if how == "few":
+        ids = np.where(rng.random((T, k)) < 0.9, E // 2, ids)
+    dev = "cuda"
+    want = gate_ref.sort_assignments(ids, E)
+    tiles = moe_ref.block_map(want[0], want[1], T, block_n)
+    given = torch.from_numpy(ids.astype(np.int32)).to(dev)
+    w = torch.full((T, k), 7.0, device=dev)
+    out = [torch.full(n, -9, dtype=torch.int32, device=dev) for n in
+           ((E,), (E + 1,), (T * k,), (T * k,), (_lib.moe_block_map_capacity(T, E, k, block_n), 3), (1,))]
+    ws = torch.zeros(_lib.moe_route_workspace_size(T, E, k, block_n), dtype=torch.uint8, device=dev)
+    for _ in range(2):  # the second call finds the scratch as the first left it
+        _lib.moe_route_gated(None, T, E, k, None, block_n, given, w, *out, ws)
+    torch.cuda.synchronize()
+    assert _lib.moe_get_device_error() == 0
+    for name, got, ref in zip(("counts", "offsets", "perm", "inv_perm"), out, want):
+        np.testing.assert_array_equal(got.cpu().numpy(), ref, err_msg=name)
+    assert int(out[5]) == len(tiles)
+    got = out[4].cpu().numpy()
+    np.testing.assert_array_equal(got[:len(tiles)], tiles)
+    assert (got[len(tiles):] == -9).all()
+    assert (given.cpu().numpy() == ids).all() and (w == 7).all()
 
 
 @pytest.mark.parametrize("T,E,k,block_n", [(1, 256, 8, 8), (100, 64, 4, 16), (129, 64, 8, 64), (3000, 256, 8, 64)])
