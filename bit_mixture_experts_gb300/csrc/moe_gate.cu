@@ -1,6 +1,7 @@
 // Router logits to experts and weights (moe_gate; see moe_gate_dev.cuh for the
 // choice itself).
 #include "moe_gate_dev.cuh"
+#include "moe_launch.cuh"
 
 namespace moe {
 
@@ -21,6 +22,7 @@ __global__ void __launch_bounds__(32 * GATE_WARPS, BATCH == 4 ? 3 : 1) gate_kern
                                                                const __grid_constant__ Gate g, int32_t* ids, float* w) {
   constexpr int SEG = 32 / BATCH;
   const int lane = threadIdx.x & 31;
+  wait_for_earlier();
   int t = (static_cast<int>(blockIdx.x) * GATE_WARPS + (threadIdx.x >> 5)) * BATCH;
   const int step = static_cast<int>(gridDim.x) * GATE_WARPS * BATCH;
   if (t >= T) return;
@@ -52,9 +54,9 @@ cudaError_t launch(const float* logits, int T, const Gate& g, int32_t* ids, floa
   int per_sm = 0;
   const cudaError_t e = cached_occupancy(reinterpret_cast<const void*>(kernel), 32 * GATE_WARPS, 0, &per_sm);
   if (e != cudaSuccess) return e;
-  kernel<<<min(ceil_div(T, GATE_WARPS * BATCH), num_sms() * per_sm), 32 * GATE_WARPS, 0, s>>>(logits, T, g, ids, w);
   note_launches(1);
-  return cudaGetLastError();
+  return launch_early(kernel, min(ceil_div(T, GATE_WARPS * BATCH), num_sms() * per_sm), 32 * GATE_WARPS, 0, s, logits, T, g,
+                      ids, w);
 }
 
 template <int EPL, int IDX, Mode MODE, bool WHOLE>

@@ -16,6 +16,7 @@
 // way of shared memory, in whole pieces, the outputs took two barriers more:
 // 253 us).
 #pragma once
+#include "moe_launch.cuh"
 #include "moe_ptx.cuh"
 #include "moe_residual_dev.cuh"
 
@@ -126,6 +127,7 @@ __global__ void __launch_bounds__(NT, ring_blocks(CH, NT))
   }
   if (tid < 64) s_sum[tid >> 5][tid >> 4 & 1][tid & 15] = 0.f;
   __syncthreads();
+  wait_for_earlier();
 
   if (tid >= threads) {
     // ------------------------------------------------ copies, a lane per row of a token's y
@@ -386,9 +388,8 @@ cudaError_t launch_ring(const ResidualArgs& p, Ring g, int threads, cudaStream_t
   if (e == cudaSuccess) e = cached_occupancy(reinterpret_cast<const void*>(kernel), threads + 32, smem, &per_sm);
   if (e != cudaSuccess) return e;
   if (per_sm < 1) return cudaErrorInvalidValue;
-  kernel<<<min(p.T, num_sms() * per_sm), threads + 32, smem, s>>>(p, g);
   note_launches(1);
-  return cudaGetLastError();
+  return launch_early(kernel, min(p.T, num_sms() * per_sm), threads + 32, smem, s, p, g);
 }
 
 // Runs the ring if it holds two stages; *ran tells.

@@ -14,6 +14,7 @@ __global__ void __launch_bounds__(1024) row_kernel(const __grid_constant__ Resid
   constexpr int XS = X32 ? 4 : 2;
   const int tid = threadIdx.x, threads = blockDim.x, warps = threads >> 5, t = blockIdx.x, H = p.H;
   const bool add = COMBINE || p.y;
+  wait_for_earlier();
   auto row_sum = [&](float v, float* s) {
 #pragma unroll
     for (int m = 16; m >= 1; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
@@ -101,6 +102,7 @@ __global__ void __launch_bounds__(256, COMBINE ? 2 : 4) short_kernel(const __gri
   const bool add = COMBINE || p.y;
   const float inv_h = 1.0f / static_cast<float>(H);
   constexpr bool KEEP = CH == 1;  // the gains in registers
+  wait_for_earlier();
   float ga[8], gb[8];
   if (KEEP) {
     gains_y<VEC>(p, 0, tid, LANES, ga);
@@ -174,9 +176,8 @@ cudaError_t launch_short(const ResidualArgs& p, cudaStream_t s) {
   int per_sm = 0;
   const cudaError_t e = cached_occupancy(reinterpret_cast<const void*>(kernel), 256, 0, &per_sm);
   if (e != cudaSuccess) return e;
-  kernel<<<min(ceil_div(p.T, 8 * 32 / LANES), num_sms() * per_sm), 256, 0, s>>>(p);
   note_launches(1);
-  return cudaGetLastError();
+  return launch_early(kernel, min(ceil_div(p.T, 8 * 32 / LANES), num_sms() * per_sm), 256, 0, s, p);
 }
 
 // Rows of up to 512 channels: lanes of a warp (131072 rows of 384 88 us, in the ring 108).  More: the ring from four
@@ -200,14 +201,10 @@ cudaError_t launch(const ResidualArgs& p, cudaStream_t s) {
     const cudaError_t e = try_ring<VEC, X32, COMBINE>(p, s, &ran);
     if (e != cudaSuccess || ran) return e;
   }
-  if (chunks <= 1024)
-    row_kernel<VEC, X32, COMBINE, 1><<<p.T, ceil_div(chunks, 32) * 32, 0, s>>>(p);
-  else if (chunks <= 2048)
-    row_kernel<VEC, X32, COMBINE, 2><<<p.T, ceil_div(chunks, 64) * 32, 0, s>>>(p);
-  else
-    row_kernel<VEC, X32, COMBINE, 4><<<p.T, ceil_div(chunks, 128) * 32, 0, s>>>(p);
   note_launches(1);
-  return cudaGetLastError();
+  if (chunks <= 1024) return launch_early(row_kernel<VEC, X32, COMBINE, 1>, p.T, ceil_div(chunks, 32) * 32, 0, s, p);
+  if (chunks <= 2048) return launch_early(row_kernel<VEC, X32, COMBINE, 2>, p.T, ceil_div(chunks, 64) * 32, 0, s, p);
+  return launch_early(row_kernel<VEC, X32, COMBINE, 4>, p.T, ceil_div(chunks, 128) * 32, 0, s, p);
 }
 
 }  // namespace residual
