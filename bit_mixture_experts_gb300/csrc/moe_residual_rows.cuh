@@ -180,11 +180,10 @@ cudaError_t launch_short(const ResidualArgs& p, cudaStream_t s) {
   return launch_early(kernel, min(ceil_div(p.T, 8 * 32 / LANES), num_sms() * per_sm), 256, 0, s, p);
 }
 
-// Rows of up to 512 channels: lanes of a warp (131072 rows of 384 88 us, in the ring 108).  More: the ring from four
-// rows per SM on (608 rows of 2048 channels 4.0 us in blocks, 4.6 in the ring; 912 5.8 and 5.4; 1216 combined 12.3
-// and 11.5), with rows of over 4096 channels from one on, as an SM holds two blocks of those (200 rows of 8192 7.6 us
-// in blocks, 6.3 in the ring; 912 20 and 13).
-constexpr int SHORT_CHUNKS = 64, WIDE_CHUNKS = 512, RING_MAX_CHUNKS = 2048;
+// Rows of up to 512 channels: lanes of a warp (131072 rows of 384 88 us, in the ring 108).  More: a block each as long
+// as all of them run at once, else the ring (760 rows of 2048 channels 3.95 us in blocks, 4.85 in the ring; 912 5.4 and
+// 4.8; 456 combined 5.8 and 6.7, 912 9.5 and 8.9; 152 of 8192 4.3 and 4.3, 200 7.3 and 5.7).
+constexpr int SHORT_CHUNKS = 64, RING_MAX_CHUNKS = 2048;
 
 template <bool VEC, bool X32, bool COMBINE>
 cudaError_t launch(const ResidualArgs& p, cudaStream_t s) {
@@ -196,15 +195,22 @@ cudaError_t launch(const ResidualArgs& p, cudaStream_t s) {
     if (chunks <= 32) return launch_short<VEC, X32, COMBINE, 32, 1>(p, s);
     return launch_short<VEC, X32, COMBINE, 32, 2>(p, s);
   }
-  if (chunks <= RING_MAX_CHUNKS && p.T > (chunks > WIDE_CHUNKS ? 1 : 4) * num_sms()) {
-    bool ran;
-    const cudaError_t e = try_ring<VEC, X32, COMBINE>(p, s, &ran);
-    if (e != cudaSuccess || ran) return e;
+  const int ch = chunks <= 1024 ? 1 : chunks <= 2048 ? 2 : 4, threads = ceil_div(chunks, 32 * ch) * 32;
+  const auto kernel = ch == 1   ? row_kernel<VEC, X32, COMBINE, 1>
+                      : ch == 2 ? row_kernel<VEC, X32, COMBINE, 2>
+                                : row_kernel<VEC, X32, COMBINE, 4>;
+  if (chunks <= RING_MAX_CHUNKS) {
+    int per_sm = 0;
+    cudaError_t e = cached_occupancy(reinterpret_cast<const void*>(kernel), threads, 0, &per_sm);
+    if (e != cudaSuccess) return e;
+    if (p.T > num_sms() * per_sm) {
+      bool ran;
+      e = try_ring<VEC, X32, COMBINE>(p, s, &ran);
+      if (e != cudaSuccess || ran) return e;
+    }
   }
   note_launches(1);
-  if (chunks <= 1024) return launch_early(row_kernel<VEC, X32, COMBINE, 1>, p.T, ceil_div(chunks, 32) * 32, 0, s, p);
-  if (chunks <= 2048) return launch_early(row_kernel<VEC, X32, COMBINE, 2>, p.T, ceil_div(chunks, 64) * 32, 0, s, p);
-  return launch_early(row_kernel<VEC, X32, COMBINE, 4>, p.T, ceil_div(chunks, 128) * 32, 0, s, p);
+  return launch_early(kernel, p.T, threads, 0, s, p);
 }
 
 }  // namespace residual
