@@ -10,7 +10,7 @@
 //
 // What bounds it: memory.  16384 rows of 8192 channels, float32 stream, a gate
 // per element: 279 us, 0.99 of the copy rate; the combine of 16384 tokens, nine
-// rows of 2048 each: 139 us, 1.0 of it; 4096 rows of 2048: 16 us where the copy
+// rows of 2048 each: 138 us, 1.0 of it; 4096 rows of 2048: 15 us where the copy
 // rate allows 9.9 (ramp and tail of a short call).  Rows that are not aligned:
 // the elements' loads and stores, 50000 rows of 1999 205 us, 0.57 of the rate (by
 // way of shared memory, in whole pieces, the outputs took two barriers more:

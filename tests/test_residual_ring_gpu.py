@@ -74,6 +74,29 @@ def test_strides_and_alignments(pad, shift, H, stream):
             assert (a == -3.0).all()  # what lies between the rows stayed as it was
 
 
+@pytest.mark.parametrize("pad,shift", [(0, 0), (3, 0), (4, 5), (8, 0)])
+@pytest.mark.parametrize("H", [520, 640, 1001, 1024])
+@pytest.mark.parametrize("k", [0, 2, 8])
+def test_narrow_rows(H, k, pad, shift):
+    """More rows than can have a block at once where blocks are small."""
+    import torch
+    for stream, gate in (("bf16", "full"), ("f32", "token")):
+        c = Case(4900, H, stream, pad=pad, shift=shift, gate=gate, k=k, seed=H + k)
+        out = (c.rows(4900, c.dtype), c.rows(4900, torch.bfloat16))
+        around = [o._base for o in out]
+        for a in around:
+            a.fill_(-3.0)
+        r, n = c.run(out)
+        check_some(c, r, n)
+        first = r.clone(), n.clone()
+        if pad == 0 and k == 0 and stream == "bf16":
+            c.run((c.y, c.x))
+            assert torch.equal(c.y, first[0]) and torch.equal(c.x, first[1])
+        for a, o in zip(around, out):
+            o.fill_(-3.0)
+            assert (a == -3.0).all()
+
+
 @pytest.mark.parametrize("H", [640, 1999, 2048, 16384])
 def test_outputs_left_out_and_in_place(H):
     import torch
