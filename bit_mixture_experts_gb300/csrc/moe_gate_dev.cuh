@@ -677,8 +677,9 @@ __device__ __forceinline__ void warp_gate(const float* logits, int t, int T, con
     float most = x;
 #pragma unroll
     for (int m = SEG / 2; m >= 1; m >>= 1) most = fmaxf(most, __shfl_xor_sync(FULL, most, m));
-    if (x != -INFINITY) {
-      const float hi = x - most, bb = hi - x, lo = (x - (hi - bb)) + (-most - bb);
+    const float hi = x - most;
+    if (hi > -104.f) {  // (e^-104 is 0 in 32 bits; a difference that overflows leaves a rest that is NaN)
+      const float bb = hi - x, lo = (x - (hi - bb)) + (-most - bb);
       z = expf(hi) * (1.0f + lo);
     }
   } else if (x != -INFINITY) {
