@@ -74,7 +74,7 @@ __device__ __forceinline__ void warp_topk(const float* __restrict__ row, int E, 
   const float bb = dh - lj;
   const float dl = (lj - (dh - bb)) + (nl0 - bb);
   float z = 0.f;
-  if (lane < k) z = expf(dh) * (1.0f + dl);
+  if (lane < k && dh > -104.f) z = expf(dh) * (1.0f + dl);  // (below e^-104 is 0; a difference that overflows leaves a dl of NaN)
   float s = z;
 #pragma unroll
   for (int m = 16; m >= 1; m >>= 1) s += __shfl_xor_sync(FULL, s, m);

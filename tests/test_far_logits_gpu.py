@@ -51,3 +51,36 @@ def test_gates(T, E, k, groups, top, score, with_bias, renorm):
     assert (want.sum(1) > 1.5).all()  # (each token has one whose score is not small)
     np.testing.assert_array_equal(ids.cpu().numpy(), want_ids[rows])
     np.testing.assert_allclose(w.double().cpu().numpy(), want[rows], rtol=REL, atol=0)
+
+
+@pytest.mark.parametrize("T,E,k", [(1, 16, 4), (100, 256, 8), (4096, 256, 8), (300, 1000, 32)])
+def test_route(T, E, k):
+    """moe_route in one block and in many: finite logits alone, as it takes no others."""
+    from test_route_gpu import run_route
+    l = np.clip(far(E)[np.arange(T) % 6], LOWEST, -LOWEST)
+    got = run_route(l, k, 64)
+    ids, w = gate_ref.choose(l[:6], k)
+    np.testing.assert_array_equal(got["topk_ids"][:6], ids)
+    np.testing.assert_allclose(got["topk_w"].astype(np.float64), w[np.arange(T) % 6], rtol=REL, atol=0)
+
+
+@pytest.mark.parametrize("T", [1, 6, 40])
+def test_layer(T):
+    """The layer's own choice, in the fused decode kernel and before the GEMMs."""
+    import gpu_util as G
+    import torch
+
+    from bit_mixture_experts_gb300 import _lib
+    from bit_mixture_experts_gb300.layer import MoELayerW4
+    d = G.workload((T, 256, 64, 4, 128, False), 1)
+    layer = MoELayerW4(256, 64, 4, 128, d, device=G.torch_dev())
+    x, _ = G.to_dev_inputs(d)
+    l = np.clip(far(64)[np.arange(T) % 6], LOWEST, -LOWEST)
+    out = layer.forward(x, torch.tensor(l, device=x.device))
+    torch.cuda.synchronize()
+    assert _lib.moe_get_device_error() == 0
+    b = layer.buffers(T)
+    ids, w = gate_ref.choose(l, 4)
+    np.testing.assert_array_equal(b["topk_ids"].cpu().numpy(), ids)
+    np.testing.assert_allclose(b["topk_w"].double().cpu().numpy(), w, rtol=REL, atol=0)
+    assert torch.isfinite(out).all()
