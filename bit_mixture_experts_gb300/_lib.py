@@ -8,6 +8,7 @@ loudly instead of falling back to anything else.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -32,7 +33,7 @@ SYMBOLS = ["moe_version", "moe_launch_count", "moe_route_noalloc", "moe_route_x"
            "moe_repacked_bytes", "moe_repack_w4", "moe_expanded_bytes", "moe_expand_w4", "moe_expert_gemm_w4", "moe_combine", "moe_decode_workspace_size",
            "moe_gate", "moe_route_gated", "moe_residual_norm", "moe_combine_residual_norm", "moe_layer_forward_gated",
            "moe_kv_append", "moe_kv_read", "moe_kv_attention", "moe_kv_attention_workspace_size",
-           "moe_layer_forward", "moe_layer_forward_host", "moe_get_device_error", "moe_set_wait_limit_ns",
+           "moe_layer_forward", "moe_layer_forward_host", "moe_get_device_error", "moe_set_wait_limit_ns", "moe_exchange_capture_mode",
            "moe_trace_words", "moe_trace_reset", "moe_trace_read"]
 
 
@@ -118,6 +119,7 @@ _SIGS = {
     "moe_kv_attention_workspace_size": (_kv + [_i], _sz),
     "moe_get_device_error": ([ctypes.POINTER(ctypes.c_int32)], _i),
     "moe_set_wait_limit_ns": ([ctypes.c_uint64], None),
+    "moe_exchange_capture_mode": ([ctypes.POINTER(ctypes.c_int32)], _i),
     "moe_trace_words": ([], ctypes.c_size_t),
     "moe_trace_reset": ([_vp], _i),
     "moe_trace_read": ([_vp, ctypes.c_size_t], _i),
@@ -357,6 +359,17 @@ def moe_kv_attention(q, scale, cache: KVCache, batch: KVBatch, out, lse, workspa
     ws, n = workspace if isinstance(workspace, tuple) else (workspace.data_ptr(), workspace.nbytes)
     _call("moe_kv_attention", q.data_ptr(), token, head, q.shape[1], scale, cache, batch, out.data_ptr(), _ptr(lse), ws,
           n, _stream(stream))
+
+
+@contextlib.contextmanager
+def relaxed_capture():
+    """A `with` block in which this thread may allocate on, and wait for, a stream while it captures another one."""
+    mode = ctypes.c_int32(2)
+    _call("moe_exchange_capture_mode", ctypes.byref(mode))
+    try:
+        yield
+    finally:
+        _call("moe_exchange_capture_mode", ctypes.byref(mode))
 
 
 def moe_set_wait_limit_ns(ns: int) -> None:

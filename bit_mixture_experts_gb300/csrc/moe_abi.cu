@@ -743,6 +743,16 @@ int moe_repack_w4(const uint32_t* packed, const uint16_t* scale, const uint16_t*
 
 void moe_set_wait_limit_ns(uint64_t ns) { set_wait_limit_ns(ns); }
 
+int moe_exchange_capture_mode(int32_t* mode) {
+  if (!mode) return MOE_ERR_NULL;
+  if (*mode < 0 || *mode > 2) return MOE_ERR_MODE;
+  static_assert(cudaStreamCaptureModeGlobal == 0 && cudaStreamCaptureModeThreadLocal == 1 && cudaStreamCaptureModeRelaxed == 2, "");
+  cudaStreamCaptureMode m = static_cast<cudaStreamCaptureMode>(*mode);
+  if (cudaThreadExchangeStreamCaptureMode(&m) != cudaSuccess) return MOE_ERR_CUDA;
+  *mode = m;
+  return MOE_OK;
+}
+
 size_t moe_trace_words(void) {
 #ifdef MOE_TRACE
   return moe::TRACE_WORDS;

@@ -8,6 +8,7 @@ from __future__ import annotations
 import numpy as np
 
 from . import _lib
+from .gate import _empty, _on
 
 DEFAULT_BLOCK_N = {_lib.IMPL_TC: 128, _lib.IMPL_GEMV: 8, _lib.IMPL_TC2: 128, _lib.IMPL_TC_BF16: 128}
 DECODE_MAX_T = 16  # token counts up to this take the GEMV kernel under impl="auto"
@@ -46,6 +47,11 @@ class MoELayerW4:
     w13_scale, w13_bias, w2_packed, w2_scale, w2_bias) as numpy arrays or torch
     tensors already on the device.  `gate` (an ExpertGate of the same k) is how
     the experts are chosen; None: softmax renormalised over the chosen.
+
+    Calls on several streams share no buffers, nor do captured calls those of
+    others: a call that torch.cuda.graph captures takes its own from the graph's
+    memory.  (A capture made in another way has no such memory: what PyTorch
+    hands out there, it hands out again.)
     """
 
     def __init__(self, H, E, k, F, weights: dict, device="cuda", impl="auto", block_n=None, fuse_combine=False,
@@ -84,6 +90,8 @@ class MoELayerW4:
         else:
             self.weights = _lib.Weights(self.w13_r.data_ptr(), self.w2_r.data_ptr())
         self._bufs = {}
+        self._captured = []  # zeroed scratch of captured calls, whose graphs live no longer than the weights
+        self._side = torch.cuda.Stream(self.device, priority=-1)
 
     def _repack(self, packed, scale, bias, gate_up):
         import torch
@@ -119,11 +127,33 @@ class MoELayerW4:
         """Block-map tile height used for T tokens."""
         return self.block_n or default_block_n(self.impl_for(T), T, self.E, self.k)
 
-    def buffers(self, T):
-        """Routing / intermediate buffers for T tokens (allocated once per T)."""
+    def buffers(self, T, stream=None):
+        """Routing / intermediate buffers of the calls for T tokens on `stream` (None: the current one), allocated once per
+        T and stream.  Where that stream is being captured into a graph: new ones, for one call."""
+        if stream is not None:
+            with _on(stream, self.device):
+                return self._buffers_here(T)
+        return self._buffers_here(T)
+
+    def _zeros(self, nbytes):
+        """Scratch that every call leaves zero as it found it.  A captured call's is zeroed before the graph is first
+        replayed, on another stream: in the graph it would be a node of every replay."""
         import torch
-        if T in self._bufs:
-            return self._bufs[T]
+        if torch.cuda.is_current_stream_capturing():
+            with torch.cuda.stream(self._side):
+                if not torch.cuda.is_current_stream_capturing():
+                    with _lib.relaxed_capture():
+                        t = torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
+                        self._side.synchronize()
+                    self._captured.append(t)
+                    return t
+        return torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
+
+    def _buffers_here(self, T):
+        import torch
+        key = None if torch.cuda.is_current_stream_capturing() else (T, _lib._stream())
+        if key in self._bufs:
+            return self._bufs[key]
         E, k, H, F, bn = self.E, self.k, self.H, self.F, self.block_n_for(T)
         A = T * k
         dev = self.device
@@ -140,20 +170,21 @@ class MoELayerW4:
             "num_blocks": torch.empty(1, dtype=torch.int32, device=dev),
             "h": torch.empty((A + T, F), dtype=torch.bfloat16, device=dev),
             "y": torch.empty((A + T, H), dtype=torch.bfloat16, device=dev),
-            "workspace": torch.zeros(max(wsb, 16), dtype=torch.uint8, device=dev),  # zero once, left zero
+            "workspace": self._zeros(wsb) if wsb else torch.empty(16, dtype=torch.uint8, device=dev),
         }
-        # counters of the fused decode kernel (used for T <= 8 with the GEMV kernel): zero once, left zero
+        # counters of the fused decode kernel (used for T <= 8 with the GEMV kernel)
         dws = _lib.moe_decode_workspace_size(T, H)
-        t["decode_ws"] = torch.zeros(max(dws, 16), dtype=torch.uint8, device=dev) if dws else None
-        # counters of the down GEMM's fused combine (tensor-core path): zero once, left zero
+        t["decode_ws"] = self._zeros(dws) if dws else None
+        # counters of the down GEMM's fused combine (tensor-core path)
         cws = _lib.moe_down_combine_workspace_size(T, H) if self.fuse_combine else 0
-        t["combine_ws"] = torch.zeros(max(cws, 16), dtype=torch.uint8, device=dev) if cws else None
+        t["combine_ws"] = self._zeros(cws) if cws else None
         t["struct"] = _lib.Buffers(*(t[n].data_ptr() for n in ("topk_ids", "topk_w", "counts", "offsets", "perm",
                                                                  "inv_perm", "block_map", "num_blocks", "h", "y",
                                                                  "workspace")), wsb,
                                    t["decode_ws"].data_ptr() if dws else None, dws,
                                    t["combine_ws"].data_ptr() if cws else None, cws)
-        self._bufs[T] = t
+        if key is not None:
+            self._bufs[key] = t
         return t
 
     def forward(self, x, logits, out=None, stream=None):
@@ -162,9 +193,9 @@ class MoELayerW4:
         T = x.shape[0]
         assert x.dtype == torch.bfloat16 and x.shape == (T, self.H) and x.is_contiguous()
         assert logits.dtype == torch.float32 and logits.shape == (T, self.E) and logits.is_contiguous()
-        b = self.buffers(T)
+        b = self.buffers(T, stream)
         if out is None:
-            out = torch.empty((T, self.H), dtype=torch.bfloat16, device=self.device)
+            out = _empty((T, self.H), torch.bfloat16, self.device, stream)
         sizes = T, self.H, self.F, self.E, self.k, self.block_n_for(T), self.impl_for(T), self.weights, b["struct"], stream
         if self.gate is None:
             _lib.moe_layer_forward(x, logits, out, *sizes)
@@ -186,7 +217,7 @@ class MoELayerW4:
             raise ValueError("either logits or a choice is needed")
         if residual.shape != x.shape:
             raise ValueError(f"residual is {tuple(residual.shape)}, x {tuple(x.shape)}")
-        b = self.buffers(T)
+        b = self.buffers(T, stream)
         struct = b["struct"]
         for t, name, shape, dtype in ([(logits, "logits", (T, self.E), torch.float32)] if choice is None else
                                       [(choice[0], "choice[0]", (T, self.k), torch.int32),
@@ -209,7 +240,7 @@ class MoELayerW4:
         if self.gate is not None:
             raise ValueError("a layer with a gate takes its inputs on the device (forward)")
         T = x_host.shape[0]
-        b = self.buffers(T)
+        b = self.buffers(T, stream)
         _lib.moe_layer_forward_host(x_host, logits_host, out_host, stage["x"], stage["logits"], stage["out"], T,
                                     self.H, self.F, self.E, self.k, self.block_n_for(T), self.impl_for(T), self.weights,
                                     b["struct"], stream)

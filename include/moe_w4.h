@@ -704,6 +704,14 @@ int moe_get_device_error(int32_t* code);
  * result left incomplete by a timeout is reported, not followed.  Test hook. */
 void moe_set_wait_limit_ns(uint64_t ns);
 
+/* moe_exchange_capture_mode -- what the calling thread may do while a stream is
+ * captured into a graph (cudaStreamCaptureMode: 0 global, 1 thread-local, 2
+ * relaxed): *mode becomes the thread's, and *mode what it was.  For a caller that
+ * allocates and zeroes the workspace of a call that it captures, on another
+ * stream: so that zeroing it is no part of the graph.  MOE_ERR_MODE for any other
+ * value. */
+int moe_exchange_capture_mode(int32_t* mode);
+
 /* Wait statistics of the tensor-core kernels (moe_gemm_tc.cu, moe_ffn_tc.cu,
  * moe_gemm_pair.cu) in a trace build: libmoe_w4_trace.so, built by
  * `python -m bit_mixture_experts_gb300.build --trace` (-DMOE_TRACE), which

@@ -1,0 +1,143 @@
+"""The layer on several streams and in graphs: no call reads what another's is writing."""
+import pytest
+
+import gpu_util as G
+
+pytestmark = pytest.mark.gpu
+
+H, E, K, F = 256, 64, 4, 256
+# fused decode; routing in one block and in several, with and without the combine in the down projection
+FORMS = [(4, False), (100, False), (600, False), (600, True)]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    G.ensure_built()
+
+
+@pytest.fixture(scope="module")
+def weights():
+    return G.workload((600, H, E, K, F, False), 2)
+
+
+def make(weights, fuse=False, gate=None):
+    from bit_mixture_experts_gb300.layer import MoELayerW4
+    return MoELayerW4(H, E, K, F, weights, device=G.torch_dev(), impl="auto" if not fuse else "tc", fuse_combine=fuse,
+                      gate=gate)
+
+
+def inputs(T, n):
+    """n calls' inputs, each with experts of its own liking."""
+    import torch
+    gen = torch.Generator().manual_seed(T)
+    return [((torch.randn((T, H), generator=gen) * 0.5).bfloat16().to(G.torch_dev()),
+             (torch.randn((T, E), generator=gen) + 2 * torch.randn(E, generator=gen)).to(G.torch_dev())) for _ in range(n)]
+
+
+def no_error():
+    import torch
+
+    from bit_mixture_experts_gb300 import _lib
+    torch.cuda.synchronize()
+    assert _lib.moe_get_device_error() == 0
+
+
+@pytest.mark.parametrize("T,fuse", FORMS)
+def test_the_first_call_is_on_another_stream(weights, T, fuse):
+    """While the current stream is busy: what the call takes is made, and zeroed, on its own stream."""
+    import torch
+
+    from bit_mixture_experts_gb300 import ExpertGate, ResidualNorm
+    (x, logits), = inputs(T, 1)
+    want = make(weights, fuse).forward(x, logits)
+    norm = ResidualNorm()
+    follows = make(weights, fuse, ExpertGate(K)).forward_residual(x, logits, x, norm)
+    no_error()
+    for as_handle in (False, True):
+        layer, gated = make(weights, fuse), make(weights, fuse, ExpertGate(K))
+        side = torch.cuda.Stream()
+        s = side.cuda_stream if as_handle else side
+        torch.cuda.synchronize()
+        torch.cuda._sleep(100_000_000)
+        got = layer.forward(x, logits, stream=s)
+        r, n = gated.forward_residual(x, logits, x, norm, stream=s)
+        side.synchronize()
+        assert torch.equal(got.cpu(), want.cpu())
+        assert torch.equal(r.cpu(), follows[0].cpu()) and torch.equal(n.cpu(), follows[1].cpu())
+        no_error()
+
+
+@pytest.mark.parametrize("T,fuse", FORMS)
+def test_two_streams(weights, T, fuse):
+    import torch
+    layer, calls = make(weights, fuse), inputs(T, 2)
+    want = [layer.forward(*c) for c in calls]
+    no_error()
+    assert not torch.equal(*want)
+    streams = [torch.cuda.Stream() for _ in calls]
+    outs = [[torch.empty_like(w) for _ in range(20)] for w in want]
+    torch.cuda.synchronize()
+    for i in range(20):
+        for s, c, o in zip(streams, calls, outs):
+            layer.forward(*c, out=o[i], stream=s)
+    no_error()
+    for w, o in zip(want, outs):
+        assert all(torch.equal(x, w) for x in o)
+    names = "counts", "perm", "y"
+    a, b = (layer.buffers(T, s) for s in streams)
+    assert not any(a[n].data_ptr() == b[n].data_ptr() for n in names)
+
+
+@pytest.mark.parametrize("warm", [True, False])
+@pytest.mark.parametrize("T,fuse", FORMS)
+def test_graphs_beside_each_other_and_eager_calls(weights, T, fuse, warm):
+    """Two graphs of two calls each, captured with and without a call before, replayed on two streams beside calls."""
+    import torch
+    layer, calls = make(weights, fuse), inputs(T, 5)
+    fresh = make(weights, fuse)
+    want = [fresh.forward(*c) for c in calls]
+    if warm:
+        layer.forward(*calls[0])
+    no_error()
+    graphs, outs = [], []
+    for pair in (calls[:2], calls[2:4]):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append([layer.forward(*c) for c in pair])
+        graphs.append(g)
+    streams = [torch.cuda.Stream() for _ in graphs]
+    eager = [torch.empty_like(want[4]) for _ in range(10)]
+    torch.cuda.synchronize()
+    for i in range(10):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        layer.forward(*calls[4], out=eager[i])
+    no_error()
+    for got, w in zip(outs[0] + outs[1] + eager, want[:4] + [want[4]] * 10):
+        assert torch.equal(got, w)
+
+
+def test_relaxed_capture():
+    """Memory made and zeroed beside a capture, which goes on; the thread's mode is the old one afterwards."""
+    import ctypes
+
+    import torch
+
+    from bit_mixture_experts_gb300 import _lib
+    c = torch.full((1001,), 7, dtype=torch.uint8, device="cuda")
+    side = torch.cuda.Stream(priority=-1)  # (captures are on streams of the usual priority)
+    mode = ctypes.c_int32(1)
+    _lib._call("moe_exchange_capture_mode", ctypes.byref(mode))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        with torch.cuda.stream(side), _lib.relaxed_capture():
+            b = torch.zeros(50_000_000, dtype=torch.uint8, device="cuda")
+            side.synchronize()
+        c.add_(1)
+    _lib._call("moe_exchange_capture_mode", ctypes.byref(mode))
+    assert mode.value == 1
+    assert not b.any() and (c == 7).all()
+    g.replay()
+    torch.cuda.synchronize()
+    assert (c == 8).all() and not b.any()
