@@ -267,26 +267,36 @@ class MoEDecodeChain:
         self.wr = [_dev(np.asarray(b, dtype=np.uint16), self.device) for b in router_bits]
         self._bufs = {}
 
-    def buffers(self, T):
-        """Per-layer outputs (bf16 [T, H]), logits (fp32 [T, E]) and the router's top-k scratch."""
+    def buffers(self, T, stream=None):
+        """Per-layer outputs (bf16 [T, H]), logits (fp32 [T, E]) and the router's top-k scratch of the calls for T tokens on
+        `stream` (None: the current one); where that is being captured, new ones for one call, as the layers'."""
+        if stream is not None:
+            with _on(stream, self.device):
+                return self._buffers_here(T)
+        return self._buffers_here(T)
+
+    def _buffers_here(self, T):
         import torch
-        if T not in self._bufs:
+        key = None if torch.cuda.is_current_stream_capturing() else (T, _lib._stream())
+        b = self._bufs.get(key)
+        if b is None:
             dev, L = self.device, len(self.layers)
-            self._bufs[T] = {
+            b = {
                 "xn": [torch.empty((T, self.H), dtype=torch.bfloat16, device=dev) for _ in range(L)],
                 "out": [torch.empty((T, self.H), dtype=torch.bfloat16, device=dev) for _ in range(L)],
                 "logits": [torch.empty((T, self.E), dtype=torch.float32, device=dev) for _ in range(L)],
                 "ids": [torch.empty((T, self.k), dtype=torch.int32, device=dev) for _ in range(L)],
                 "w": [torch.empty((T, self.k), dtype=torch.float32, device=dev) for _ in range(L)],
             }
-            for layer in self.layers:
-                layer.buffers(T)
-        return self._bufs[T]
+            if key is not None:
+                self._bufs[key] = b
+        return b
 
     def forward(self, x, stream=None):
-        """x bf16 [T, H] on the device -> the last layer's output (a buffer of the chain)."""
+        """x bf16 [T, H] on the device -> the last layer's output (a buffer of the chain, which the next call for T
+        tokens on the stream writes; of a captured call the graph's)."""
         T = x.shape[0]
-        b = self.buffers(T)
+        b = self.buffers(T, stream)
         cur = x
         for l, layer in enumerate(self.layers):
             _lib.moe_norm_router(cur, self.wr[l], b["xn"][l], b["logits"][l], stream=stream)

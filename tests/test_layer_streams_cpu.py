@@ -99,3 +99,20 @@ def test_captured_calls_share_no_buffers(layer, monkeypatch, T):
     dev.capturing.add(side)
     layer.buffers(T, side)
     assert len(layer._captured) == 4
+
+
+def test_a_chains_streams_and_captures_share_no_buffers(monkeypatch):
+    from bit_mixture_experts_gb300.layer import MoEDecodeChain
+    dev = Device(monkeypatch)
+    chain = MoEDecodeChain.__new__(MoEDecodeChain)
+    chain.H, chain.E, chain.k, chain.device, chain.layers, chain._bufs = 128, 64, 4, torch.device("cpu"), [None] * 2, {}
+    sets = [chain.buffers(4), chain.buffers(4, 7)]
+    assert chain.buffers(4) is sets[0] and chain.buffers(4, 7) is sets[1]
+    dev.capturing.add(7)
+    sets += [chain.buffers(4, 7), chain.buffers(4, 7)]
+    dev.capturing.clear()
+    assert chain.buffers(4, 7) is sets[1]
+    at = [{t.data_ptr() for ts in b.values() for t in ts} for b in sets]
+    assert len(set.union(*at)) == sum(len(a) for a in at) == 4 * 10
+    for a, s in zip(at, (0, 7, 7, 7)):
+        assert {stream for _, p, stream in dev.made if p in a} == {s}

@@ -141,3 +141,34 @@ def test_relaxed_capture():
     g.replay()
     torch.cuda.synchronize()
     assert (c == 8).all() and not b.any()
+
+
+def test_a_chain_on_two_streams_and_in_graphs():
+    import torch
+
+    import workloads
+    from bit_mixture_experts_gb300.layer import MoEDecodeChain
+    shape = workloads.LayerShape(H=H, E=E, k=K, F=128)
+    chain = MoEDecodeChain(H, E, K, 128, [workloads.make_weights(shape, seed=l) for l in range(2)],
+                           [workloads.router_weight_bits(shape, seed=l) for l in range(2)], device=G.torch_dev(), impl="gemv")
+    xs = [x for x, _ in inputs(4, 4)]
+    want = [chain.forward(x).clone() for x in xs]
+    no_error()
+    streams = [torch.cuda.Stream() for _ in xs[:2]]
+    outs = [[], []]
+    graphs, kept = [], []
+    for x in xs[2:]:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            kept.append(chain.forward(x))
+        graphs.append(g)
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for x, s, o, g in zip(xs, streams, outs, graphs):
+            with torch.cuda.stream(s):
+                o.append(chain.forward(x).clone())
+                g.replay()
+    no_error()
+    for w, o in zip(want, outs):
+        assert all(torch.equal(x, w) for x in o)
+    assert all(torch.equal(x, w) for x, w in zip(kept, want[2:]))
