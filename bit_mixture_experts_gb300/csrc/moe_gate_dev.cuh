@@ -5,7 +5,7 @@
 //   s_e = sigmoid(l_e)  or  exp(l_e - m) / sum_i exp(l_i - m)
 //   v_e = s_e + b_e;  chosen: the k largest v_e of the groups that stay, in
 //   descending order, equal ones by index
-//   w_j = scale s_j / (sum of the chosen s, or 1)
+//   w_j = scale s_j / (sum of the chosen s, or 1), by ratios of the s
 //
 // The choice has to be what exact scores give, and FP32 scores can be off by
 // more than two experts differ.  So values are compared as integers m, v in
@@ -671,16 +671,19 @@ __device__ __forceinline__ void warp_gate(const float* logits, int t, int T, con
     if (tj < g.k) x = available(__ldg(row + id));
   }
   // ---- weights
-  float z = 0.f;
-  if (g.softmax && g.renorm) {
-    // exp(x - the chosen ones' largest): the difference carried exactly (two-sum)
-    float most = x;
+  float z = 0.f, most = x;
+  if (g.renorm) {
 #pragma unroll
     for (int m = SEG / 2; m >= 1; m >>= 1) most = fmaxf(most, __shfl_xor_sync(FULL, most, m));
+  }
+  if (g.renorm && (g.softmax || most < 0.f)) {
+    // exp(x - the chosen ones' largest), so that scores which 32 bits do not hold keep their ratios; the difference
+    // is carried exactly (two-sum).  Sigmoid: e^x / (1 + e^x) over e^most; from 0 on the largest is 1/2 or more.
     const float hi = x - most;
     if (hi > -104.f) {  // (e^-104 is 0 in 32 bits; a difference that overflows leaves a rest that is NaN)
       const float bb = hi - x, lo = (x - (hi - bb)) + (-most - bb);
       z = expf(hi) * (1.0f + lo);
+      if (!g.softmax) z /= 1.0f + expf(x);
     }
   } else if (x != -INFINITY) {
     z = g.softmax ? expf(x - top) * inv : 1.0f / (1.0f + expf(-x));

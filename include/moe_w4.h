@@ -225,16 +225,19 @@ int moe_norm_router(const uint16_t* x, const uint16_t* w_router, int T, int H, i
  * ("Perplexity Open Sources Lily", Technical Details, Model bullet names no
  * other).  A gate describes the other ways that mixture-of-experts models
  * choose.  For a token's logits l:
- *   s_e = sigmoid(l_e), or exp(l_e) / sum of all exp(l_i); below 2^-126 it is 0
+ *   s_e = sigmoid(l_e), or exp(l_e) / sum of all exp(l_i)
  *   v_e = s_e + bias_e          (the bias, which balances the experts' load,
- *                                takes part in the choice alone)
+ *                                takes part in the choice alone; an s_e below
+ *                                2^-126 counts as 0 here)
  *   groups: the experts in order form `groups` groups of E / groups; a group's
  *           score is its largest v_e or the sum of its two largest, and the
  *           top_groups best groups stay (equal scores: lower index first)
  *   chosen: the k largest v_e of the groups that stay, in descending order,
  *           equal ones by index
- *   w_j = scale * s_j / (sum of the chosen s_i, if renorm, else 1); 0 where
- *         that sum is 0
+ *   w_j = scale * s_j / (sum of the chosen s_i, if renorm, else 1).  With renorm
+ *         the scores' ratios hold however small all of them are (only a ratio
+ *         below 2^-126 may come out as 0); without, an s_j below 2^-126 may.
+ *         All are 0 where no chosen expert is available
  * The choice is that of values that are off by less than 2^-40 (times the
  * largest bias, where that is above 1): a token whose choice a rounding in 32
  * bits could change is done again with scores of twice the length.  Without a

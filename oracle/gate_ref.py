@@ -21,6 +21,21 @@ def scores(logits, score):
     return np.where(s < 2.0 ** -126, 0.0, s), here
 
 
+def weights(logits, ids, score="softmax", renorm=True, scale=1.0):
+    """The weights of one token's chosen experts: their scores' ratios (renorm), or the scores, those below 2^-126 as 0."""
+    if not renorm:
+        return scores(logits, score)[0][ids] * scale
+    l = np.asarray(logits, np.float64)[ids]
+    here = l > -np.inf
+    if not here.any():
+        return np.zeros(len(ids))
+    l = np.minimum(l[here], np.finfo(np.float32).max)
+    log_s = l if score == "softmax" else -np.logaddexp(0.0, -l)
+    s = np.zeros(len(ids))
+    s[here] = np.exp(log_s - log_s.max())
+    return s / s.sum() * scale
+
+
 def choose_token(logits, k, score="softmax", bias=None, groups=1, top_groups=None, group_score="top2", renorm=True,
                  scale=1.0):
     """One token's (ids int [k], weights float64 [k])."""
@@ -41,10 +56,7 @@ def choose_token(logits, k, score="softmax", bias=None, groups=1, top_groups=Non
         allowed = np.isin(np.arange(E) // per, stay)
     order = sorted((e for e in range(E) if allowed[e]), key=lambda e: (not here[e], -v[e] if here[e] else 0.0, e))
     ids = np.array(order[:k])
-    w = np.where(here[ids], s[ids], 0.0)
-    if renorm:
-        w = w / w.sum() if w.sum() > 0 else np.zeros(k)
-    return ids, w * scale
+    return ids, weights(logits, ids, score, renorm, scale)
 
 
 def choose(logits, k, **kw):
