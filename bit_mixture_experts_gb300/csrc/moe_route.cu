@@ -29,7 +29,7 @@ __global__ void __launch_bounds__(1024) route_small_kernel(
     const float* __restrict__ logits, int T, int E, int k, int bn, int32_t* __restrict__ topk_ids,
     float* __restrict__ topk_w, int32_t* __restrict__ counts, int32_t* __restrict__ offsets,
     int32_t* __restrict__ perm, int32_t* __restrict__ inv_perm, int32_t* __restrict__ block_map,
-    int32_t* __restrict__ num_blocks, int ids_given) {
+    int32_t* __restrict__ num_blocks, int ids_given, int* err) {
   extern __shared__ int smem_i[];
   int* s_cnt = smem_i;                    // [E]
   int* s_wc = smem_i + E;                 // [32][E] per-warp counts
@@ -40,8 +40,12 @@ __global__ void __launch_bounds__(1024) route_small_kernel(
 
   for (int i = threadIdx.x; i < 33 * E; i += blockDim.x) smem_i[i] = 0;
   for (int t = warp; t < T; t += 32) {
-    if (ids_given) {  // top-k already chosen (moe_route_x): take the ids
-      if (lane < k) s_ids[t * k + lane] = min(max(__ldg(topk_ids + t * k + lane), 0), E - 1);
+    if (ids_given) {  // top-k already chosen (by moe_route_x, a gate or the caller): take the ids
+      if (lane < k) {
+        const int e = __ldg(topk_ids + t * k + lane);
+        if (e < 0 || e >= E) set_device_error(err, MOE_DEV_BAD_INDEX);
+        s_ids[t * k + lane] = min(max(e, 0), E - 1);
+      }
       continue;
     }
     int id;
@@ -316,7 +320,7 @@ cudaError_t launch_route(const float* logits, int T, int E, int k, int bn, int32
       if (e0 != cudaSuccess) return e0;
     }
     route_small_kernel<<<1, 1024, sm, s>>>(logits, T, E, k, bn, ids, w, counts, offsets, perm, inv_perm, bm, nb,
-                                           ids_given);
+                                           ids_given, err);
     note_launches(1);
     return cudaGetLastError();
   }

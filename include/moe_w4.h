@@ -275,7 +275,7 @@ int moe_gate(const float* logits, int T, int E, int k, const moe_gate_t* gate, i
  * outputs, workspace and limits.  With logits NULL the experts are those that
  * topk_ids and topk_w hold (`gate` is not read; a token may name an expert more
  * than once, which are then rows of their own; an id outside [0, E) is taken as
- * one inside it, and sets MOE_DEV_BAD_INDEX where T * k > 1024).
+ * one inside it, and sets MOE_DEV_BAD_INDEX).
  */
 int moe_route_gated(const float* logits, int T, int E, int k, const moe_gate_t* gate, int block_n, int32_t* topk_ids,
                     float* topk_w, int32_t* counts, int32_t* offsets, int32_t* perm, int32_t* inv_perm,
