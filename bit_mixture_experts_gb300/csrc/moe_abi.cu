@@ -192,11 +192,13 @@ int residual_args(const uint16_t* y, long long y_stride, long long y_rows, bool 
   const Rows in[5] = {rows_of(p->x, p->x_stride, H, xs, T), rows_of(y, y_stride, H, 2, y_rows),
                       rows_of(p->gate, p->gate_token_stride, p->gate_per_channel ? H : 1, gs, T),
                       rows_of(p->w_pre, 0, H, ps, 1), rows_of(p->w_post, 0, H, ps, 1)};
+  // Inputs whose place an output may take: each value is read before it is written, by the same thread.  (Not those of
+  // all tokens, although with one token their rows are as the output's.)
+  const bool place[5] = {true, !combine, (p->gate_per_channel || H == 1) && p->gate_token_stride != 0, false, false};
   if (overlap(r, n)) return MOE_ERR_OVERLAP;
-  for (const Rows& i : in)
+  for (int i = 0; i < 5; ++i)
     for (const Rows& o : {r, n})
-      // an output in the place of an input: each value is read before it is written, by the same thread
-      if (overlap(i, o) && !(same(i, o) && (!combine || &i != &in[1]))) return MOE_ERR_OVERLAP;
+      if (overlap(in[i], o) && !(place[i] && same(in[i], o))) return MOE_ERR_OVERLAP;
   a->y = y;
   a->y_stride = y_stride;
   a->inv_perm = nullptr;

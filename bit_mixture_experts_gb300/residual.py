@@ -76,7 +76,9 @@ class ResidualNorm(Fixed):
                 raise ValueError(f"gate must be bfloat16 or float32 on {dev}, with contiguous rows, and fit {tuple(shape)}: "
                                  f"got {g_type} {tuple(gate.shape)} on {gate.device}, strides {gate.stride()}")
             s.gate, s.gate_f32 = gate.data_ptr(), _F32[g_type]
-            s.gate_token_stride, s.gate_per_channel = strides[0] if dims[0] > 1 else 0, int(dims[1] > 1)
+            s.gate_per_channel = int(dims[1] > 1)
+            # (one token's own row is told apart from all tokens': an output may take its place)
+            s.gate_token_stride = strides[0] if dims[0] > 1 or (shape[0] == 1 and dims[1] > 1 and len(gate.shape) == 2) else 0
         return s, (r, n)
 
     def add(self, x, y, gate=None, out=None, stream=None):

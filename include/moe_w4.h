@@ -315,7 +315,7 @@ typedef struct {
   const void* w_pre;  /* [H] bf16, or float32 if param_f32; NULL: n = r / rms(r) */
   const void* w_post; /* as w_pre; NULL with post: z = y / rms(y) */
   const void* gate;   /* bf16, or float32 if gate_f32; NULL: 1 */
-  int64_t gate_token_stride; /* 0: the same for all tokens */
+  int64_t gate_token_stride; /* 0: the same for all tokens (also where T = 1) */
   int32_t gate_per_channel;  /* 0: one value per token, else H consecutive ones */
   int32_t post;
   int32_t stream_f32, param_f32, gate_f32;
