@@ -140,6 +140,7 @@ __global__ void __launch_bounds__(NT, ring_blocks(CH, NT))
       }
     };
     auto expect = [&](uint32_t bytes) {
+      __syncwarp();  // every lane's weight is written before the stage is announced by one (reductions do not order memory)
       if (lane == 0)
         asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(full(turn.st)), "r"(bytes) : "memory");
       __syncwarp();
