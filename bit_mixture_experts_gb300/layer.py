@@ -91,7 +91,7 @@ class MoELayerW4:
             self.weights = _lib.Weights(self.w13_r.data_ptr(), self.w2_r.data_ptr())
         self._bufs = {}
         self._captured = []  # zeroed scratch of captured calls, whose graphs live no longer than the weights
-        self._side = torch.cuda.Stream(self.device, priority=-1)
+        self._side = None  # the stream that zeroes it
 
     def _repack(self, packed, scale, bias, gate_up):
         import torch
@@ -140,13 +140,15 @@ class MoELayerW4:
         replayed, on another stream: in the graph it would be a node of every replay."""
         import torch
         if torch.cuda.is_current_stream_capturing():
-            with torch.cuda.stream(self._side):
-                if not torch.cuda.is_current_stream_capturing():
-                    with _lib.relaxed_capture():
+            with _lib.relaxed_capture():
+                if self._side is None:
+                    self._side = torch.cuda.Stream(self.device, priority=-1)
+                with torch.cuda.stream(self._side):
+                    if not torch.cuda.is_current_stream_capturing():
                         t = torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
                         self._side.synchronize()
-                    self._captured.append(t)
-                    return t
+                        self._captured.append(t)
+                        return t
         return torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
 
     def _buffers_here(self, T):
