@@ -421,7 +421,7 @@ cudaError_t try_ring(const ResidualArgs& p, cudaStream_t s, bool* ran) {
   // a thread's work: with one chunk more warps share what a token's k + 1 rows or unaligned pieces take (4096
   // tokens of 2048 channels, nine rows: 34.6 us, two chunks 41), with two the sums of plain rows cost less
   // (12.2 us, one chunk 13.1)
-  if (COMBINE || !VEC) {
+  if constexpr (COMBINE || !VEC) {
     if (chunks <= 256) return launch_ring<VEC, X32, COMBINE, 1, 288, false>(p, g, one, s);
     if (chunks <= 512) return launch_ring<VEC, X32, COMBINE, 1, 544, false>(p, g, one, s);
   } else {
