@@ -30,6 +30,7 @@ class DecoderBlockW4:
     `norms`: three ResidualNorm for a block with gains, post-norms, gates and scales of its own: of the block's input,
     around the addition of the attention's output (its n is what router and experts take), and around that of the
     experts' (its n is what the next block's attention takes).  `gates`: their gates' values per channel, or None.
+    Such a block's router is moe_router at every size: E a multiple of 64, at most 512.
     """
 
     def __init__(self, w_qkv, w_o, w_router, moe: MoELayerW4, cache: PagedKVCache, norms=None, gates=(None, None)):

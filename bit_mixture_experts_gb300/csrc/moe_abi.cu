@@ -598,7 +598,7 @@ int moe_layer_forward_gated(const uint16_t* x, const float* logits, const moe_ga
                             const moe_residual_t* residual, int T, int H, int F, int E, int k, int block_n, int impl,
                             const moe_weights_t* w, const moe_buffers_t* b, moe_stream_t stream) {
   if (!w || !b) return MOE_ERR_NULL;
-  // all of it is checked before anything is enqueued
+  // the choice and what follows the experts are checked before anything is enqueued
   int rc = check_shape(T, H, F, E, k, block_n);
   if (rc || (logits && (rc = check_gate(gate, E, k)))) return rc;
   if (!aligned16(logits)) return MOE_ERR_ALIGN;

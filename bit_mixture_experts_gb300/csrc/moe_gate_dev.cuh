@@ -14,8 +14,8 @@
 // expert, or the last group that stays and the first that does not are not
 // further apart than their errors, the token is done again with scores of twice
 // the length, off by less than 2^-40 (256 experts, 8 chosen: about one token in
-// 700).  Experts whose logit and bias are
-// the same bits tie in any precision and need no second look.  Without a bias
+// 700; 1024 experts, softmax: one in 25 with 16 chosen, one in 8 with 32).  Experts
+// whose logit and bias are the same bits tie in any precision and need no second look.  Without a bias
 // the scores are monotone in the logits, which are then compared themselves: m
 // is the upper 23 (21) bits of the logit, and the second look is at all of it.
 //
@@ -26,9 +26,9 @@
 // and is done for all of them at once.
 //
 // What bounds it: 262144 tokens of 256 experts (sigmoid, bias, four of eight
-// groups, eight chosen) take 130 us where the bytes of their logits take 42.  The
-// ALU pipe, which does minima, maxima and compares at half rate, is 67 % busy, the
-// issue slots are 58 %.  A single token takes 3.4 us, a chain of latencies.
+// groups, eight chosen) take 129 us where the bytes of their logits take 42.  The
+// ALU pipe, which does minima, maxima and compares at half rate, is 65 % busy, the
+// issue slots are 58 %.  A single token takes 3.0 us, a chain of latencies.
 #pragma once
 #include <float.h>
 
@@ -84,7 +84,8 @@ struct Lane {
   }
 };
 
-// ---- The second look: scores as pairs of floats (high part, rest), about 45 bits, on the FP32 pipe.  (In
+// ---- The second look: scores as pairs of floats (high part, rest), about 45 bits, on the FP32 pipe, by the known
+// error-free sums (fast two-sum: Dekker; two-sum: Knuth) and the product whose rest an FMA gives.  (In
 // 64-bit floats, of which an SM does one a clock, a token's 256 exponentials took 9000 cycles, all of its
 // second look 29000.)
 struct Pair {
@@ -228,7 +229,8 @@ __device__ __forceinline__ bool group_stays(const float* row, const Lane& me, co
 }
 
 // The choice among the groups that stay with every value worked out anew for each of the k: for tokens of
-// which more experts are close to the last one chosen than a warp has lanes.
+// which more experts are close to the last one chosen than a warp has lanes, or, with 32 chosen, any other.  Slow:
+// 400 tokens of 1024 experts, 32 chosen, take 437 us (softmax; with 31 chosen 29), although it is 3 tokens of them.
 template <Mode MODE>
 __device__ __forceinline__ int choose_slowly(const float* row, const Lane& me, bool stays, const Gate& g, const Scale& s,
                                              int lane) {
@@ -483,7 +485,9 @@ __device__ __forceinline__ void load_tokens(const float* logits, int t, int T, c
 }
 
 // Tokens t .. t + BATCH - 1 (those below T) by one warp: lane i (32 / BATCH) + j ends with the j-th choice of
-// token t + i and its weight.  l: load_tokens'.  WHOLE: every lane has EPL experts, which start on 16 bytes.
+// token t + i and its weight.  l: load_tokens'.  WHOLE: every lane has EPL experts, which start on 16 bytes, or none
+// (the last lanes of 232, 240 and 248 experts, or of two groups of 120).  The keys of those that have none name
+// experts behind the group's, as not available: behind the 120 or more of the group itself, of which at most 32 are chosen.
 template <int EPL, int IDX, Mode MODE, int BATCH, bool WHOLE>
 __device__ __forceinline__ void warp_gate(const float* logits, int t, int T, const float (&l)[BATCH][EPL],
                                           const Units<EPL, IDX, MODE>& u, const Gate& g, const Lane& me, int lane,

@@ -22,7 +22,7 @@
  *    are detected on the host before anything is enqueued.  Faults found by a
  *    kernel (a corrupt block map, an out-of-range index) are recorded in a
  *    device error word instead of trapping; read it with moe_get_device_error.
- *  - Behaviour for NaN or infinite logits is undefined.
+ *  - Behaviour for NaN or infinite logits is undefined, except by a gate.
  *
  * Sizes: T tokens, H hidden, E routed experts (the shared expert is index E of
  * every weight array), k experts per token, F expert FFN width, A = T*k
