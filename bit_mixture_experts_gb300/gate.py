@@ -34,6 +34,15 @@ def _empty(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+def _in_a_graphs_pool(t):
+    """Whether t, made during a capture, is memory that PyTorch keeps for the graph: so in its own captures alone."""
+    at = t.data_ptr()
+    for s in torch.cuda.memory_snapshot():
+        if s["address"] <= at < s["address"] + s["total_size"]:
+            return tuple(s.get("segment_pool_id", (0, 0))) != (0, 0)
+    return False
+
+
 class Fixed:
     """An object whose description the library has been given: its public attributes keep their values.  (The memory
     of a tensor put in another's place would not be what the calls read.)"""
@@ -75,6 +84,7 @@ class ExpertGate(Fixed):
         self.top_groups = groups if top_groups is None else top_groups
         self.group_score, self.renorm, self.scale = group_score, renorm, scale
         self._workspaces, self._plans = {}, {}
+        self._captured = []  # scratch of captures that PyTorch did not begin, and keeps none for
         self.struct = _lib.Gate(_lib._ptr(bias), _lib.SCORES[score], groups, self.top_groups,
                                 _lib.GROUP_SCORES[group_score], int(renorm), scale)
 
@@ -137,7 +147,10 @@ class ExpertGate(Fixed):
 
     def _workspace_here(self, need, dev):
         if torch.cuda.is_current_stream_capturing():
-            return torch.zeros(need, dtype=torch.uint8, device=dev)
+            own = torch.zeros(need, dtype=torch.uint8, device=dev)
+            if not _in_a_graphs_pool(own):
+                self._captured.append(own)
+            return own
         key = (dev, _lib._stream())
         have = self._workspaces.get(key)
         if have is None or have.numel() < need:

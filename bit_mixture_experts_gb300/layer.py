@@ -8,7 +8,7 @@ from __future__ import annotations
 import numpy as np
 
 from . import _lib
-from .gate import _empty, _on
+from .gate import _empty, _in_a_graphs_pool, _on
 
 DEFAULT_BLOCK_N = {_lib.IMPL_TC: 128, _lib.IMPL_GEMV: 8, _lib.IMPL_TC2: 128, _lib.IMPL_TC_BF16: 128}
 DECODE_MAX_T = 16  # token counts up to this take the GEMV kernel under impl="auto"
@@ -50,8 +50,8 @@ class MoELayerW4:
 
     Calls on several streams share no buffers, nor do captured calls those of
     others: a call that torch.cuda.graph captures takes its own from the graph's
-    memory.  (A capture made in another way has no such memory: what PyTorch
-    hands out there, it hands out again.)
+    memory; one captured in another way, for which PyTorch keeps no memory, has
+    some that the layer keeps for good.
     """
 
     def __init__(self, H, E, k, F, weights: dict, device="cuda", impl="auto", block_n=None, fuse_combine=False,
@@ -90,7 +90,7 @@ class MoELayerW4:
         else:
             self.weights = _lib.Weights(self.w13_r.data_ptr(), self.w2_r.data_ptr())
         self._bufs = {}
-        self._captured = []  # zeroed scratch of captured calls, whose graphs live no longer than the weights
+        self._captured = []  # what captured calls take of the layer's, as their graphs take the weights: for good
         self._side = None  # the stream that zeroes it
 
     def _repack(self, packed, scale, bias, gate_up):
@@ -187,6 +187,8 @@ class MoELayerW4:
                                    t["combine_ws"].data_ptr() if cws else None, cws)
         if key is not None:
             self._bufs[key] = t
+        elif not _in_a_graphs_pool(t["y"]):
+            self._captured.append(t)
         return t
 
     def forward(self, x, logits, out=None, stream=None):
@@ -267,7 +269,7 @@ class MoEDecodeChain:
         self.layers = [MoELayerW4(H, E, k, F, w, device=self.device, impl=impl, block_n=block_n)
                        for w in layer_weights]
         self.wr = [_dev(np.asarray(b, dtype=np.uint16), self.device) for b in router_bits]
-        self._bufs = {}
+        self._bufs, self._captured = {}, []
 
     def buffers(self, T, stream=None):
         """Per-layer outputs (bf16 [T, H]), logits (fp32 [T, E]) and the router's top-k scratch of the calls for T tokens on
@@ -292,6 +294,8 @@ class MoEDecodeChain:
             }
             if key is not None:
                 self._bufs[key] = b
+            elif not _in_a_graphs_pool(b["out"][0]):
+                self._captured.append(b)
         return b
 
     def forward(self, x, stream=None):

@@ -22,12 +22,13 @@ class Device:
 
     def __init__(self, monkeypatch):
         from bit_mixture_experts_gb300 import layer
-        self.current, self.capturing, self.made = 0, set(), []
+        self.current, self.capturing, self.made, self.pool = 0, set(), [], True
         monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: self.current in self.capturing)
         monkeypatch.setattr(torch.cuda, "stream", self.on)
         monkeypatch.setattr(layer, "_on", lambda stream, device: self.on(stream), raising=False)
         monkeypatch.setattr(layer._lib, "_stream", lambda stream=None: self.current if stream is None else stream)
         monkeypatch.setattr(layer._lib, "relaxed_capture", contextlib.nullcontext, raising=False)
+        monkeypatch.setattr(layer, "_in_a_graphs_pool", lambda t: self.pool, raising=False)
         for name in ("empty", "zeros"):
             make = getattr(torch, name)
             monkeypatch.setattr(torch, name, lambda *a, name=name, make=make, **kw: self.note(name, make(*a, **kw)))
@@ -99,6 +100,11 @@ def test_captured_calls_share_no_buffers(layer, monkeypatch, T):
     dev.capturing.add(side)
     layer.buffers(T, side)
     assert len(layer._captured) == 4
+    # a capture that PyTorch keeps no memory for: the layer does
+    dev.pool = False
+    dev.capturing.add(7)
+    b = layer.buffers(T, 7)
+    assert any(x is b for x in layer._captured)
 
 
 def test_a_chains_streams_and_captures_share_no_buffers(monkeypatch):

@@ -172,3 +172,77 @@ def test_a_chain_on_two_streams_and_in_graphs():
     for w, o in zip(want, outs):
         assert all(torch.equal(x, w) for x in o)
     assert all(torch.equal(x, w) for x, w in zip(kept, want[2:]))
+
+
+@pytest.mark.parametrize("T,fuse", FORMS)
+def test_a_capture_that_pytorch_did_not_begin(weights, T, fuse):
+    """Nothing that is allocated later takes the memory that its replays write to."""
+    import ctypes
+
+    import torch
+    rt = ctypes.CDLL("libcudart.so.13")
+    layer, calls = make(weights, fuse), inputs(T, 2)
+    fresh = make(weights, fuse)
+    want = [fresh.forward(*c) for c in calls]
+    no_error()
+    x, logits = (t.clone() for t in calls[0])
+    out = torch.empty_like(x)
+    st = torch.cuda.Stream()
+    handle, graph, run = ctypes.c_void_p(st.cuda_stream), ctypes.c_void_p(), ctypes.c_void_p()
+    torch.cuda.synchronize()
+    assert rt.cudaStreamBeginCapture(handle, 0) == 0
+    with torch.cuda.stream(st):
+        layer.forward(x, logits, out)
+    assert rt.cudaStreamEndCapture(handle, ctypes.byref(graph)) == 0
+    assert rt.cudaGraphInstantiate(ctypes.byref(run), graph, ctypes.c_ulonglong(0)) == 0
+    with torch.cuda.stream(st):  # what would be handed out again
+        others = [torch.full((n,), 7, dtype=torch.uint8, device="cuda")
+                  for n in [16, 512, 1024, 4096, 1 << 16, 1 << 18, 1 << 20, T * K * F * 2, T * K * H * 2] * 20]
+    for c, w in zip(calls, want):
+        x.copy_(c[0])
+        logits.copy_(c[1])
+        torch.cuda.synchronize()
+        assert rt.cudaGraphLaunch(run, handle) == 0
+        no_error()
+        assert torch.equal(out, w)
+    assert all((t == 7).all() for t in others)
+    assert rt.cudaGraphExecDestroy(run) == 0 and rt.cudaGraphDestroy(graph) == 0
+
+
+def test_graphs_of_pytorch_keep_no_buffers(weights):
+    """The layer keeps counters alone of a call that torch.cuda.graph captures."""
+    import torch
+    layer, ((x, logits),) = make(weights), inputs(600, 1)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        layer.forward(x, logits)
+    assert len(layer._captured) == 1 and torch.is_tensor(layer._captured[0])
+
+
+def test_a_gates_scratch_in_such_a_capture():
+    import ctypes
+
+    import torch
+
+    from bit_mixture_experts_gb300 import ExpertGate
+    rt = ctypes.CDLL("libcudart.so.13")
+    gate = ExpertGate(K)
+    logits = torch.randn((900, E), device="cuda")
+    want = gate.route(logits, 64)
+    no_error()
+    st = torch.cuda.Stream()
+    handle, graph, run = ctypes.c_void_p(st.cuda_stream), ctypes.c_void_p(), ctypes.c_void_p()
+    torch.cuda.synchronize()
+    assert rt.cudaStreamBeginCapture(handle, 0) == 0
+    got = gate.route(logits, 64, stream=st)
+    assert rt.cudaStreamEndCapture(handle, ctypes.byref(graph)) == 0
+    assert rt.cudaGraphInstantiate(ctypes.byref(run), graph, ctypes.c_ulonglong(0)) == 0
+    with torch.cuda.stream(st):
+        others = [torch.full((n,), 7, dtype=torch.uint8, device="cuda") for n in [512, 4096, 1 << 14, 1 << 16] * 50]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        assert rt.cudaGraphLaunch(run, handle) == 0
+    no_error()
+    assert all(torch.equal(a, b) for a, b in zip(got[:6], want[:6]))
+    assert all((t == 7).all() for t in others)
+    assert rt.cudaGraphExecDestroy(run) == 0 and rt.cudaGraphDestroy(graph) == 0
